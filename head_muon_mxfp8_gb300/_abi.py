@@ -43,6 +43,7 @@ HM_STAGE_FUSED = 32
 HM_STAGE_ALL_FUSED = 63
 HM_STAGE_SCRATCH = 64
 HM_STAGE_STEP = 127
+HM_RMSNORM_MAX_D = 16384
 HM_RS_FP32, HM_RS_BF16, HM_RS_BF16_SR = 0, 1, 2
 
 
@@ -87,6 +88,10 @@ class hm_scale_relayout(C.Structure):
                 ("block_rows", C.c_int32), ("pad", C.c_int32)]
 
 
+class hm_grad_tensor(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32), ("pad", C.c_int32)]
+
+
 class HmError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn} returned {status} ({status_str(status)})")
@@ -125,6 +130,18 @@ _SIGS = {
     "mxfp8_scale_relayout": (C.c_int, [_P, _P, C.POINTER(hm_scale_relayout), C.c_int, _P]),
     "reduce_scatter_grad": (C.c_int, [_P, _P, C.c_int, C.c_int, _P, C.c_int, C.c_int, C.c_uint64, C.c_uint64,
                                       _P]),
+    "mxfp8_tiled_scale_bytes": (C.c_int, [C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
+    "mxfp8_gemm": (C.c_int, [_P, C.c_int64, _P, _P, C.c_int64, _P, C.c_int64, C.c_int64, C.c_int64, _P, C.c_int64,
+                             C.c_int, C.c_int, _P]),
+    "mxfp8_quantize": (C.c_int, [_P, C.c_int, C.c_int64, C.c_int64, C.c_int64, _P, _P, C.c_int, _P, C.c_int64, _P, _P,
+                                 C.c_int64, _P, _P]),
+    "rmsnorm_mxfp8": (C.c_int, [_P, C.c_int64, _P, _P, C.c_int64, C.c_int, C.c_int64, C.c_int64, _P, C.c_float,
+                                C.c_int, _P, _P, _P, _P]),
+    "rmsnorm_backward_workspace": (C.c_int, [C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
+    "rmsnorm_backward": (C.c_int, [_P, C.c_int64, _P, _P, _P, C.c_int64, C.c_int, C.c_int64, C.c_int64, _P, _P, _P,
+                                   C.c_int, _P, C.c_size_t, _P]),
+    "grad_norm_clip_workspace": (C.c_int, [_P, C.c_int, C.POINTER(C.c_size_t)]),
+    "grad_norm_clip": (C.c_int, [_P, C.c_int, C.c_float, C.c_float, _P, _P, C.c_size_t, _P]),
     "newton_schulz_noalloc": (C.c_int, [_P, C.c_int32, C.c_int32, _P, C.POINTER(hm_muon_hparams), _P]),
 }
 
@@ -314,3 +331,63 @@ def newton_schulz_noalloc(u: int, rows: int, cols: int, v: int, hp: hm_muon_hpar
     """One unit's Newton-Schulz on the library's built-in scratch: for callers
     that cannot allocate device memory (see include/hm.h)."""
     check("newton_schulz_noalloc", lib().newton_schulz_noalloc(_P(u), rows, cols, _P(v), C.byref(hp), _P(stream)))
+
+
+def mxfp8_tiled_scale_bytes(rows: int, k: int) -> int:
+    """Bytes of the 128 x 4 tiled scales of a [rows][k] operand."""
+    n = C.c_size_t(0)
+    check("mxfp8_tiled_scale_bytes", lib().mxfp8_tiled_scale_bytes(rows, k, C.byref(n)))
+    return n.value
+
+
+def mxfp8_gemm(a: int, lda: int, a_scales: int, b: int, ldb: int, b_scales: int, m: int, n: int, k: int, d: int,
+               ldd: int, d_dtype: int, accumulate: bool = False, stream: int = 0) -> None:
+    """D[m][n] (+)= A[m][k] B[n][k]^T of MXFP8 operands (see include/hm.h)."""
+    check("mxfp8_gemm", lib().mxfp8_gemm(a, lda, a_scales, b, ldb, b_scales, m, n, k, d, ldd, d_dtype, accumulate,
+                                         stream))
+
+
+def mxfp8_quantize(x: int, x_dtype: int, rows: int, cols: int, ldx: int, row_mul: int, col_mul: int, block: int,
+                   q: int, ldq: int, s: int, qt: int, ldqt: int, st: int, stream: int = 0) -> None:
+    """MXFP8 codes and tiled scales of x along its columns (q, s) and / or rows (qt, st); 0 leaves a pair out."""
+    check("mxfp8_quantize", lib().mxfp8_quantize(x, x_dtype, rows, cols, ldx, row_mul, col_mul, block, q, ldq, s, qt,
+                                                 ldqt, st, stream))
+
+
+def rmsnorm_mxfp8(x: int, ldx: int, res: int, h: int, ldh: int, dtype: int, rows: int, d: int, gamma: int, eps: float,
+                  block: int, rstd: int, q: int, s: int, stream: int = 0) -> None:
+    """h = x + res, its RMS norm times gamma as MXFP8 codes and tiled scales."""
+    check("rmsnorm_mxfp8", lib().rmsnorm_mxfp8(x, ldx, res, h, ldh, dtype, rows, d, gamma, eps, block, rstd, q, s,
+                                               stream))
+
+
+def rmsnorm_backward_workspace(rows: int, d: int) -> int:
+    n = C.c_size_t(0)
+    check("rmsnorm_backward_workspace", lib().rmsnorm_backward_workspace(rows, d, C.byref(n)))
+    return n.value
+
+
+def rmsnorm_backward(dy: int, lddy: int, dres: int, h: int, dx: int, ldh: int, dtype: int, rows: int, d: int,
+                     gamma: int, rstd: int, dgamma: int, accumulate: bool, workspace: int, workspace_bytes: int,
+                     stream: int = 0) -> None:
+    check("rmsnorm_backward", lib().rmsnorm_backward(dy, lddy, dres, h, dx, ldh, dtype, rows, d, gamma, rstd, dgamma,
+                                                     accumulate, workspace, workspace_bytes, stream))
+
+
+def grad_list(tensors):
+    """(src, dst, elements, dtype) of every tensor as the array grad_norm_clip
+    takes; build it once for gradients that stay in place."""
+    return (hm_grad_tensor * len(tensors))(*[hm_grad_tensor(s, d, n, t, 0) for (s, d, n, t) in tensors])
+
+
+def grad_norm_clip_workspace(tensors) -> int:
+    n = C.c_size_t(0)
+    check("grad_norm_clip_workspace", lib().grad_norm_clip_workspace(tensors, len(tensors), C.byref(n)))
+    return n.value
+
+
+def grad_norm_clip(tensors, max_norm: float, eps: float, stats: int, workspace: int, workspace_bytes: int,
+                   stream: int = 0) -> None:
+    """Global norm of a grad_list and dst = src * min(1, max_norm / (norm + eps)); stats: norm, coefficient."""
+    check("grad_norm_clip", lib().grad_norm_clip(tensors, len(tensors), max_norm, eps, stats, workspace,
+                                                 workspace_bytes, stream))

@@ -48,7 +48,7 @@ extern "C" const char* hm_status_str(hm_status s) {
     }
 }
 
-namespace {
+namespace hm {
 
 // Unsupported hardware is rejected before any launch (Table 4).
 hm_status check_arch() {
@@ -67,6 +67,12 @@ hm_status check_arch() {
     cache[dev] = st;
     return st;
 }
+
+}  // namespace hm
+
+using hm::check_arch;
+
+namespace {
 
 inline hm_status cuda_status(cudaError_t e) { return e == cudaSuccess ? HM_OK : HM_ERR_CUDA; }
 
@@ -620,12 +626,7 @@ extern "C" hm_status muon_plan_unit(const hm_muon_plan* p, int unit, int32_t* ex
     return HM_OK;
 }
 
-namespace {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
+namespace hm {
 
 EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
@@ -640,6 +641,13 @@ EncodeTiledFn encode_fn() {
     });
     return fn;
 }
+
+}  // namespace hm
+
+using hm::encode_fn;
+using hm::EncodeTiledFn;
+
+namespace {
 
 // 3-D bf16 tensor [units][rows][inner] (inner contiguous), tile box
 // [1][box_rows][64] with the 128-byte swizzle the UMMA K-major layout expects.

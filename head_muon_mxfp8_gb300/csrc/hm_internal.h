@@ -196,6 +196,16 @@ inline int resident_grid(Kernel kernel, int threads, int64_t items) {
 }
 int32_t* device_error_word();
 
+// HM_OK on a current sm_103 device, else HM_ERR_ARCH / HM_ERR_CUDA (cached per device).
+int check_arch();
+
+// The driver's tensor-map encoder, looked up once; nullptr without a driver.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                   CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 // stage_only: ranges flagged for the staging write u there only (not in the u root)
 cudaError_t launch_f0(const RangeArgs& ra, float* m, const float* g, uint16_t* u, uint16_t* u_stage,
                       float mu, int nesterov, int stage_only, cudaStream_t st);

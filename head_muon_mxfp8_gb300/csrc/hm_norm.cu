@@ -1,0 +1,308 @@
+// RMS norm with the residual's addition and an MXFP8 output, and its gradient.
+//
+//   h = round(x + res);  rstd = 1 / sqrt(mean(h^2) + eps);  y = h rstd gamma
+//   (q, s) = MXFP8(y)
+//   dx = dres + rstd (t - xhat mean(t xhat)),  t = dy gamma, xhat = h rstd
+//   dgamma = sum over rows of dy xhat
+// Every statistic is fp32 and of the stored h, so the gradient, which has only
+// the stored h, differentiates exactly the function the forward pass computed.
+// Memory-bound; a row stays in registers between its reduction and its output,
+// so every tensor is read and written once.
+#include "hm_internal.h"
+#include "hm_mx_device.cuh"
+#include "hm_ops.h"
+
+#include <cuda_bf16.h>
+
+namespace hm {
+
+namespace {
+
+constexpr int kMaxRowThreads = 512;
+
+// 8 elements of a row
+template <bool F32>
+struct Vec8;
+template <>
+struct Vec8<true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* base, int64_t at) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+        a = __ldcs(p);
+        b = __ldcs(p + 1);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    // stores v and leaves in v what was stored
+    static __device__ __forceinline__ void put(void* base, int64_t at, float (&v)[8]) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    static __device__ __forceinline__ void round(float (&)[8]) {}
+};
+template <>
+struct Vec8<false> {
+    uint4 a;
+    __device__ __forceinline__ void load(const void* base, int64_t at) {
+        a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[2 * k] = __uint_as_float(w[k] << 16);
+            v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ void put(void* base, int64_t at, float (&v)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ void round(float (&v)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __bfloat162float(__float2bfloat16_rn(v[k]));
+    }
+};
+
+__device__ __forceinline__ void load_f8(const float* p, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// Sum over the block, the same in every thread: warp sums, then every thread
+// adds the warps' in order.  `red` alternates between two rows of 16, so one
+// barrier per sum is enough.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = 0.f;
+    const int warps = blockDim.x >> 5;
+    for (int k = 0; k < warps; ++k) t += red[k];
+    return t;
+}
+
+// One row per CTA; a thread owns V vectors of 8 columns, vector i * blockDim + t.
+template <bool F32, int V>
+__global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_kernel(const __grid_constant__ RmsArgs p) {
+    __shared__ float red[16];
+    const int64_t row = blockIdx.x;
+    const int nv = p.d >> 3;
+    const int lane = threadIdx.x & 31;
+    const int64_t col_tiles = (p.d + 127) >> 7;
+    uint8_t* srow = p.s + (row >> 7) * col_tiles * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4;
+    if (row >= p.rows) {  // padding of the last scale tiles
+        for (int64_t j = threadIdx.x; j < col_tiles; j += blockDim.x) *reinterpret_cast<uint32_t*>(srow + j * 512) = 0u;
+        return;
+    }
+    float h[V][8];
+    float sq = 0.f;
+    Vec8<F32> x[V], r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int j = i * blockDim.x + threadIdx.x;
+        if (j < nv) {
+            x[i].load(p.x, row * p.ldx + j * 8);
+            if (p.res) r[i].load(p.res, row * p.ldh + j * 8);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int j = i * blockDim.x + threadIdx.x;
+        if (j < nv) {
+            x[i].get(h[i]);
+            if (p.res) {
+                float rv[8];
+                r[i].get(rv);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) h[i][k] += rv[k];
+            }
+            if (p.h) Vec8<F32>::put(p.h, row * p.ldh + j * 8, h[i]);
+            Vec8<F32>::round(h[i]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sq = fmaf(h[i][k], h[i][k], sq);
+        }
+    }
+    const float rstd = 1.0f / sqrtf(block_sum(sq, red) / static_cast<float>(p.d) + p.eps);
+    if (threadIdx.x == 0) p.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int j = i * blockDim.x + threadIdx.x;
+        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (j < nv) {
+            float gm[8];
+            load_f8(p.gamma + j * 8, gm);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = h[i][k] * rstd * gm[k];
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(y[k]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        if (p.block == 128) {
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+        }
+        const int e = mx_scale_exponent(amax);
+        const float sc = mx_inv_scale(e);
+        if (j < nv) {
+            const uint32_t lo = cvt_e4m3x2(y[0] * sc, y[1] * sc) | (static_cast<uint32_t>(cvt_e4m3x2(y[2] * sc, y[3] * sc)) << 16);
+            const uint32_t hi = cvt_e4m3x2(y[4] * sc, y[5] * sc) | (static_cast<uint32_t>(cvt_e4m3x2(y[6] * sc, y[7] * sc)) << 16);
+            __stcs(reinterpret_cast<uint2*>(p.q + row * p.d + j * 8), make_uint2(lo, hi));
+        }
+        // the four scales of 128 columns as one word: bytes from lanes 0, 4, 8, 12 of each half warp
+        const uint32_t byte = j < nv ? static_cast<uint32_t>(e + 127) : 0u;
+        uint32_t word = byte << (8 * ((lane >> 2) & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, 4);
+        word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        if ((lane & 15) == 0 && j < nv) *reinterpret_cast<uint32_t*>(srow + (j >> 4) * 512) = word;
+    }
+}
+
+// CTAs take rows round-robin; a thread owns the same columns of every row and
+// keeps their part of dgamma in registers.
+template <bool F32, int V>
+__global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_grad_kernel(const __grid_constant__ RmsGradArgs p) {
+    __shared__ float red[2][16];
+    const int nv = p.d >> 3;
+    float dg[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dg[i][k] = 0.f;
+    const float inv_d = 1.0f / static_cast<float>(p.d);
+    int flip = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+        Vec8<F32> dy[V], h[V], dr[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int j = i * blockDim.x + threadIdx.x;
+            if (j < nv) {
+                dy[i].load(p.dy, row * p.lddy + j * 8);
+                h[i].load(p.h, row * p.ldh + j * 8);
+                if (p.dres) dr[i].load(p.dres, row * p.ldh + j * 8);
+            }
+        }
+        const float rstd = p.rstd[row];
+        float t[V][8], xh[V][8];
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int j = i * blockDim.x + threadIdx.x;
+            if (j < nv) {
+                float gm[8], y[8];
+                load_f8(p.gamma + j * 8, gm);
+                dy[i].get(y);
+                h[i].get(xh[i]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    xh[i][k] *= rstd;
+                    dg[i][k] = fmaf(y[k], xh[i][k], dg[i][k]);
+                    t[i][k] = y[k] * gm[k];
+                    dot = fmaf(t[i][k], xh[i][k], dot);
+                }
+            }
+        }
+        const float mean = block_sum(dot, red[flip]) * inv_d;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int j = i * blockDim.x + threadIdx.x;
+            if (j < nv) {
+                float o[8], rv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (p.dres) dr[i].get(rv);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = fmaf(rstd, t[i][k] - xh[i][k] * mean, rv[k]);
+                Vec8<F32>::put(p.dx, row * p.ldh + j * 8, o);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int j = i * blockDim.x + threadIdx.x;
+        if (j < nv) {
+            float4* out = reinterpret_cast<float4*>(p.partials + static_cast<int64_t>(blockIdx.x) * p.d + j * 8);
+            out[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+            out[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+        }
+    }
+}
+
+// dgamma from the CTAs' partials: 32 columns per CTA, 16 threads per column each
+// adding every 16th partial in order, then the 16 in order.
+__global__ void __launch_bounds__(512) dgamma_kernel(const float* __restrict__ partials, int parts, int d,
+                                                     int accumulate, float* __restrict__ dgamma) {
+    __shared__ float red[16][33];
+    const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + c;
+    float s = 0.f;
+    for (int k = g; k < parts; k += 16) s += partials[static_cast<int64_t>(k) * d + col];
+    red[g][c] = s;
+    __syncthreads();
+    if (g == 0) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) t += red[k][c];
+        dgamma[col] = accumulate ? dgamma[col] + t : t;
+    }
+}
+
+int row_vectors(int64_t d) { return d <= 4096 ? 1 : d <= 8192 ? 2 : 4; }
+int row_threads(int64_t d, int v) { return static_cast<int>(((d / 8 + v - 1) / v + 31) / 32 * 32); }
+
+template <bool F32>
+cudaError_t launch_fwd(const RmsArgs& a, cudaStream_t st) {
+    const int v = row_vectors(a.d), threads = row_threads(a.d, v);
+    const unsigned grid = static_cast<unsigned>((a.rows + 127) / 128 * 128);
+    note_launch();
+    if (v == 1) rmsnorm_kernel<F32, 1><<<grid, threads, 0, st>>>(a);
+    else if (v == 2) rmsnorm_kernel<F32, 2><<<grid, threads, 0, st>>>(a);
+    else rmsnorm_kernel<F32, 4><<<grid, threads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool F32>
+cudaError_t launch_bwd(const RmsGradArgs& a, cudaStream_t st) {
+    const int parts = rmsnorm_grad_parts(a.rows, a.d);
+    if (parts) {
+        const int v = row_vectors(a.d), threads = row_threads(a.d, v);
+        note_launch();
+        if (v == 1) rmsnorm_grad_kernel<F32, 1><<<parts, threads, 0, st>>>(a);
+        else if (v == 2) rmsnorm_grad_kernel<F32, 2><<<parts, threads, 0, st>>>(a);
+        else rmsnorm_grad_kernel<F32, 4><<<parts, threads, 0, st>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    note_launch();
+    dgamma_kernel<<<a.d / 32, 512, 0, st>>>(a.partials, parts, a.d, a.accumulate, a.dgamma);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int rmsnorm_grad_parts(int64_t rows, int64_t d) {
+    (void)d;
+    const int64_t most = 2 * static_cast<int64_t>(device_sm_count());
+    return static_cast<int>(rows < most ? rows : most);
+}
+
+cudaError_t launch_rmsnorm(const RmsArgs& a, int f32, cudaStream_t st) {
+    return f32 ? launch_fwd<true>(a, st) : launch_fwd<false>(a, st);
+}
+
+cudaError_t launch_rmsnorm_grad(const RmsGradArgs& a, int f32, cudaStream_t st) {
+    return f32 ? launch_bwd<true>(a, st) : launch_bwd<false>(a, st);
+}
+
+}  // namespace hm

@@ -1,0 +1,101 @@
+// Internal declarations of the operators around the update (MXFP8 product,
+// quantization, RMS norm, gradient clipping): kernel arguments and launchers.
+// Not part of the C ABI.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace hm {
+
+struct MxGemmArgs {
+    const uint8_t* sa;   // tiled scales
+    const uint8_t* sb;
+    void* d;
+    int64_t ldd;         // elements
+    int32_t m, n, k;
+    int32_t d_f32, accumulate;
+    // filled in by launch_mx_gemm
+    int32_t num_kb;      // stages of 128 along K
+    int32_t last_nk;     // blocks of 32 in the last stage
+    int32_t sf_rows_b;   // 128-row tiles of B's scales
+    int32_t tiles_m, tiles_n;
+    int32_t split;       // CTAs of a cluster that share K
+    int32_t vec;         // bytes every row of D is aligned to: 16 or 0
+    int32_t* err;
+};
+cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, const MxGemmArgs& args,
+                           cudaStream_t st);
+
+struct QuantArgs {
+    const void* x;
+    int64_t rows, cols, ldx;
+    const float* row_mul;
+    const float* col_mul;
+    uint8_t* q;          // [rows][ldq] or nullptr
+    int64_t ldq;
+    uint8_t* s;
+    uint8_t* qt;         // [cols][ldqt] or nullptr
+    int64_t ldqt;
+    uint8_t* st;
+    int32_t block;       // 32 or 128
+    int32_t vec;         // x's rows are 16-byte aligned
+};
+cudaError_t launch_quantize(const QuantArgs& a, int f32, cudaStream_t st);
+
+struct RmsArgs {
+    const void* x;       // [rows][ldx]
+    const void* res;     // [rows][ldh] or nullptr
+    void* h;             // [rows][ldh] or nullptr
+    int64_t ldx, ldh, rows;
+    int32_t d, block;
+    const float* gamma;
+    float eps;
+    float* rstd;
+    uint8_t* q;          // [rows][d]
+    uint8_t* s;
+};
+cudaError_t launch_rmsnorm(const RmsArgs& a, int f32, cudaStream_t st);
+
+struct RmsGradArgs {
+    const void* dy;      // [rows][lddy]
+    const void* dres;    // [rows][ldh] or nullptr
+    const void* h;
+    void* dx;
+    int64_t lddy, ldh, rows;
+    int32_t d, accumulate;
+    const float* gamma;
+    const float* rstd;
+    float* dgamma;
+    float* partials;     // [CTAs][d]
+};
+// CTAs (= partial rows of dgamma) that launch_rmsnorm_grad uses, at most
+int rmsnorm_grad_parts(int64_t rows, int64_t d);
+cudaError_t launch_rmsnorm_grad(const RmsGradArgs& a, int f32, cudaStream_t st);
+
+// One launch handles up to kClipTensors tensors, passed by value.
+constexpr int kClipTensors = 256;
+struct ClipTensor {
+    const void* src;
+    void* dst;           // nullptr: only counted
+    int64_t n;
+    int32_t first;       // chunks before this tensor
+    int32_t f32;
+};
+struct ClipArgs {
+    int32_t n;           // tensors
+    int32_t chunks;
+    int32_t parts;       // partial sums of every launch of the call together
+    int32_t part0;       // this launch's first one
+    float max_norm, eps;
+    float* stats;
+    double* partials;
+    ClipTensor t[kClipTensors];
+};
+int clip_chunks(const void* src, int64_t n, int f32);  // of one tensor with n > 0
+int clip_parts(int chunks);            // partial sums of one launch
+cudaError_t launch_clip_norm(const ClipArgs& a, cudaStream_t st);
+cudaError_t launch_clip_scale(const ClipArgs& a, cudaStream_t st);
+
+}  // namespace hm

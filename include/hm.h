@@ -395,6 +395,124 @@ hm_status mxfp8_scale_relayout(const uint8_t* src, uint8_t* dst, const hm_scale_
 hm_status reduce_scatter_grad(const hm_chain* chain, const float* parts, int n_parts, int ranks_per_node,
                               float* g, int mode, int accumulate, uint64_t seed, uint64_t offset, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Operators around the update.  The paper's runtime side multiplies by the
+ * requantized weights (section 3.1 EG1: the scales are relaid out for the MXFP8
+ * GEMM) and hands the update a main gradient; the calls below are that product,
+ * what feeds it, its gradients and the clipping of the gradient.
+ *
+ * An MXFP8 operand is a matrix of E4M3 codes [rows][ld] (K contiguous, one byte
+ * each) and its UE8M0 scales in the 128 x 4 tiled layout of
+ * mxfp8_scale_relayout: one scale per 1 x 32 block of codes.  `block` = 128
+ * takes one scale per 1 x 128 block and stores it for each of the four 1 x 32
+ * blocks, so every reader of the layout takes both.  Scale rule and rounding
+ * are G's.  A NaN quantizes to the NaN code, an infinity to +-448.
+ *
+ * Bytes of the tiled scales of a [rows][k] operand (k a multiple of 32, else
+ * HM_ERR_ALIGN): 512 * ceil(rows / 128) * ceil(k / 128). */
+hm_status mxfp8_tiled_scale_bytes(int64_t rows, int64_t k, size_t* bytes);
+
+/* Matrix product of MXFP8 operands, D[m][n] = sum_k A[m][k] B[n][k] with the
+ * scales applied (fp32 accumulation in TMEM, one rounding to D's dtype), or
+ * D += that sum when accumulate != 0 (HM_F32 only, else HM_ERR_DTYPE; the
+ * earlier D is added last).
+ * A linear layer's three products are this call: forward A = X, B = W;
+ * gradient of X: A = dY, B = W^T (quantized along W's rows); gradient of W:
+ * A = dY^T, B = X^T (both quantized along the tokens), accumulated into the
+ * main gradient.
+ *   a [m][lda], b [n][ldb]: codes; lda, ldb >= k, multiples of 16; both and
+ *       both scale pointers 16-byte aligned (HM_ERR_ALIGN)
+ *   k: a multiple of 32 (HM_ERR_ALIGN); k = 0 gives D = 0 (D unchanged when
+ *       accumulating)
+ *   d [m][ldd]: HM_BF16 or HM_F32 (HM_ERR_DTYPE), aligned to its element,
+ *       any ldd >= n; columns n .. ldd - 1 are left alone
+ * m = 0 or n = 0 is a no-op.  m, n, k, lda, ldb at most 2^31 - 1 - 256
+ * (HM_ERR_GEOMETRY).  D must not overlap an operand (HM_ERR_OVERLAP).  Scale
+ * bytes of rows and blocks outside the operand are never used.  No workspace;
+ * the same call gives the same bits every time. */
+hm_status mxfp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_scales, const uint8_t* b, int64_t ldb,
+                     const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, void* d, int64_t ldd,
+                     hm_dtype d_dtype, int accumulate, void* stream);
+
+/* Quantizes x [rows][ldx] (HM_BF16 or HM_F32) to MXFP8 along its columns
+ * and / or along its rows, reading x once:
+ *   y[r][c] = x[r][c] * row_mul[r] * col_mul[c]   (fp32, in this order; a NULL
+ *       factor is left out) -- with a norm's rstd and gamma, y is the normed
+ *       activation without having been stored
+ *   q  [rows][ldq]:  codes of y, blocks along the columns; s: its tiled scales
+ *   qt [cols][ldqt]: codes of y^T, blocks along the rows; st: its tiled scales
+ * Either pair may be NULL (not both: HM_ERR_ARG).  block is 32 or 128
+ * (HM_ERR_ARG).  Rows and columns need not be multiples of 32: q is written up
+ * to column round_up(cols, 32) and qt up to round_up(rows, 32) with zero codes,
+ * so k = those lengths in the product; ldq and ldqt are at least that and
+ * multiples of 16, q, s, qt, st 16-byte aligned (HM_ERR_ALIGN).  x and the
+ * factors need their element's alignment only.  The scales' padding is
+ * written as zero.  rows = 0 or cols = 0 is a no-op.  An output that overlaps
+ * x or another output is HM_ERR_OVERLAP.  cols at most 2^30 and rows at most
+ * 2^22 (HM_ERR_GEOMETRY). */
+hm_status mxfp8_quantize(const void* x, hm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                         const float* row_mul, const float* col_mul, int block, uint8_t* q, int64_t ldq, uint8_t* s,
+                         uint8_t* qt, int64_t ldqt, uint8_t* st, void* stream);
+
+/* RMS norm with the residual's addition and an MXFP8 output, per row of d:
+ *   h    = round(x + res)             (stored in `dtype`; res NULL: h = x)
+ *   rstd = 1 / sqrt(mean(h^2) + eps)  (fp32, of the stored h)
+ *   y    = h * rstd * gamma           (fp32, in this order)
+ *   q [rows][d], s = MXFP8(y) along d (scales tiled)
+ * x [rows][ldx], res and h [rows][ldh] in `dtype` (HM_BF16 or HM_F32); h may be
+ * res or x themselves (x only with ldx == ldh), and may be NULL when res is
+ * NULL.  gamma fp32 [d]; rstd fp32 [rows].  d a multiple of 32, ldx and ldh
+ * multiples of 8, x, res, h, gamma, q, s 16-byte aligned (HM_ERR_ALIGN);
+ * d <= HM_RMSNORM_MAX_D (HM_ERR_GEOMETRY).  block as above.  rows = 0 or d = 0
+ * is a no-op. */
+#define HM_RMSNORM_MAX_D 16384
+hm_status rmsnorm_mxfp8(const void* x, int64_t ldx, const void* res, void* h, int64_t ldh, hm_dtype dtype,
+                        int64_t rows, int64_t d, const float* gamma, float eps, int block, float* rstd, uint8_t* q,
+                        uint8_t* s, void* stream);
+
+/* Gradient of the norm (the quantization counts as the identity): with
+ * xhat = h * rstd and t = dy * gamma,
+ *   dx     = dres + rstd * (t - xhat * mean(t * xhat))   (dres NULL: left out)
+ *   dgamma = sum over rows of dy * xhat       (added to dgamma when accumulate)
+ * dx is the gradient of x and of res alike.  dy [rows][lddy]; dres, h, dx
+ * [rows][ldh], all in `dtype`; dx may be dy (lddy == ldh), dres or h.
+ * Alignments and limits as rmsnorm_mxfp8, lddy a multiple of 8.  dgamma's sums
+ * run in a fixed order in fp32.  workspace: 16-byte aligned, at least
+ * rmsnorm_backward_workspace(rows, d) bytes (HM_ERR_WORKSPACE), its contents
+ * need not be kept; calls that share one must not overlap.  rows = 0 writes
+ * dgamma = 0 unless accumulating. */
+hm_status rmsnorm_backward_workspace(int64_t rows, int64_t d, size_t* bytes);
+hm_status rmsnorm_backward(const void* dy, int64_t lddy, const void* dres, const void* h, void* dx, int64_t ldh,
+                           hm_dtype dtype, int64_t rows, int64_t d, const float* gamma, const float* rstd,
+                           float* dgamma, int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Global gradient norm over n tensors, and clipping:
+ *   norm = sqrt(sum of every element's square)
+ *   coef = min(1, max_norm / (norm + eps))
+ *   dst  = round(src * coef)    (dst == src: in place, untouched when coef is 1;
+ *                                dst == NULL: the tensor only counts)
+ * stats[0] = norm, stats[1] = coef (device, fp32).  Tensors are HM_BF16 or
+ * HM_F32, dst in src's dtype, each aligned to its element only, n >= 0
+ * elements; host array `tensors` is read during the call.  Sums run in a fixed
+ * order.  A finite gradient has a finite norm unless the norm itself leaves
+ * fp32; a NaN makes norm, coef and every dst NaN; an infinite norm gives
+ * coef 0 (dst: 0, and NaN where src is infinite).  max_norm > 0 (infinity:
+ * never clips), eps >= 0 (HM_ERR_ARG).  dst overlapping its own src other
+ * than exactly, or any other tensor's memory, is the caller's error.
+ * workspace: 16-byte aligned, grad_norm_clip_workspace bytes
+ * (HM_ERR_WORKSPACE), contents need not be kept; calls that share one must
+ * not overlap. */
+typedef struct {
+    const void* src;
+    void* dst;
+    int64_t n;        /* elements */
+    int32_t dtype;    /* hm_dtype */
+    int32_t pad;
+} hm_grad_tensor;
+hm_status grad_norm_clip_workspace(const hm_grad_tensor* tensors, int n, size_t* bytes);
+hm_status grad_norm_clip(const hm_grad_tensor* tensors, int n, float max_norm, float eps, float* stats,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

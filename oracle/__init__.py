@@ -22,6 +22,8 @@ Flexible Sharded Data Parallelism via Runtime-Update Decoupling"):
             parameters Muon does not), PyTorch's documented algorithm.
   mxfp8   - G: MXFP8 quantization, E4M3 elements + UE8M0 scale per block
             (section 3.1 EG1, Figure 4; OCP Microscaling format, ref. [28]).
+  operators - the operators around the update: MXFP8 product, quantization
+            along either axis, RMS norm and its gradient, gradient clipping.
   update  - the composed update phase on logical arrays.
 
 Every function here has a pin in tests/ against something other than itself;
