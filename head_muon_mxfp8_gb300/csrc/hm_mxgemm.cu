@@ -10,7 +10,7 @@
 // scales by 512-byte bulk copies onto the same mbarriers.
 //
 // Two kernels:
-//   mx_gemm_kernel   persistent, 128 x 256 tiles of D, A's rows on the M side.
+//   mx_gemm_pair_kernel   persistent CTA pairs, tiles of 256 x 128 to 256.
 //   mx_gemm_split_kernel  few rows of A: B's rows take the M side (128 lanes),
 //                    A's rows the N side (16 to 128 columns), and K is split
 //                    over the CTAs of a cluster that add their parts through
@@ -45,6 +45,26 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster, int c0,
+                                                 int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void umma_mx_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_cp_sf_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
 __device__ __forceinline__ void umma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                         uint32_t sfb, uint32_t accumulate) {
     asm volatile(
@@ -71,230 +91,333 @@ __host__ __device__ constexpr uint32_t mx_idesc(int m, int n) {
 }
 __device__ __forceinline__ uint32_t sf_id(int kk) { return (static_cast<uint32_t>(kk) << 4) | (static_cast<uint32_t>(kk) << 29); }
 
-__device__ __forceinline__ uint32_t bf16_pair(uint32_t lo, uint32_t hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// ---------------------------------------------------------------------------
-// Epilogue of a 32-column chunk held one row per lane: D's row pointer plus
-// the chunk's first column.  vec: bytes every row start is aligned to (32, 16
-// or 0), so whole chunks leave as full 32-byte sectors.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void store_chunk(const MxGemmArgs& p, int row, int col0, const uint32_t (&r)[32]) {
-    if (row >= p.m || col0 >= p.n) return;
-    const int64_t at = static_cast<int64_t>(row) * p.ldd + col0;
-    const bool whole = col0 + 32 <= p.n;
+// One element of D, row-major.
+__device__ __forceinline__ void store_one(const MxGemmArgs& p, int64_t row, int col, float v) {
+    const int64_t at = row * p.ldd + col;
     if (p.d_f32) {
         float* d = static_cast<float*>(p.d) + at;
-        if (whole && p.vec >= 16) {
-            float4* d4 = reinterpret_cast<float4*>(d);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                                       __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-                if (p.accumulate) {
-                    const float4 o = d4[j];
-                    v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
-                }
-                d4[j] = v;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (col0 + j < p.n) d[j] = p.accumulate ? d[j] + __uint_as_float(r[j]) : __uint_as_float(r[j]);
-        }
+        *d = p.accumulate ? *d + v : v;
     } else {
+        static_cast<uint16_t*>(p.d)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    }
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// ---------------------------------------------------------------------------
+// Epilogue of a 32-column chunk of a tile: lane = column i of D, register j =
+// row j0 + j.  A warp's lanes store neighbours in one row of D: one line per
+// instruction at any alignment and pitch.  With A's rows on the M side instead
+// (a lane holding 32 columns of its row, stored as 32-byte sectors) an
+// instruction touched 32 lines: adding a 256 x 192 fp32 tile to D took 16,000
+// clocks instead of the 4,100 of a 1024-long chunk of its products.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void store_chunk(const MxGemmArgs& p, int i, int j0, const uint32_t (&r)[32]) {
+    if (i >= p.n || j0 >= p.m) return;
+    if (j0 + 32 > p.m) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j0 + j < p.m) store_one(p, j0 + j, i, __uint_as_float(r[j]));
+        return;
+    }
+    const int64_t at = static_cast<int64_t>(j0) * p.ldd + i;
+    if (!p.d_f32) {
         uint16_t* d = static_cast<uint16_t*>(p.d) + at;
-        if (whole && p.vec >= 16) {
-            uint4* d4 = reinterpret_cast<uint4*>(d);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                d4[j] = make_uint4(bf16_pair(r[8 * j], r[8 * j + 1]), bf16_pair(r[8 * j + 2], r[8 * j + 3]),
-                                   bf16_pair(r[8 * j + 4], r[8 * j + 5]), bf16_pair(r[8 * j + 6], r[8 * j + 7]));
-        } else {
+        for (int j = 0; j < 32; ++j, d += p.ldd) *d = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j])));
+    } else if (!p.accumulate) {
+        float* d = static_cast<float*>(p.d) + at;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (col0 + j < p.n) d[j] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j])));
-        }
+        for (int j = 0; j < 32; ++j, d += p.ldd) *d = __uint_as_float(r[j]);
+    } else {
+        float* d = static_cast<float*>(p.d) + at;
+        float old[32];
+        const float* o = d;
+#pragma unroll
+        for (int j = 0; j < 32; ++j, o += p.ldd) old[j] = *o;
+#pragma unroll
+        for (int j = 0; j < 32; ++j, d += p.ldd) *d = old[j] + __uint_as_float(r[j]);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Persistent kernel, 128 x 256 tiles, 320 threads:
-//   warp 0      producer (one thread): codes by TMA, scales by bulk copies;
-//   warp 1      owns TMEM, issues scale copies and MMAs (one thread);
-//   warps 2-9   epilogue, two per TMEM lane quadrant, 128 columns each.
-// TMEM (512 columns): two accumulators of 256 columns at 0 and 224, which
-// share columns 224..255, and two slots of 12 scale columns at 480 and 496.
-// The epilogue drains the shared columns of a tile first and then releases
-// them, so the next tile's MMAs start while the rest is being stored.
+// Persistent kernel on CTA pairs (cta_group::2), tiles of 256 M-side rows (B's
+// rows, D's columns) x BN N-side rows (A's, D's rows), 320 threads per CTA.  Each CTA of a pair loads its 128 M-side rows
+// and half of the N-side rows; the even one issues the MMAs, which read both
+// CTAs' shared memory and leave 128 rows x BN columns in each CTA's TMEM.  The
+// scales of all BN N-side rows are needed by both CTAs, those of the M-side rows
+// by their own.
+//   warp 0      producer (one thread): codes and scales by TMA, both CTAs'
+//               copies counted on the even CTA's barrier;
+//   warp 1      owns TMEM; in the even CTA issues scale copies and MMAs;
+//   warps 2-9   epilogue, two per TMEM lane quadrant, every other 32 columns.
+// TMEM (512 columns): two accumulators and, from column 480, two slots of 16
+// scale columns.  For BN = 256 the accumulators (at 0 and 224) share columns
+// 224..255: the epilogue drains those first and releases them, and the next
+// tile's MMAs start then.  For BN <= 192 they are disjoint.
+//
+// SUMS (fp32 D, K > kChunkK): the tensor core truncates when it adds a product
+// to an accumulator, a bias towards zero that grows with the number of additions
+// (relative error of a 6144 x 4096 weight gradient over 4096 tokens: 1.7e-6 with
+// one sum over all of K, 2.0e-7 in chunks of 2048, 1.1e-7 in chunks of 1024; a
+// plain fp32 product 2.5e-7).  A tile's K is then cut into chunks of 2048,
+// accumulated alternately in the two accumulators, and the epilogue adds the
+// chunks in registers with rounding to nearest while the next one runs.
 // ---------------------------------------------------------------------------
-constexpr int kBigN = 256;
-constexpr int kBigStages = 4;
-constexpr int kBigThreads = 320;
-constexpr int kBigQBytes = kBigN * kTileK;
-constexpr int kBigAcc1 = 224;
-constexpr int kBigSf = 480;
-constexpr int kBigSmem = kBigStages * (kPBytes + kBigQBytes + 3 * kSfBytes) + 1024 + 256;
+constexpr int kPairThreads = 320;
+constexpr int kPairEpiWarps = kPairThreads / 32 - 2;
+constexpr int kChunkK = 2048;
+constexpr int kSfCol = 480;
 
-__device__ __forceinline__ void big_tile(const MxGemmArgs& p, int t, int& tm, int& tn) {
-    // bands of kGroup tile-rows, columns within a band: a band's A stays in L2
-    constexpr int kGroup = 16;
-    const int band = t / (kGroup * p.tiles_n);
-    const int rows = min(kGroup, p.tiles_m - band * kGroup);
-    const int l = t - band * kGroup * p.tiles_n;
-    tm = band * kGroup + l % rows;
-    tn = l / rows;
+template <int BN>
+struct PairMx {
+    static constexpr int STAGES = BN == 256 ? 6 : BN == 128 ? 8 : 7;
+    static constexpr int Q_BYTES = BN / 2 * kTileK;               // this CTA's half of the N side
+    static constexpr int NSF = (BN + 127) / 128;                  // 128-row scale tiles that BN rows from a multiple of 64 touch
+    static constexpr int SF_BYTES = (1 + NSF) * kSfBytes;
+    static constexpr int STAGE_BYTES = kPBytes + Q_BYTES + SF_BYTES;
+    static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 256;
+    static constexpr int ACC1 = BN == 256 ? 224 : BN;
+    static constexpr int CHUNKS = BN / 32;
+    // scale columns are addressed at even offsets only: BN a multiple of 64
+    static_assert(BN % 64 == 0 && SMEM <= 232448 && ACC1 + BN <= kSfCol, "pair tile");
+};
+
+__device__ __forceinline__ void pair_tile(const MxGemmArgs& p, int t, int& tp, int& tq) {
+    // bands of 8 256-row M-side tiles, N-side tiles within a band
+    constexpr int kGroup = 8;
+    const int band = t / (kGroup * p.tiles_q);
+    const int rows = min(kGroup, p.tiles_p - band * kGroup);
+    const int l = t - band * kGroup * p.tiles_q;
+    tp = band * kGroup + l % rows;
+    tq = l / rows;
 }
 
-__global__ void __launch_bounds__(kBigThreads, 1)
-    mx_gemm_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
-                   const __grid_constant__ MxGemmArgs p) {
+template <int BN, bool SUMS>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUtensorMap mq,
+                        const __grid_constant__ CUtensorMap msp, const __grid_constant__ CUtensorMap msq,
+                        const __grid_constant__ MxGemmArgs p) {
+    using C = PairMx<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sp = smem;
-    uint8_t* sq = sp + kBigStages * kPBytes;
-    uint8_t* ssf = sq + kBigStages * kBigQBytes;  // per stage: 512 bytes of A's scales, 1024 of B's
-    uint64_t* full = reinterpret_cast<uint64_t*>(ssf + kBigStages * 3 * kSfBytes);
-    uint64_t* empty = full + kBigStages;
-    uint64_t* tfull = empty + kBigStages;  // two: accumulator written
-    uint64_t* tfree = tfull + 2;           // shared columns of the current tile drained
-    uint64_t* drain = tfree + 1;
+    uint8_t* sq = sp + C::STAGES * kPBytes;
+    uint8_t* ssf = sq + C::STAGES * C::Q_BYTES;  // per stage: the M side's scale tile, then the N side's NSF
+    uint64_t* full = reinterpret_cast<uint64_t*>(ssf + C::STAGES * C::SF_BYTES);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* tfull = empty + C::STAGES;
+    uint64_t* tfree = tfull + 2;
+    uint64_t* drain = tfree + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* bail = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank() & 1u;
+    const bool leader = rank == 0;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kBigStages; ++s) {
+        for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        mbar_init(smem_u32(&tfull[0]), 1);
-        mbar_init(smem_u32(&tfull[1]), 1);
-        mbar_init(smem_u32(tfree), kBigThreads - 64);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&tfull[b]), 1);
+            mbar_init(smem_u32(&tfree[b]), 2 * kPairEpiWarps);
+        }
         mbar_init(smem_u32(drain), 1);
         *bail = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), 512);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_u32(tmem_slot), 512);
+        tmem_relinquish_pair();
     }
     tc_fence_before();
-    __syncthreads();
+    cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int total = p.tiles_m * p.tiles_n;
+    const int total = p.tiles_p * p.tiles_q;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    // a unit: the part of a tile's K that one accumulator sums
+    const int unit_kb = SUMS ? kChunkK / kTileK : p.num_kb;
+    const int units = SUMS ? (p.num_kb + unit_kb - 1) / unit_kb : 1;
 
     if (warp == 0) {
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0, armed = 0, armed_par = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                int tm, tn;
-                big_tile(p, t, tm, tn);
-                const int nsf = min(2, p.sf_rows_b - 2 * tn);  // B's scale tiles that exist
-                const uint8_t* sfa = p.sa + static_cast<int64_t>(tm) * p.num_kb * kSfBytes;
-                const uint8_t* sfb = p.sb + static_cast<int64_t>(2 * tn) * p.num_kb * kSfBytes;
+            for (int t = pair; t < total && ok; t += npairs) {
+                int tp, tq;
+                pair_tile(p, t, tp, tq);
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, p.err, bail)) { ok = false; break; }
-                    const uint32_t fb = smem_u32(&full[s]);
-                    mbar_arrive_expect_tx(fb, kPBytes + kBigQBytes + kSfBytes * (1 + nsf));
-                    tma_load_2d(smem_u32(sp + s * kPBytes), &tma, fb, kb * kTileK, tm * kTileP);
-                    tma_load_2d(smem_u32(sq + s * kBigQBytes), &tmb, fb, kb * kTileK, tn * kBigN);
-                    const uint32_t sf = smem_u32(ssf + s * 3 * kSfBytes);
-                    bulk_load(sf, sfa + static_cast<int64_t>(kb) * kSfBytes, kSfBytes, fb);
-                    for (int j = 0; j < nsf; ++j)
-                        bulk_load(sf + kSfBytes * (1 + j), sfb + (static_cast<int64_t>(j) * p.num_kb + kb) * kSfBytes,
-                                  kSfBytes, fb);
                     armed |= 1u << s;
                     armed_par = (armed_par & ~(1u << s)) | (ph << s);
-                    if (++s == kBigStages) { s = 0; ph ^= 1u; }
+                    const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
+                    if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * C::STAGE_BYTES);
+                    tma_load_2d_pair(smem_u32(sp + s * kPBytes), &mp, fb, kb * kTileK, tp * 256 + rank * 128);
+                    tma_load_2d_pair(smem_u32(sq + s * C::Q_BYTES), &mq, fb, kb * kTileK, tq * BN + rank * (BN / 2));
+                    const uint32_t sf = smem_u32(ssf + s * C::SF_BYTES);
+                    tma_load_3d_pair(sf, &msp, fb, 0, kb, tp * 2 + rank);
+                    tma_load_3d_pair(sf + kSfBytes, &msq, fb, 0, kb, tq * BN / 128);
+                    if (++s == C::STAGES) { s = 0; ph ^= 1u; }
                 }
             }
-            // wait for this CTA's own copies still in flight
-            for (int k = 0; k < kBigStages; ++k)
-                if (armed & (1u << k)) mbar_wait(smem_u32(&full[k]), (armed_par >> k) & 1u, p.err, bail, false);
+            // the even CTA's full barriers count both CTAs' bytes: waiting on
+            // them covers every copy of the pair still in flight
+            if (leader)
+                for (int k = 0; k < C::STAGES; ++k)
+                    if (armed & (1u << k)) mbar_wait(smem_u32(&full[k]), (armed_par >> k) & 1u, p.err, bail, false);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int s = 0, slot = 0;
+        if (leader) {
+            // the whole warp walks the loop (its waits and descriptors are warp-uniform)
+            // and one elected lane issues: with a single lane in the loop the issue of a
+            // stage's copies and MMAs took longer than the MMAs themselves
+            int s = 0, slot = 0, u = 0;
             uint32_t ph = 0;
             bool ok = true;
-            int it = 0;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
-                // tile it - 1 has released the shared columns (which also means
-                // that tile it - 2, in this accumulator, was drained)
-                if (it && !mbar_wait(smem_u32(tfree), (it - 1) & 1, p.err, bail)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + ((it & 1) ? kBigAcc1 : 0);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!mbar_wait(smem_u32(&full[s]), ph, p.err, bail)) { ok = false; break; }
+            const uint64_t pd0 = desc_sw128(smem_u32(sp)), qd0 = desc_sw128(smem_u32(sq)), sd0 = desc_sf(smem_u32(ssf));
+            for (int t = pair; t < total && ok; t += npairs) {
+                int tp, tq;
+                pair_tile(p, t, tp, tq);
+                const uint32_t sfq_col = static_cast<uint32_t>(tq * BN % 128) / 32;  // the tile's rows inside its scale tiles
+                for (int c = 0; c < units && ok; ++c, ++u) {
+                    // BN = 256: unit u - 1 has released the shared columns, so unit u - 2
+                    // (this accumulator's last) is drained too; else unit u - 2 is drained
+                    if (BN == 256) {
+                        if (u >= 1) ok = mbar_wait(smem_u32(&tfree[(u - 1) & 1]), ((u - 1) >> 1) & 1, p.err, bail);
+                    } else {
+                        if (u >= 2) ok = mbar_wait(smem_u32(&tfree[u & 1]), ((u >> 1) - 1) & 1, p.err, bail);
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sf = smem_u32(ssf + s * 3 * kSfBytes);
-                    const uint32_t tsf = tmem + kBigSf + slot * 16;
-                    tmem_cp_sf(tsf, desc_sf(sf));
-                    tmem_cp_sf(tsf + 4, desc_sf(sf + kSfBytes));
-                    tmem_cp_sf(tsf + 8, desc_sf(sf + 2 * kSfBytes));
-                    slot ^= 1;
-                    const uint64_t ad = desc_sw128(smem_u32(sp + s * kPBytes));
-                    const uint64_t bd = desc_sw128(smem_u32(sq + s * kBigQBytes));
-                    // the last stage may hold fewer blocks: codes and scales past k are not used
-                    const int nk = kb + 1 < p.num_kb ? 4 : p.last_nk;
-                    for (int kk = 0; kk < nk; ++kk)
-                        umma_mx(d, ad + 2 * kk, bd + 2 * kk, mx_idesc(kTileP, kBigN) | sf_id(kk), tsf, tsf + 4,
-                                (kb | kk) != 0);
-                    umma_commit(smem_u32(&empty[s]));
-                    if (++s == kBigStages) { s = 0; ph ^= 1u; }
+                    const uint32_t d = tmem + ((u & 1) ? C::ACC1 : 0);
+                    const int kb0 = c * unit_kb, kb1 = min(kb0 + unit_kb, p.num_kb);
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), ph, p.err, bail));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t tsf = tmem + kSfCol + slot * 16;
+                        const uint64_t pd = pd0 + static_cast<uint64_t>(s * (kPBytes >> 4));
+                        const uint64_t qd = qd0 + static_cast<uint64_t>(s * (C::Q_BYTES >> 4));
+                        const uint64_t sd = sd0 + static_cast<uint64_t>(s * (C::SF_BYTES >> 4));
+                        // the last stage may hold fewer blocks: codes and scales past k are not used
+                        const int nk = kb + 1 < p.num_kb ? 4 : p.last_nk;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k <= C::NSF; ++k) tmem_cp_sf_pair(tsf + 4 * k, sd + k * (kSfBytes >> 4));
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                if (kk < nk)
+                                    umma_mx_pair(d, pd + 2 * kk, qd + 2 * kk, mx_idesc(256, BN) | sf_id(kk), tsf,
+                                                 tsf + 4 + sfq_col, (kb - kb0) | kk);
+                            umma_commit_pair(smem_u32(&empty[s]));
+                            if (kb + 1 == kb1) umma_commit_pair(smem_u32(&tfull[u & 1]));
+                        }
+                        __syncwarp();
+                        slot ^= 1;
+                        if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+                    }
                 }
-                if (!ok) break;
-                umma_commit(smem_u32(&tfull[it & 1]));
             }
-            // every MMA this thread issued has completed before TMEM is freed
-            umma_commit(smem_u32(drain));
-            mbar_wait(smem_u32(drain), 0, p.err, bail, false);
+            // every MMA this warp issued has completed before TMEM is freed
+            if (elect_one()) {
+                umma_commit_pair(smem_u32(drain));
+                mbar_wait(smem_u32(drain), 0, p.err, bail, false);
+            }
+            __syncwarp();
         }
     } else {
         const int q = warp & 3;            // TMEM lane quadrant of this warp
-        const int half = (warp - 2) >> 2;  // which 128 of the tile's columns it drains
-        int it = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
-            int tm, tn;
-            big_tile(p, t, tm, tn);
-            bool ok = mbar_wait(smem_u32(&tfull[it & 1]), (it >> 1) & 1, p.err, bail);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            const int row = tm * kTileP + q * 32 + lane;
-            const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + ((it & 1) ? kBigAcc1 : 0) + half * 128;
-            // chunk order: accumulator 0 shares its last chunk, accumulator 1 its first
-            const bool owner = half == ((it & 1) ? 0 : 1);
-            if (!owner) {
-                tc_fence_before();  // its loads of the previous tile
-                mbar_arrive(smem_u32(tfree));
+        const int half = (warp - 2) >> 2;  // takes the chunks of this parity
+        // one relaxed arrival per warp: it hands back TMEM columns that were read, no
+        // memory, and a release at cluster scope held each one for 2,000 clocks
+        auto release = [&](uint32_t bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(bar);
+        };
+        const uint32_t free0 = mapa_shared(smem_u32(&tfree[0]), 0), free1 = mapa_shared(smem_u32(&tfree[1]), 0);
+        int u = 0;
+        bool ok = true;
+        for (int t = pair; t < total && ok; t += npairs) {
+            int tp, tq;
+            pair_tile(p, t, tp, tq);
+            const int i = tp * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
+            float sum[SUMS ? (C::CHUNKS + 1) / 2 : 1][32];
+            if (p.accumulate) {
+                // the earlier D is read when the tile is done: start it into the L2
+                // now, lane l the line of row l of each chunk
+#pragma unroll
+                for (int ch = half; ch < C::CHUNKS; ch += 2)
+                    if (i - lane < p.n && tq * BN + ch * 32 + lane < p.m)
+                        prefetch_l2(static_cast<const float*>(p.d) +
+                                    static_cast<int64_t>(tq * BN + ch * 32 + lane) * p.ldd + (i - lane));
             }
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                const int ch = (it & 1) ? c : 3 - c;
-                uint32_t r[32];
-                tmem_ld32(acc + ch * 32, r);
-                tmem_ld_wait();
-                tmem_ld_pin(r);
-                if (c == 0 && owner) {
-                    tc_fence_before();
-                    mbar_arrive(smem_u32(tfree));
+            for (int c = 0; c < units; ++c, ++u) {
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[u & 1]), (u >> 1) & 1, p.err, bail));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + ((u & 1) ? C::ACC1 : 0);
+                const uint32_t freed = (u & 1) ? free1 : free0;
+                // BN = 256: accumulator 0 shares its last chunk (odd half), accumulator 1 its
+                // first (even half); that half drains it first, the other has nothing to release
+                const bool owner = BN == 256 && half == ((u & 1) ? 0 : 1);
+                if (BN == 256 && !owner) release(freed);
+#pragma unroll
+                for (int k = 0; k < (C::CHUNKS + 1) / 2; ++k) {
+                    const int order = BN == 256 && !(u & 1) ? (C::CHUNKS + 1) / 2 - 1 - k : k;
+                    const int ch = 2 * order + half;
+                    if (ch >= C::CHUNKS) break;
+                    if (SUMS) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t r[16];
+                            tmem_ld16(acc + ch * 32 + h * 16, r);
+                            tmem_ld_wait();
+                            tmem_ld_pin16(r);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float v = __uint_as_float(r[j]);
+                                sum[k][16 * h + j] = c ? sum[k][16 * h + j] + v : v;
+                            }
+                        }
+                        continue;
+                    }
+                    uint32_t r[32];
+                    tmem_ld32(acc + ch * 32, r);
+                    tmem_ld_wait();
+                    tmem_ld_pin(r);
+                    if (owner && k == 0) release(freed);
+                    store_chunk(p, i, tq * BN + ch * 32, r);
                 }
-                store_chunk(p, row, tn * kBigN + half * 128 + ch * 32, r);
+                if (BN != 256) release(freed);
+            }
+            if (SUMS && ok) {
+#pragma unroll
+                for (int k = 0; k < (C::CHUNKS + 1) / 2; ++k) {
+                    const int ch = 2 * k + half;
+                    if (ch >= C::CHUNKS) break;
+                    uint32_t r[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[k][j]);
+                    store_chunk(p, i, tq * BN + ch * 32, r);
+                }
             }
         }
     }
-    __syncthreads();
+    // the peer's MMAs read this CTA's shared memory and write its TMEM: keep
+    // both alive until every role of both CTAs is done
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 
@@ -321,16 +444,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
-}
-
-__device__ __forceinline__ void store_one(const MxGemmArgs& p, int row, int col, float v) {
-    const int64_t at = static_cast<int64_t>(row) * p.ldd + col;
-    if (p.d_f32) {
-        float* d = static_cast<float*>(p.d) + at;
-        *d = p.accumulate ? *d + v : v;
-    } else {
-        static_cast<uint16_t*>(p.d)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    }
 }
 
 template <int BN>
@@ -397,28 +510,34 @@ __global__ void __launch_bounds__(kSplitThreads)
                 if (armed & (1u << k)) mbar_wait(smem_u32(&full[k]), (armed_par >> k) & 1u, p.err, bail, false);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int s = 0, slot = 0;
-            uint32_t ph = 0;
-            const uint32_t sfq_col = static_cast<uint32_t>(tq * BN % 128) / 32;  // A's rows inside its 128-row scale tile
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(smem_u32(&full[s]), ph, p.err, bail)) break;
-                tc_fence_after();
-                const uint32_t sf = smem_u32(ssf + s * 2 * kSfBytes);
-                const uint32_t tsf = tmem + C::ACC + slot * 8;
-                tmem_cp_sf(tsf, desc_sf(sf));
-                tmem_cp_sf(tsf + 4, desc_sf(sf + kSfBytes));
-                slot ^= 1;
-                const uint64_t pd = desc_sw128(smem_u32(sp + s * kPBytes));
-                const uint64_t qd = desc_sw128(smem_u32(sq + s * C::Q_BYTES));
-                const int nk = kb + 1 < p.num_kb ? 4 : p.last_nk;
-                for (int kk = 0; kk < nk; ++kk)
-                    umma_mx(tmem, pd + 2 * kk, qd + 2 * kk, mx_idesc(kTileP, BN) | sf_id(kk), tsf, tsf + 4 + sfq_col,
-                            (kb - kb0) | kk);
+        int s = 0, slot = 0;
+        uint32_t ph = 0;
+        const uint32_t sfq_col = static_cast<uint32_t>(tq * BN % 128) / 32;  // A's rows inside its 128-row scale tile
+        const uint64_t pd0 = desc_sw128(smem_u32(sp)), qd0 = desc_sw128(smem_u32(sq)), sd0 = desc_sf(smem_u32(ssf));
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), ph, p.err, bail))) break;
+            tc_fence_after();
+            const uint32_t tsf = tmem + C::ACC + slot * 8;
+            const uint64_t pd = pd0 + static_cast<uint64_t>(s * (kPBytes >> 4));
+            const uint64_t qd = qd0 + static_cast<uint64_t>(s * (C::Q_BYTES >> 4));
+            const uint64_t sd = sd0 + static_cast<uint64_t>(s * (2 * kSfBytes >> 4));
+            const int nk = kb + 1 < p.num_kb ? 4 : p.last_nk;
+            if (elect_one()) {
+                tmem_cp_sf(tsf, sd);
+                tmem_cp_sf(tsf + 4, sd + (kSfBytes >> 4));
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    if (kk < nk)
+                        umma_mx(tmem, pd + 2 * kk, qd + 2 * kk, mx_idesc(kTileP, BN) | sf_id(kk), tsf, tsf + 4 + sfq_col,
+                                (kb - kb0) | kk);
                 umma_commit(smem_u32(&empty[s]));
-                if (++s == C::STAGES) { s = 0; ph ^= 1u; }
             }
-            // also covers every MMA issued before an early exit
+            __syncwarp();
+            slot ^= 1;
+            if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+        }
+        // also covers every MMA issued before an early exit
+        if (elect_one()) {
             umma_commit(smem_u32(tfull));
             mbar_wait(smem_u32(tfull), 0, p.err, bail, false);
         }
@@ -490,6 +609,20 @@ bool map_codes(CUtensorMap* m, const uint8_t* base, int64_t k, int64_t rows, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tiled scales of `rows` rows as [row tiles][num_kb][128 words]: boxes of `tiles`
+// 512-byte scale tiles of one K stage, zero past the last row tile.
+bool map_scales(CUtensorMap* m, const uint8_t* base, int num_kb, int64_t rows, int tiles) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(num_kb), static_cast<cuuint64_t>((rows + 127) / 128)};
+    const cuuint64_t strides[2] = {kSfBytes, static_cast<cuuint64_t>(num_kb) * kSfBytes};
+    const cuuint32_t box[3] = {128, 1, static_cast<cuuint32_t>(tiles)};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class Kernel>
 cudaError_t allow_smem(Kernel kernel, int bytes, bool (&done)[64]) {
     int dev = 0;
@@ -531,6 +664,44 @@ cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_
     return cudaLaunchKernelEx(&cfg, mx_gemm_split_kernel<BN>, ma, mb, p);
 }
 
+template <int BN, bool SUMS>
+cudaError_t launch_pair(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, MxGemmArgs p, cudaStream_t st) {
+    using C = PairMx<BN>;
+    static bool done[64] = {false};
+    cudaError_t e = allow_smem(mx_gemm_pair_kernel<BN, SUMS>, C::SMEM, done);
+    if (e != cudaSuccess) return e;
+    CUtensorMap mp, mq, msp, msq;
+    if (!map_codes(&mp, b, p.k, p.n, ldb, kTileP) || !map_codes(&mq, a, p.k, p.m, lda, BN / 2) ||
+        !map_scales(&msp, p.sb, p.num_kb, p.n, 1) || !map_scales(&msq, p.sa, p.num_kb, p.m, C::NSF))
+        return cudaErrorUnknown;
+    p.tiles_p = (p.n + 255) / 256;
+    p.tiles_q = (p.m + BN - 1) / BN;
+    const int64_t total = static_cast<int64_t>(p.tiles_p) * p.tiles_q;
+    const int pairs = static_cast<int>(total < device_sm_count() / 2 ? total : device_sm_count() / 2);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs, 1, 1);
+    cfg.blockDim = dim3(kPairThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    note_launch();
+    return cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<BN, SUMS>, mp, mq, msp, msq, p);
+}
+
+template <int BN>
+cudaError_t launch_pair_of(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, const MxGemmArgs& p, cudaStream_t st) {
+    // the sums in registers take disjoint accumulators
+    if constexpr (BN <= 192)
+        if (p.d_f32 && p.num_kb > kChunkK / kTileK) return launch_pair<BN, true>(a, lda, b, ldb, p, st);
+    return launch_pair<BN, false>(a, lda, b, ldb, p, st);
+}
+
 }  // namespace
 
 cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, const MxGemmArgs& args,
@@ -545,26 +716,27 @@ cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int6
     }
     p.num_kb = (p.k + kTileK - 1) / kTileK;
     p.last_nk = (p.k - (p.num_kb - 1) * kTileK) / 32;
-    p.sf_rows_b = (p.n + 127) / 128;
     p.err = device_error_word();
-    const int64_t row_bytes = p.ldd * (p.d_f32 ? 4 : 2);
-    p.vec = (reinterpret_cast<uintptr_t>(p.d) | static_cast<uintptr_t>(row_bytes)) % 16 == 0 ? 16 : 0;
     if (p.m <= 16) return launch_split<16>(a, lda, b, ldb, p, st);
     if (p.m <= 32) return launch_split<32>(a, lda, b, ldb, p, st);
     if (p.m <= 64) return launch_split<64>(a, lda, b, ldb, p, st);
     if (p.m <= 128) return launch_split<128>(a, lda, b, ldb, p, st);
-    static bool done[64] = {false};
-    cudaError_t e = allow_smem(mx_gemm_kernel, kBigSmem, done);
-    if (e != cudaSuccess) return e;
-    CUtensorMap ma, mb;
-    if (!map_codes(&ma, a, p.k, p.m, lda, kTileP) || !map_codes(&mb, b, p.k, p.n, ldb, kBigN)) return cudaErrorUnknown;
-    p.tiles_m = (p.m + kTileP - 1) / kTileP;
-    p.tiles_n = (p.n + kBigN - 1) / kBigN;
-    const int64_t total = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-    const int grid = static_cast<int>(total < device_sm_count() ? total : device_sm_count());
-    note_launch();
-    mx_gemm_kernel<<<grid, kBigThreads, kBigSmem, st>>>(ma, mb, p);
-    return cudaGetLastError();
+    // The tile width that leaves the least time to the pair with the most tiles.  A
+    // stage's time goes with the rows it loads (256 + BN): 128-wide tiles took 0.79 of
+    // the time of 256-wide ones (293 and 371 ns per stage, K = 5120, 640 tiles of 256).
+    const bool sums = p.d_f32 && p.num_kb > kChunkK / kTileK;
+    const int64_t pairs = device_sm_count() / 2;
+    int best = 0;
+    int64_t least = 0;
+    for (const int bn : {256, 192, 128}) {
+        if (bn > 192 && sums) continue;
+        const int64_t tiles = static_cast<int64_t>((p.n + 255) / 256) * ((p.m + bn - 1) / bn);
+        const int64_t cost = (tiles + pairs - 1) / pairs * (256 + bn);
+        if (!best || cost < least) best = bn, least = cost;
+    }
+    if (best == 256) return launch_pair_of<256>(a, lda, b, ldb, p, st);
+    if (best == 192) return launch_pair_of<192>(a, lda, b, ldb, p, st);
+    return launch_pair_of<128>(a, lda, b, ldb, p, st);
 }
 
 }  // namespace hm

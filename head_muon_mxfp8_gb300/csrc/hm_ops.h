@@ -19,10 +19,8 @@ struct MxGemmArgs {
     // filled in by launch_mx_gemm
     int32_t num_kb;      // stages of 128 along K
     int32_t last_nk;     // blocks of 32 in the last stage
-    int32_t sf_rows_b;   // 128-row tiles of B's scales
-    int32_t tiles_m, tiles_n;
+    int32_t tiles_p, tiles_q;  // pair kernel: tiles along n and m
     int32_t split;       // CTAs of a cluster that share K
-    int32_t vec;         // bytes every row of D is aligned to: 16 or 0
     int32_t* err;
 };
 cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, const MxGemmArgs& args,

@@ -582,3 +582,31 @@ def test_operators_in_a_graph(hm, dev):
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(stats, want_stats)
     assert hm.hm_device_error() == 0
+
+
+@pytest.mark.parametrize("m,n,k,out", [
+    (1024, 6400, 2208, "f32"),    # 256 x 192 tiles, K summed in two chunks, last one short
+    (2304, 3264, 1056, "bf16"),   # 256 x 256 tiles past the last column
+    (2000, 3201, 160, "f32"),     # odd pitch: the swapped roles
+])
+def test_product_tile_widths(hm, dev, m, n, k, out):
+    """Every tile width of the persistent kernel, against float64 on the GPU (too large for the host)."""
+    g = torch.Generator(device=dev)
+    g.manual_seed(m + n)
+    ops = []
+    for rows in (m, n):
+        codes = torch.randint(0, 256, (rows, k), generator=g, device=dev, dtype=torch.uint8)
+        codes[codes & 0x7F == 0x7F] = 0x10
+        sf = torch.randint(120, 131, (rows, k // 32), generator=g, device=dev, dtype=torch.uint8)
+        tiled = torch.from_numpy(OX.scale_tile_128x4(sf.cpu().numpy())).to(dev)
+        val = codes.view(torch.float8_e4m3fn).double().view(rows, -1, 32) * torch.exp2(sf.double() - 127)[:, :, None]
+        ops.append((codes, tiled, val.view(rows, k)))
+    (qa, ta, va), (qb, tb, vb) = ops
+    d = torch.zeros(m, n, dtype=_dt(hm, out)[0], device=dev)
+    _gemm(hm, qa, ta, qb, tb, m, n, k, d)
+    ref, bound = va @ vb.t(), va.abs() @ vb.abs().t()
+    tol = (k / 32 + 33) * 2 * U * bound
+    if out == "bf16":
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()
+    assert bool(((d.double() - ref).abs() <= tol).all())
+    assert hm.hm_device_error() == 0
