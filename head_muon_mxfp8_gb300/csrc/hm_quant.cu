@@ -13,6 +13,8 @@
 #include "hm_mx_device.cuh"
 #include "hm_ops.h"
 
+#include <cuda_bf16.h>
+
 namespace hm {
 
 namespace {
@@ -51,9 +53,37 @@ __device__ __forceinline__ void load8(const void* x, int64_t at, int left, bool 
     }
 }
 
-template <bool F32>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float sc) {
+    return cvt_e4m3x2(a * sc, b * sc) | (static_cast<uint32_t>(cvt_e4m3x2(c * sc, d * sc)) << 16);
+}
+__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// elementwise max of magnitudes of two bf16 pairs (a NaN is left out, as by fmaxf)
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// The block's scale exponent from this lane's amax over 8 of its columns.
+__device__ __forceinline__ int row_exponent(float amax, int block) {
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    if (block == 128) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+    }
+    return mx_scale_exponent(amax);
+}
+
+// The tile, in two forms.
+//   PACKED (bf16 x, no factors): y is x, so the tile stays in bf16 pairs --
+//     half the shared memory and half its traffic, and magnitudes are compared
+//     two at a time; a thread's column work is a pair of columns x 32 rows.
+//   else: y in fp32; a thread's column work is one column x 2 x 32 rows.
+// A thread loads 8 vectors of 8 columns before it uses the first.
+template <bool F32, bool PACKED, bool COL>
 __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_constant__ QuantArgs p) {
-    extern __shared__ __align__(16) float tile[];  // [128][128], transposed output only
+    extern __shared__ __align__(16) uint32_t tile[];  // [128][64] bf16 pairs or [128][128] fp32
     __shared__ __align__(16) uint8_t s_row[512];
     __shared__ __align__(16) uint8_t s_col[512];
     __shared__ float amax_col[4][kQTile];
@@ -63,51 +93,82 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
     const int64_t cols32 = (p.cols + 31) / 32 * 32, rows32 = (p.rows + 31) / 32 * 32;
     const int c8 = (lane & 15) * 8;
     const int left = static_cast<int>(min(static_cast<int64_t>(8), max(static_cast<int64_t>(0), p.cols - (c0 + c8))));
-    float cm[8];
+    const int rl0 = warp * 16 + (lane >> 4);  // this lane's rows: rl0 + 2 i
+
+    if constexpr (PACKED) {
+        uint4 raw[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) cm[k] = p.col_mul && k < left ? p.col_mul[c0 + c8 + k] : 1.f;
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = r0 + rl0 + 2 * i;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < p.rows && left > 0) {
+                const uint16_t* src = static_cast<const uint16_t*>(p.x) + r * p.ldx + c0 + c8;
+                if (p.vec && left == 8) {
+                    raw[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+                } else {
+                    uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int rl = warp * 16 + i * 2 + (lane >> 4);
-        const int64_t r = r0 + rl;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (r < p.rows && left > 0) {
-            load8<F32>(p.x, r * p.ldx + c0 + c8, left, p.vec, v);
-            if (p.row_mul) {
-                const float rm = p.row_mul[r];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] *= rm;
-            }
-            if (p.col_mul) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] *= cm[k];
+                    for (int k = 0; k < 8; ++k) h[k] = k < left ? src[k] : 0u;
+                    raw[i] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+                }
             }
         }
-        if (p.qt) {
-            float4* t4 = reinterpret_cast<float4*>(tile + rl * kQTile + c8);
-            t4[0] = make_float4(v[0], v[1], v[2], v[3]);
-            t4[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
-        if (p.q) {
-            float amax = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[k]));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            if (p.block == 128) {
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+        for (int i = 0; i < 8; ++i) {
+            const int rl = rl0 + 2 * i;
+            if (COL) *reinterpret_cast<uint4*>(tile + rl * (kQTile / 2) + c8 / 2) = raw[i];
+            if (p.q) {
+                const uint32_t m = max_abs2(max_abs2(max_abs2(max_abs2(0u, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
+                const int e = row_exponent(fmaxf(lo_f32(m), hi_f32(m)), p.block);
+                const float sc = mx_inv_scale(e);
+                const bool live = r0 + rl < p.rows && c0 + c8 < cols32;
+                if (live)
+                    __stcs(reinterpret_cast<uint2*>(p.q + (r0 + rl) * p.ldq + c0 + c8),
+                           make_uint2(codes4(lo_f32(raw[i].x), hi_f32(raw[i].x), lo_f32(raw[i].y), hi_f32(raw[i].y), sc),
+                                      codes4(lo_f32(raw[i].z), hi_f32(raw[i].z), lo_f32(raw[i].w), hi_f32(raw[i].w), sc)));
+                if ((lane & 3) == 0)
+                    s_row[(rl & 31) * 16 + (rl >> 5) * 4 + ((lane & 15) >> 2)] = live ? static_cast<uint8_t>(e + 127) : 0;
             }
-            const int e = mx_scale_exponent(amax);
-            const float sc = mx_inv_scale(e);
-            const bool live = r < p.rows && c0 + c8 < cols32;
-            if (live) {
-                const uint32_t lo = cvt_e4m3x2(v[0] * sc, v[1] * sc) | (static_cast<uint32_t>(cvt_e4m3x2(v[2] * sc, v[3] * sc)) << 16);
-                const uint32_t hi = cvt_e4m3x2(v[4] * sc, v[5] * sc) | (static_cast<uint32_t>(cvt_e4m3x2(v[6] * sc, v[7] * sc)) << 16);
-                *reinterpret_cast<uint2*>(p.q + r * p.ldq + c0 + c8) = make_uint2(lo, hi);
+        }
+    } else {
+        float cm[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) cm[k] = p.col_mul && k < left ? p.col_mul[c0 + c8 + k] : 1.f;
+        float v[8][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = r0 + rl0 + 2 * i;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+            if (r < p.rows && left > 0) load8<F32>(p.x, r * p.ldx + c0 + c8, left, p.vec, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int rl = rl0 + 2 * i;
+            const int64_t r = r0 + rl;
+            if (r < p.rows) {  // outside x the zeros stay +0 whatever the factors' signs
+                const float rm = p.row_mul ? p.row_mul[r] : 1.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[i][k] = k < left ? v[i][k] * rm * cm[k] : 0.f;
             }
-            if ((lane & 3) == 0)
-                s_row[(rl & 31) * 16 + (rl >> 5) * 4 + ((lane & 15) >> 2)] = live ? static_cast<uint8_t>(e + 127) : 0;
+            if (COL) {
+                float4* t4 = reinterpret_cast<float4*>(tile + rl * kQTile + c8);
+                t4[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+                t4[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
+            }
+            if (p.q) {
+                float amax = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[i][k]));
+                const int e = row_exponent(amax, p.block);
+                const float sc = mx_inv_scale(e);
+                const bool live = r < p.rows && c0 + c8 < cols32;
+                if (live)
+                    __stcs(reinterpret_cast<uint2*>(p.q + r * p.ldq + c0 + c8),
+                           make_uint2(codes4(v[i][0], v[i][1], v[i][2], v[i][3], sc), codes4(v[i][4], v[i][5], v[i][6], v[i][7], sc)));
+                if ((lane & 3) == 0)
+                    s_row[(rl & 31) * 16 + (rl >> 5) * 4 + ((lane & 15) >> 2)] = live ? static_cast<uint8_t>(e + 127) : 0;
+            }
         }
     }
     __syncthreads();
@@ -115,65 +176,114 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
         const int64_t col_tiles = (cols32 + 127) / 128;
         reinterpret_cast<uint4*>(p.s + (rt * col_tiles + ct) * 512)[threadIdx.x] = reinterpret_cast<const uint4*>(s_row)[threadIdx.x];
     }
-    if (!p.qt) return;
-    // thread: one column, two of its four 32-row blocks
-    const int c = threadIdx.x & 127, h = threadIdx.x >> 7;
-    const bool col_live = c0 + c < p.cols;
-    for (int b = 2 * h; b < 2 * h + 2; ++b) {
-        float amax = 0.f;
+    if constexpr (COL) {
+        if constexpr (PACKED) {
+            const int cp = threadIdx.x & 63, b = threadIdx.x >> 6;
+            const int c = 2 * cp;
+            uint32_t w[32];
+            uint32_t m = 0u;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) amax = fmaxf(amax, fabsf(tile[(b * 32 + k) * kQTile + c]));
-        amax_col[b][c] = amax;
-    }
-    if (p.block == 128) __syncthreads();
-    for (int b = 2 * h; b < 2 * h + 2; ++b) {
-        float amax = amax_col[b][c];
-        if (p.block == 128)
-            amax = fmaxf(fmaxf(amax_col[0][c], amax_col[1][c]), fmaxf(amax_col[2][c], amax_col[3][c]));
-        const int e = mx_scale_exponent(amax);
-        const float sc = mx_inv_scale(e);
-        const bool live = col_live && r0 + b * 32 < rows32;
-        s_col[(c & 31) * 16 + (c >> 5) * 4 + b] = live ? static_cast<uint8_t>(e + 127) : 0;
-        if (!live) continue;
-        uint32_t w[8];
+            for (int k = 0; k < 32; ++k) w[k] = tile[(b * 32 + k) * (kQTile / 2) + cp];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float* t = tile + (b * 32 + 4 * k) * kQTile + c;
-            w[k] = cvt_e4m3x2(t[0] * sc, t[kQTile] * sc) |
-                   (static_cast<uint32_t>(cvt_e4m3x2(t[2 * kQTile] * sc, t[3 * kQTile] * sc)) << 16);
+            for (int k = 0; k < 32; ++k) m = max_abs2(m, w[k]);
+            float a0 = lo_f32(m), a1 = hi_f32(m);
+            if (p.block == 128) {
+                amax_col[b][c] = a0;
+                amax_col[b][c + 1] = a1;
+                __syncthreads();
+                a0 = fmaxf(fmaxf(amax_col[0][c], amax_col[1][c]), fmaxf(amax_col[2][c], amax_col[3][c]));
+                a1 = fmaxf(fmaxf(amax_col[0][c + 1], amax_col[1][c + 1]), fmaxf(amax_col[2][c + 1], amax_col[3][c + 1]));
+            }
+            const int e0 = mx_scale_exponent(a0), e1 = mx_scale_exponent(a1);
+            const float sc0 = mx_inv_scale(e0), sc1 = mx_inv_scale(e1);
+            const bool row_live = r0 + b * 32 < rows32;
+            const bool live0 = row_live && c0 + c < p.cols, live1 = row_live && c0 + c + 1 < p.cols;
+            uint8_t* out = p.qt + (c0 + c) * p.ldqt + r0 + b * 32;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t x[4], y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t* q = w + 16 * h + 4 * k;
+                    x[k] = codes4(lo_f32(q[0]), lo_f32(q[1]), lo_f32(q[2]), lo_f32(q[3]), sc0);
+                    y[k] = codes4(hi_f32(q[0]), hi_f32(q[1]), hi_f32(q[2]), hi_f32(q[3]), sc1);
+                }
+                if (live0) reinterpret_cast<uint4*>(out)[h] = make_uint4(x[0], x[1], x[2], x[3]);
+                if (live1) reinterpret_cast<uint4*>(out + p.ldqt)[h] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            s_col[(c & 31) * 16 + (c >> 5) * 4 + b] = live0 ? static_cast<uint8_t>(e0 + 127) : 0;
+            s_col[((c + 1) & 31) * 16 + (c >> 5) * 4 + b] = live1 ? static_cast<uint8_t>(e1 + 127) : 0;
+        } else {
+            const float* y = reinterpret_cast<const float*>(tile);
+            const int c = threadIdx.x & 127, h = threadIdx.x >> 7;
+            const bool col_live = c0 + c < p.cols;
+            float w[2][32], a[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                a[j] = 0.f;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) w[j][k] = y[((2 * h + j) * 32 + k) * kQTile + c];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) a[j] = fmaxf(a[j], fabsf(w[j][k]));
+            }
+            if (p.block == 128) {
+                amax_col[h][c] = fmaxf(a[0], a[1]);
+                __syncthreads();
+                a[0] = a[1] = fmaxf(amax_col[0][c], amax_col[1][c]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int b = 2 * h + j;
+                const int e = mx_scale_exponent(a[j]);
+                const float sc = mx_inv_scale(e);
+                const bool live = col_live && r0 + b * 32 < rows32;
+                s_col[(c & 31) * 16 + (c >> 5) * 4 + b] = live ? static_cast<uint8_t>(e + 127) : 0;
+                if (!live) continue;
+                uint4* out = reinterpret_cast<uint4*>(p.qt + (c0 + c) * p.ldqt + r0 + b * 32);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float* q = w[j] + 16 * g + 4 * k;
+                        x[k] = codes4(q[0], q[1], q[2], q[3], sc);
+                    }
+                    out[g] = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            }
         }
-        uint4* out = reinterpret_cast<uint4*>(p.qt + (c0 + c) * p.ldqt + r0 + b * 32);
-        out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        out[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int64_t row_tiles = (rows32 + 127) / 128;
-        reinterpret_cast<uint4*>(p.st + (ct * row_tiles + rt) * 512)[threadIdx.x] = reinterpret_cast<const uint4*>(s_col)[threadIdx.x];
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            const int64_t row_tiles = (rows32 + 127) / 128;
+            reinterpret_cast<uint4*>(p.st + (ct * row_tiles + rt) * 512)[threadIdx.x] = reinterpret_cast<const uint4*>(s_col)[threadIdx.x];
+        }
     }
 }
 
-template <bool F32>
+template <bool F32, bool PACKED, bool COL>
 cudaError_t launch(const QuantArgs& a, cudaStream_t st) {
-    const int smem = a.qt ? kQTile * kQTile * 4 : 0;
+    constexpr int smem = !COL ? 0 : kQTile * kQTile * (PACKED ? 2 : 4);
     static bool done[64] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(quantize_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQTile * kQTile * 4);
+    if (smem && (dev < 0 || dev >= 64 || !done[dev])) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(quantize_kernel<F32, PACKED, COL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) done[dev] = true;
     }
     const dim3 grid(static_cast<unsigned>((a.cols + 127) / 128), static_cast<unsigned>((a.rows + 127) / 128));
     note_launch();
-    quantize_kernel<F32><<<grid, kQThreads, smem, st>>>(a);
+    quantize_kernel<F32, PACKED, COL><<<grid, kQThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_quantize(const QuantArgs& a, int f32, cudaStream_t st) {
-    return f32 ? launch<true>(a, st) : launch<false>(a, st);
+    if (f32) return a.qt ? launch<true, false, true>(a, st) : launch<true, false, false>(a, st);
+    if (a.row_mul || a.col_mul) return a.qt ? launch<false, false, true>(a, st) : launch<false, false, false>(a, st);
+    return a.qt ? launch<false, true, true>(a, st) : launch<false, true, false>(a, st);
 }
 
 }  // namespace hm

@@ -270,6 +270,24 @@ def test_quantize(hm, dev, rows, cols, dtype, rowwise, transposed, rf, cf, block
         assert np.array_equal(scales.cpu().numpy(), OX.scale_tile_128x4(osf))
 
 
+def test_quantize_padding_is_positive_zero(hm, dev):
+    """Negative factors leave no negative zeros in the padding of either output."""
+    rng = np.random.default_rng(77)
+    rows, cols = 41, 45
+    x = torch.from_numpy(_spread(rng, rows, cols)).to(dev).to(torch.bfloat16)
+    row, col = -torch.ones(rows, device=dev), -2 * torch.ones(cols, device=dev)
+    for rm, cm in ((row, None), (None, col)):
+        q, s = _poison(dev, rows, 64), _poison(dev, 512)
+        qt, st = _poison(dev, cols, 64), _poison(dev, 512)
+        hm.mxfp8_quantize(x.data_ptr(), hm.HM_BF16, rows, cols, cols, rm.data_ptr() if rm is not None else 0,
+                          cm.data_ptr() if cm is not None else 0, 32, q.data_ptr(), 64, s.data_ptr(), qt.data_ptr(), 64,
+                          st.data_ptr())
+        y = x.float().cpu().numpy() * (-1 if cm is None else -2)
+        oq, _ = OO.quantize(y)
+        oqt, _ = OO.quantize(np.ascontiguousarray(y.T))
+        assert np.array_equal(q.cpu().numpy(), oq) and np.array_equal(qt.cpu().numpy(), oqt)
+
+
 def test_quantize_nan_inf_and_zeros(hm, dev):
     x = torch.zeros(64, 64, device=dev)
     x[0, 0], x[1, 1], x[2, 2] = float("nan"), float("inf"), -float("inf")
