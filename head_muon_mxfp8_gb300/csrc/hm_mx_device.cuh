@@ -31,6 +31,17 @@ __device__ __forceinline__ uint16_t cvt_e4m3x2(float lo, float hi) {
     return r;
 }
 
+// The same rule as the scale's byte e + 127: the biased exponent less 8, at
+// least 0 -- amax below 2^-119, subnormal or zero clamps to e = -127, and an
+// infinity gives e = 120, as above.
+__device__ __forceinline__ int mx_scale_byte(float amax) {
+    return max(static_cast<int>(__float_as_uint(amax) >> 23), 8) - 8;
+}
+// 2^-e for a scale's byte (0 .. 247: a normal fp32).
+__device__ __forceinline__ float mx_inv_of_byte(int byte) {
+    return __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+}
+
 // 2^-e for e in [-127, 119] (always a normal fp32).
 __device__ __forceinline__ float mx_inv_scale(int e) { return __uint_as_float(static_cast<uint32_t>(127 - e) << 23); }
 

@@ -23,32 +23,36 @@ constexpr int kQThreads = 256;
 constexpr int kQTile = 128;
 
 template <bool F32>
-__device__ __forceinline__ void load8(const void* x, int64_t at, int left, bool vec, float (&v)[8]) {
-    // elements at .. at + 7, those from `left` on being zero
+__device__ __forceinline__ void load16(const void* x, int64_t at, int left, bool vec, float (&v)[16]) {
+    // elements at .. at + 15, those from `left` on being zero
     if (F32) {
         const float* p = static_cast<const float*>(x) + at;
-        if (vec && left >= 8) {
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-            const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = k < left ? p[k] : 0.f;
-        }
-    } else {
-        const uint16_t* p = static_cast<const uint16_t*>(x) + at;
-        if (vec && left >= 8) {
-            const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        if (vec && left == 16) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                v[2 * k] = __uint_as_float(w[k] << 16);
-                v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+                const float4 a = __ldcs(reinterpret_cast<const float4*>(p) + k);
+                v[4 * k] = a.x; v[4 * k + 1] = a.y; v[4 * k + 2] = a.z; v[4 * k + 3] = a.w;
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = k < left ? __uint_as_float(static_cast<uint32_t>(p[k]) << 16) : 0.f;
+            for (int k = 0; k < 16; ++k) v[k] = k < left ? p[k] : 0.f;
+        }
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(x) + at;
+        if (vec && left == 16) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p) + j);
+                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
+                    v[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = k < left ? __uint_as_float(static_cast<uint32_t>(p[k]) << 16) : 0.f;
         }
     }
 }
@@ -64,23 +68,26 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// The block's scale exponent from this lane's amax over 8 of its columns.
-__device__ __forceinline__ int row_exponent(float amax, int block) {
+// The block's scale byte from this lane's amax over 16 of its columns.
+__device__ __forceinline__ int row_scale(float amax, int block) {
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     if (block == 128) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
     }
-    return mx_scale_exponent(amax);
+    return mx_scale_byte(amax);
 }
 
-// The tile, in two forms.
+// Row phase: 8 lanes hold a row of the tile, 16 columns each (two lanes per
+// block of 32), a warp 16 rows in four steps whose loads are all issued before
+// the first is used.  16 columns per lane rather than 8: the work per block
+// (exponent, scale, addresses) is shared by more of them; at 8 the kernel
+// issued 20 instructions per element and the issue slots bounded it.
+// The tile, in two forms:
 //   PACKED (bf16 x, no factors): y is x, so the tile stays in bf16 pairs --
 //     half the shared memory and half its traffic, and magnitudes are compared
 //     two at a time; a thread's column work is a pair of columns x 32 rows.
 //   else: y in fp32; a thread's column work is one column x 2 x 32 rows.
-// A thread loads 8 vectors of 8 columns before it uses the first.
 template <bool F32, bool PACKED, bool COL>
 __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_constant__ QuantArgs p) {
     extern __shared__ __align__(16) uint32_t tile[];  // [128][64] bf16 pairs or [128][128] fp32
@@ -91,83 +98,100 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
     const int64_t ct = blockIdx.x, rt = blockIdx.y;
     const int64_t r0 = rt * kQTile, c0 = ct * kQTile;
     const int64_t cols32 = (p.cols + 31) / 32 * 32, rows32 = (p.rows + 31) / 32 * 32;
-    const int c8 = (lane & 15) * 8;
-    const int left = static_cast<int>(min(static_cast<int64_t>(8), max(static_cast<int64_t>(0), p.cols - (c0 + c8))));
-    const int rl0 = warp * 16 + (lane >> 4);  // this lane's rows: rl0 + 2 i
+    const int c16 = (lane & 7) * 16;
+    const int left = static_cast<int>(min(static_cast<int64_t>(16), max(static_cast<int64_t>(0), p.cols - (c0 + c16))));
+    const int rl0 = warp * 16 + (lane >> 3);                                        // this lane's rows: rl0 + 4 i
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kQTile), p.rows - r0));  // of the tile
+    const bool q_live = p.q && c0 + c16 < cols32;
+    const int flip = (lane >> 2) & 1;  // which of its two 16-byte pieces a lane stores first: no bank twice
+    uint8_t* qp = p.q + (r0 + rl0) * p.ldq + c0 + c16;
 
     if constexpr (PACKED) {
-        uint4 raw[8];
+        uint4 raw[4][2];
+        const uint16_t* src = static_cast<const uint16_t*>(p.x) + (r0 + rl0) * p.ldx + c0 + c16;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t r = r0 + rl0 + 2 * i;
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < p.rows && left > 0) {
-                const uint16_t* src = static_cast<const uint16_t*>(p.x) + r * p.ldx + c0 + c8;
-                if (p.vec && left == 8) {
-                    raw[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+        for (int i = 0; i < 4; ++i, src += 4 * p.ldx) {
+            raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (rl0 + 4 * i < rows && left > 0) {
+                if (p.vec && left == 16) {
+                    raw[i][0] = __ldcs(reinterpret_cast<const uint4*>(src));
+                    raw[i][1] = __ldcs(reinterpret_cast<const uint4*>(src) + 1);
                 } else {
-                    uint32_t h[8];
+                    uint32_t h[16];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) h[k] = k < left ? src[k] : 0u;
-                    raw[i] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+                    for (int k = 0; k < 16; ++k) h[k] = k < left ? src[k] : 0u;
+                    raw[i][0] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+                    raw[i][1] = make_uint4(h[8] | (h[9] << 16), h[10] | (h[11] << 16), h[12] | (h[13] << 16), h[14] | (h[15] << 16));
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int rl = rl0 + 2 * i;
-            if (COL) *reinterpret_cast<uint4*>(tile + rl * (kQTile / 2) + c8 / 2) = raw[i];
+        for (int i = 0; i < 4; ++i) {
+            const int rl = rl0 + 4 * i;
+            if (COL) {
+                uint4* t4 = reinterpret_cast<uint4*>(tile + rl * (kQTile / 2) + c16 / 2);
+                t4[flip] = flip ? raw[i][1] : raw[i][0];
+                t4[flip ^ 1] = flip ? raw[i][0] : raw[i][1];
+            }
             if (p.q) {
-                const uint32_t m = max_abs2(max_abs2(max_abs2(max_abs2(0u, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
-                const int e = row_exponent(fmaxf(lo_f32(m), hi_f32(m)), p.block);
-                const float sc = mx_inv_scale(e);
-                const bool live = r0 + rl < p.rows && c0 + c8 < cols32;
-                if (live)
-                    __stcs(reinterpret_cast<uint2*>(p.q + (r0 + rl) * p.ldq + c0 + c8),
-                           make_uint2(codes4(lo_f32(raw[i].x), hi_f32(raw[i].x), lo_f32(raw[i].y), hi_f32(raw[i].y), sc),
-                                      codes4(lo_f32(raw[i].z), hi_f32(raw[i].z), lo_f32(raw[i].w), hi_f32(raw[i].w), sc)));
-                if ((lane & 3) == 0)
-                    s_row[(rl & 31) * 16 + (rl >> 5) * 4 + ((lane & 15) >> 2)] = live ? static_cast<uint8_t>(e + 127) : 0;
+                const uint32_t w[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
+                                       raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
+                uint32_t m = 0u;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m = max_abs2(m, w[k]);
+                const int byte = row_scale(fmaxf(lo_f32(m), hi_f32(m)), p.block);
+                const float sc = mx_inv_of_byte(byte);
+                const bool live = q_live && rl < rows;
+                if (live) {
+                    uint32_t c[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        c[k] = codes4(lo_f32(w[2 * k]), hi_f32(w[2 * k]), lo_f32(w[2 * k + 1]), hi_f32(w[2 * k + 1]), sc);
+                    __stcs(reinterpret_cast<uint4*>(qp + 4 * i * p.ldq), make_uint4(c[0], c[1], c[2], c[3]));
+                }
+                // row rl = rl0 + 4 i of the scale tile: (rl % 32) * 16 + (rl / 32) * 4 + block
+                if (!(lane & 1)) s_row[(rl & 31) * 16 + (rl >> 5) * 4 + ((lane & 7) >> 1)] = live ? static_cast<uint8_t>(byte) : 0;
             }
         }
     } else {
-        float cm[8];
+        float cm[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) cm[k] = p.col_mul && k < left ? p.col_mul[c0 + c8 + k] : 1.f;
-        float v[8][8];
+        for (int k = 0; k < 16; ++k) cm[k] = p.col_mul && k < left ? p.col_mul[c0 + c16 + k] : 1.f;
+        float v[4][16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t r = r0 + rl0 + 2 * i;
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
-            if (r < p.rows && left > 0) load8<F32>(p.x, r * p.ldx + c0 + c8, left, p.vec, v[i]);
+            for (int k = 0; k < 16; ++k) v[i][k] = 0.f;
+            if (rl0 + 4 * i < rows && left > 0) load16<F32>(p.x, (r0 + rl0 + 4 * i) * p.ldx + c0 + c16, left, p.vec, v[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int rl = rl0 + 2 * i;
-            const int64_t r = r0 + rl;
-            if (r < p.rows) {  // outside x the zeros stay +0 whatever the factors' signs
-                const float rm = p.row_mul ? p.row_mul[r] : 1.f;
+        for (int i = 0; i < 4; ++i) {
+            const int rl = rl0 + 4 * i;
+            if (rl < rows) {  // outside x the zeros stay +0 whatever the factors' signs
+                const float rm = p.row_mul ? p.row_mul[r0 + rl] : 1.f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[i][k] = k < left ? v[i][k] * rm * cm[k] : 0.f;
+                for (int k = 0; k < 16; ++k) v[i][k] = k < left ? v[i][k] * rm * cm[k] : 0.f;
             }
             if (COL) {
-                float4* t4 = reinterpret_cast<float4*>(tile + rl * kQTile + c8);
-                t4[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-                t4[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
+                float4* t4 = reinterpret_cast<float4*>(tile + rl * kQTile + c16);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    t4[k] = make_float4(v[i][4 * k], v[i][4 * k + 1], v[i][4 * k + 2], v[i][4 * k + 3]);
             }
             if (p.q) {
                 float amax = 0.f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[i][k]));
-                const int e = row_exponent(amax, p.block);
-                const float sc = mx_inv_scale(e);
-                const bool live = r < p.rows && c0 + c8 < cols32;
-                if (live)
-                    __stcs(reinterpret_cast<uint2*>(p.q + r * p.ldq + c0 + c8),
-                           make_uint2(codes4(v[i][0], v[i][1], v[i][2], v[i][3], sc), codes4(v[i][4], v[i][5], v[i][6], v[i][7], sc)));
-                if ((lane & 3) == 0)
-                    s_row[(rl & 31) * 16 + (rl >> 5) * 4 + ((lane & 15) >> 2)] = live ? static_cast<uint8_t>(e + 127) : 0;
+                for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(v[i][k]));
+                const int byte = row_scale(amax, p.block);
+                const float sc = mx_inv_of_byte(byte);
+                const bool live = q_live && rl < rows;
+                if (live) {
+                    uint32_t c[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) c[k] = codes4(v[i][4 * k], v[i][4 * k + 1], v[i][4 * k + 2], v[i][4 * k + 3], sc);
+                    __stcs(reinterpret_cast<uint4*>(qp + 4 * i * p.ldq), make_uint4(c[0], c[1], c[2], c[3]));
+                }
+                if (!(lane & 1)) s_row[(rl & 31) * 16 + (rl >> 5) * 4 + ((lane & 7) >> 1)] = live ? static_cast<uint8_t>(byte) : 0;
             }
         }
     }
@@ -194,8 +218,8 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
                 a0 = fmaxf(fmaxf(amax_col[0][c], amax_col[1][c]), fmaxf(amax_col[2][c], amax_col[3][c]));
                 a1 = fmaxf(fmaxf(amax_col[0][c + 1], amax_col[1][c + 1]), fmaxf(amax_col[2][c + 1], amax_col[3][c + 1]));
             }
-            const int e0 = mx_scale_exponent(a0), e1 = mx_scale_exponent(a1);
-            const float sc0 = mx_inv_scale(e0), sc1 = mx_inv_scale(e1);
+            const int y0 = mx_scale_byte(a0), y1 = mx_scale_byte(a1);
+            const float sc0 = mx_inv_of_byte(y0), sc1 = mx_inv_of_byte(y1);
             const bool row_live = r0 + b * 32 < rows32;
             const bool live0 = row_live && c0 + c < p.cols, live1 = row_live && c0 + c + 1 < p.cols;
             uint8_t* out = p.qt + (c0 + c) * p.ldqt + r0 + b * 32;
@@ -211,8 +235,8 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
                 if (live0) reinterpret_cast<uint4*>(out)[h] = make_uint4(x[0], x[1], x[2], x[3]);
                 if (live1) reinterpret_cast<uint4*>(out + p.ldqt)[h] = make_uint4(y[0], y[1], y[2], y[3]);
             }
-            s_col[(c & 31) * 16 + (c >> 5) * 4 + b] = live0 ? static_cast<uint8_t>(e0 + 127) : 0;
-            s_col[((c + 1) & 31) * 16 + (c >> 5) * 4 + b] = live1 ? static_cast<uint8_t>(e1 + 127) : 0;
+            s_col[(c & 31) * 16 + (c >> 5) * 4 + b] = live0 ? static_cast<uint8_t>(y0) : 0;
+            s_col[((c + 1) & 31) * 16 + (c >> 5) * 4 + b] = live1 ? static_cast<uint8_t>(y1) : 0;
         } else {
             const float* y = reinterpret_cast<const float*>(tile);
             const int c = threadIdx.x & 127, h = threadIdx.x >> 7;
@@ -234,10 +258,10 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int b = 2 * h + j;
-                const int e = mx_scale_exponent(a[j]);
-                const float sc = mx_inv_scale(e);
+                const int byte = mx_scale_byte(a[j]);
+                const float sc = mx_inv_of_byte(byte);
                 const bool live = col_live && r0 + b * 32 < rows32;
-                s_col[(c & 31) * 16 + (c >> 5) * 4 + b] = live ? static_cast<uint8_t>(e + 127) : 0;
+                s_col[(c & 31) * 16 + (c >> 5) * 4 + b] = live ? static_cast<uint8_t>(byte) : 0;
                 if (!live) continue;
                 uint4* out = reinterpret_cast<uint4*>(p.qt + (c0 + c) * p.ldqt + r0 + b * 32);
 #pragma unroll
