@@ -11,14 +11,19 @@
 #include "hm_internal.h"
 #include "hm_mx_device.cuh"
 #include "hm_ops.h"
+#include "hm_ptx.cuh"
 
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 namespace hm {
 
 namespace {
 
 constexpr int kMaxRowThreads = 512;
+constexpr int kMaxGradStages = 16;
+constexpr int kGradRing = 208 * 1024;  // bytes of rows in flight per SM; a stage is at most 3 x 64 KB
 
 // 8 elements of a row
 template <bool F32>
@@ -30,6 +35,10 @@ struct Vec8<true> {
         const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
         a = __ldcs(p);
         b = __ldcs(p + 1);
+    }
+    __device__ __forceinline__ void lds(const uint8_t* row, int j) {
+        a = reinterpret_cast<const float4*>(row)[2 * j];
+        b = reinterpret_cast<const float4*>(row)[2 * j + 1];
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -49,6 +58,7 @@ struct Vec8<false> {
     __device__ __forceinline__ void load(const void* base, int64_t at) {
         a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
     }
+    __device__ __forceinline__ void lds(const uint8_t* row, int j) { a = reinterpret_cast<const uint4*>(row)[j]; }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -171,63 +181,122 @@ __global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_kernel(const __grid_co
     }
 }
 
-// CTAs take rows round-robin; a thread owns the same columns of every row and
-// keeps their part of dgamma in registers.
-template <bool F32, int V>
-__global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_grad_kernel(const __grid_constant__ RmsGradArgs p) {
-    __shared__ float red[2][16];
+// Gradient: one or two CTAs per SM take rows round-robin; a thread owns the same columns
+// of every row (V vectors of 8, vector i * blockDim + t) and keeps their part of
+// dgamma in registers.  The rows of dy, h and dres come into a ring of `stages`
+// rows in shared memory by bulk copies issued several rows ahead -- loading a row
+// into registers only when its turn came left the memory idle during every
+// reduction (3.6 TB/s at 8192 x 5120 bf16).  One barrier per row: it publishes
+// the warps' sums of t xhat and says that the row has been read, so thread 0
+// refills its stage right behind it.  Waits are bounded (HM_ERR_TIMEOUT).
+template <bool F32>
+__device__ __forceinline__ void fill_stage(const RmsGradArgs& p, uint8_t* stage, uint64_t* bar, int64_t row) {
+    const uint32_t bytes = static_cast<uint32_t>(p.d) * (F32 ? 4 : 2);
+    const int64_t es = F32 ? 4 : 2;
+    mbar_arrive_expect_tx(smem_u32(bar), bytes * (p.dres ? 3 : 2));
+    const uint32_t dst = smem_u32(stage);
+    bulk_load(dst, static_cast<const char*>(p.dy) + row * p.lddy * es, bytes, smem_u32(bar));
+    bulk_load(dst + bytes, static_cast<const char*>(p.h) + row * p.ldh * es, bytes, smem_u32(bar));
+    if (p.dres) bulk_load(dst + 2 * bytes, static_cast<const char*>(p.dres) + row * p.ldh * es, bytes, smem_u32(bar));
+}
+
+// T: most threads, B: CTAs per SM.  gamma stays in registers where they suffice.
+template <bool F32, int V, int T, int B>
+__global__ void __launch_bounds__(T, B) rmsnorm_grad_kernel(const __grid_constant__ RmsGradArgs p) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float red[2][T / 32];
+    __shared__ uint64_t full[kMaxGradStages];
+    __shared__ int bail_word;
+    volatile int* bail = &bail_word;
     const int nv = p.d >> 3;
-    float dg[V][8];
+    const int row_bytes = p.d * (F32 ? 4 : 2);
+    const int stage_bytes = row_bytes * (p.dres ? 3 : 2);
+    const int stages = p.stages;
+    const int64_t mine = (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;  // rows of this CTA
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        bail_word = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int s = 0; s < stages && s < mine; ++s)
+            fill_stage<F32>(p, ring + s * stage_bytes, &full[s], blockIdx.x + static_cast<int64_t>(s) * gridDim.x);
+    constexpr bool kKeepGamma = V == 1 || T * B <= 640;
+    float dg[V][8], gamma[V][8];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+        const int j = i * blockDim.x + threadIdx.x;
+        if (kKeepGamma && j < nv) load_f8(p.gamma + j * 8, gamma[i]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) dg[i][k] = 0.f;
+    }
     const float inv_d = 1.0f / static_cast<float>(p.d);
-    int flip = 0;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    int s = 0;
+    uint32_t ph = 0;
+    float rstd_next = mine > 0 ? __ldg(p.rstd + blockIdx.x) : 0.f;
+    int64_t it = 0;
+    for (; it < mine; ++it) {
+        const int64_t row = blockIdx.x + it * gridDim.x;
+        const float rstd = rstd_next;
+        if (it + 1 < mine) rstd_next = __ldg(p.rstd + row + gridDim.x);
+        const int ok = mbar_wait(smem_u32(&full[s]), ph, p.err, bail);
+        const uint8_t* stage = ring + s * stage_bytes;
         Vec8<F32> dy[V], h[V], dr[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int j = i * blockDim.x + threadIdx.x;
-            if (j < nv) {
-                dy[i].load(p.dy, row * p.lddy + j * 8);
-                h[i].load(p.h, row * p.ldh + j * 8);
-                if (p.dres) dr[i].load(p.dres, row * p.ldh + j * 8);
-            }
-        }
-        const float rstd = p.rstd[row];
-        float t[V][8], xh[V][8];
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int j = i * blockDim.x + threadIdx.x;
             if (j < nv) {
-                float gm[8], y[8];
-                load_f8(p.gamma + j * 8, gm);
+                dy[i].lds(stage, j);
+                h[i].lds(stage + row_bytes, j);
+                if (p.dres) dr[i].lds(stage + 2 * row_bytes, j);
+                float y[8], x[8];
+                if (!kKeepGamma) load_f8(p.gamma + j * 8, gamma[i]);
                 dy[i].get(y);
-                h[i].get(xh[i]);
+                h[i].get(x);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    xh[i][k] *= rstd;
-                    dg[i][k] = fmaf(y[k], xh[i][k], dg[i][k]);
-                    t[i][k] = y[k] * gm[k];
-                    dot = fmaf(t[i][k], xh[i][k], dot);
+                    const float yx = y[k] * (x[k] * rstd);
+                    dg[i][k] += yx;
+                    dot = fmaf(yx, gamma[i][k], dot);
                 }
             }
         }
-        const float mean = block_sum(dot, red[flip]) * inv_d;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if ((threadIdx.x & 31) == 0) red[it & 1][threadIdx.x >> 5] = dot;
+        if (!__syncthreads_and(ok)) break;
+        if (threadIdx.x == 0 && it + stages < mine)
+            fill_stage<F32>(p, ring + s * stage_bytes, &full[s], row + static_cast<int64_t>(stages) * gridDim.x);
+        if (++s == stages) { s = 0; ph ^= 1u; }
+        // every warp adds the warps' sums the same way: lane k holds warp k's
+        float mean = (threadIdx.x & 31) < (blockDim.x >> 5) ? red[it & 1][threadIdx.x & 31] : 0.f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+        const float back = -rstd * (mean * inv_d);  // dx = dres + rstd t - xhat rstd mean
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int j = i * blockDim.x + threadIdx.x;
             if (j < nv) {
-                float o[8], rv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                float y[8], x[8], o[8], rv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (!kKeepGamma) load_f8(p.gamma + j * 8, gamma[i]);
+                dy[i].get(y);
+                h[i].get(x);
                 if (p.dres) dr[i].get(rv);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] = fmaf(rstd, t[i][k] - xh[i][k] * mean, rv[k]);
+                for (int k = 0; k < 8; ++k) o[k] = fmaf(x[k] * rstd, back, fmaf(y[k] * gamma[i][k], rstd, rv[k]));
                 Vec8<F32>::put(p.dx, row * p.ldh + j * 8, o);
             }
         }
     }
+    // after a wait that gave up: this CTA's copies still in flight
+    if (it < mine && threadIdx.x == 0)
+        for (int k = 0; k < stages; ++k) {
+            const int64_t i = it + k;
+            if (i >= mine) break;
+            mbar_wait(smem_u32(&full[i % stages]), static_cast<uint32_t>(i / stages) & 1u, p.err, bail, false);
+        }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int j = i * blockDim.x + threadIdx.x;
@@ -239,21 +308,22 @@ __global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_grad_kernel(const __gr
     }
 }
 
-// dgamma from the CTAs' partials: 32 columns per CTA, 16 threads per column each
-// adding every 16th partial in order, then the 16 in order.
-__global__ void __launch_bounds__(512) dgamma_kernel(const float* __restrict__ partials, int parts, int d,
-                                                     int accumulate, float* __restrict__ dgamma) {
-    __shared__ float red[16][33];
+// dgamma from the CTAs' partials: 32 columns per CTA, 32 threads per column each
+// adding every 32nd partial in order, then the 32 in order.
+__global__ void __launch_bounds__(1024) dgamma_kernel(const float* __restrict__ partials, int parts, int d,
+                                                      int accumulate, float* __restrict__ dgamma) {
+    __shared__ float red[32][33];
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + c;
     float s = 0.f;
-    for (int k = g; k < parts; k += 16) s += partials[static_cast<int64_t>(k) * d + col];
+#pragma unroll 10
+    for (int k = g; k < parts; k += 32) s += partials[static_cast<int64_t>(k) * d + col];
     red[g][c] = s;
     __syncthreads();
     if (g == 0) {
         float t = 0.f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) t += red[k][c];
+        for (int k = 0; k < 32; ++k) t += red[k][c];
         dgamma[col] = accumulate ? dgamma[col] + t : t;
     }
 }
@@ -272,20 +342,45 @@ cudaError_t launch_fwd(const RmsArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <bool F32, int V, int T, int B>
+cudaError_t launch_grad(RmsGradArgs a, int parts, int stage, cudaStream_t st) {
+    constexpr int ring = kGradRing / B;
+    a.stages = std::min(kMaxGradStages, ring / stage);
+    static bool done[64] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(rmsnorm_grad_kernel<F32, V, T, B>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+    const int threads = ((a.d / 8 + V - 1) / V + 31) / 32 * 32;
+    note_launch();
+    rmsnorm_grad_kernel<F32, V, T, B><<<parts, threads, a.stages * stage, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <bool F32>
-cudaError_t launch_bwd(const RmsGradArgs& a, cudaStream_t st) {
-    const int parts = rmsnorm_grad_parts(a.rows, a.d);
+cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
+    RmsGradArgs a = a0;
+    a.err = device_error_word();
+    // Two CTAs per SM where half the ring still holds two rows: one computes while
+    // the other stands at its barrier (8192 x 5120 bf16: 71 us with one, {TWO} with two).
+    const int stage = a.d * (F32 ? 4 : 2) * (a.dres ? 3 : 2);
+    const bool two = a.d <= 8192 && 2 * stage <= kGradRing / 2;
+    const int most = rmsnorm_grad_parts(a.rows, a.d);
+    const int parts = two ? most : std::min(most, device_sm_count());
     if (parts) {
-        const int v = row_vectors(a.d), threads = row_threads(a.d, v);
-        note_launch();
-        if (v == 1) rmsnorm_grad_kernel<F32, 1><<<parts, threads, 0, st>>>(a);
-        else if (v == 2) rmsnorm_grad_kernel<F32, 2><<<parts, threads, 0, st>>>(a);
-        else rmsnorm_grad_kernel<F32, 4><<<parts, threads, 0, st>>>(a);
-        const cudaError_t e = cudaGetLastError();
+        cudaError_t e;
+        if (a.d <= 4096) e = two ? launch_grad<F32, 1, 512, 2>(a, parts, stage, st) : launch_grad<F32, 1, 512, 1>(a, parts, stage, st);
+        else if (a.d <= 5120 && two) e = launch_grad<F32, 2, 320, 2>(a, parts, stage, st);
+        else if (a.d <= 8192) e = two ? launch_grad<F32, 2, 512, 2>(a, parts, stage, st) : launch_grad<F32, 2, 512, 1>(a, parts, stage, st);
+        else e = launch_grad<F32, 2, 1024, 1>(a, parts, stage, st);
         if (e != cudaSuccess) return e;
     }
     note_launch();
-    dgamma_kernel<<<a.d / 32, 512, 0, st>>>(a.partials, parts, a.d, a.accumulate, a.dgamma);
+    dgamma_kernel<<<a.d / 32, 1024, 0, st>>>(a.partials, parts, a.d, a.accumulate, a.dgamma);
     return cudaGetLastError();
 }
 

@@ -67,6 +67,8 @@ struct RmsGradArgs {
     const float* rstd;
     float* dgamma;
     float* partials;     // [CTAs][d]
+    int32_t stages;      // rows in flight per CTA (set by launch_rmsnorm_grad, as err)
+    int32_t* err;
 };
 // CTAs (= partial rows of dgamma) that launch_rmsnorm_grad uses, at most
 int rmsnorm_grad_parts(int64_t rows, int64_t d);
