@@ -7,12 +7,18 @@
 // after the last whole vector, so any element alignment runs on vector loads.
 // A thread adds the squares of one chunk's 16 vectors in fp32 and carries its
 // sum from chunk to chunk in double; CTA sums are doubles too, added in a fixed
-// order.  A thread's fp32 sum that overflowed or may have underflowed (squares
+// order.  Two launches: the norm pass, and a pass that adds the CTA sums (every CTA
+// the same way) and scales.  The second pass has to read the gradient again; it
+// walks the chunks backwards, and the norm pass marks all but the last ones
+// (as much as half the L2 holds) evict-first, so those come from the L2.
+// A thread's fp32 sum that overflowed or may have underflowed (squares
 // leave fp32 for |g| > 2^63 or < 2^-63) is formed again in double.
 #include "hm_internal.h"
 #include "hm_ops.h"
 
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 namespace hm {
 
@@ -100,7 +106,7 @@ __device__ __noinline__ double squares_in_double(const uint4* src, int nv) {
 }
 
 template <bool F32>
-__device__ __forceinline__ double chunk_squares(const uint4* src, int nv) {
+__device__ __forceinline__ double chunk_squares(const uint4* src, int nv, bool keep) {
     float s = 0.f;
     uint32_t bits = 0;
     for (int i0 = threadIdx.x; i0 < nv; i0 += kClipUnroll * kClipThreads) {
@@ -108,7 +114,7 @@ __device__ __forceinline__ double chunk_squares(const uint4* src, int nv) {
 #pragma unroll
         for (int u = 0; u < kClipUnroll; ++u) {
             const int i = i0 + u * kClipThreads;
-            x[u] = i < nv ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+            x[u] = i >= nv ? make_uint4(0u, 0u, 0u, 0u) : keep ? __ldcg(src + i) : __ldcs(src + i);
         }
 #pragma unroll
         for (int u = 0; u < kClipUnroll; ++u) add_squares<F32>(x[u], s, bits);
@@ -137,7 +143,8 @@ __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_co
         const ClipTensor& t = a.t[find_tensor(a, ch)];
         const Place c = place_of(t, ch);
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(t.src) + c.head * (t.f32 ? 4 : 2)) + c.v0;
-        sum += t.f32 ? chunk_squares<true>(src, c.nv) : chunk_squares<false>(src, c.nv);
+        const bool keep = ch >= a.keep_from;
+        sum += t.f32 ? chunk_squares<true>(src, c.nv, keep) : chunk_squares<false>(src, c.nv, keep);
         if (c.first && threadIdx.x < c.head) {
             const double v = one_value(t, threadIdx.x);
             sum += v * v;
@@ -177,7 +184,8 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
     }
     __syncthreads();
     const float coef = s_coef;
-    for (int ch = blockIdx.x; ch < a.chunks; ch += gridDim.x) {
+    for (int k = blockIdx.x; k < a.chunks; k += gridDim.x) {
+        const int ch = a.chunks - 1 - k;  // the chunks the norm pass read last are still in the L2
         const ClipTensor& t = a.t[find_tensor(a, ch)];
         if (!t.dst || (t.dst == t.src && coef == 1.f)) continue;
         const Place c = place_of(t, ch);
@@ -233,7 +241,8 @@ int clip_parts(int chunks) {
     return chunks < most ? chunks : most;
 }
 
-cudaError_t launch_clip_norm(const ClipArgs& a, cudaStream_t st) {
+cudaError_t launch_clip_norm(ClipArgs& a, cudaStream_t st) {
+    a.keep_from = static_cast<int32_t>(std::max<int64_t>(0, a.chunks - device_l2_bytes() / 2 / (kChunkVecs * 16)));
     note_launch();
     clip_norm_kernel<<<clip_parts(a.chunks), kClipThreads, 0, st>>>(a);
     return cudaGetLastError();

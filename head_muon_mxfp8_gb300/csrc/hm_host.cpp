@@ -760,7 +760,8 @@ hm_status refresh_steps(const hm_muon_plan* p, const hm_muon_hparams* hp, cudaSt
 }  // namespace
 
 // L2 size of the current device (cached per device).
-static int64_t device_l2_bytes() {
+namespace hm {
+int64_t device_l2_bytes() {
     static int cached[64] = {0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 128 << 20;
@@ -771,6 +772,8 @@ static int64_t device_l2_bytes() {
     }
     return cached[dev];
 }
+}  // namespace hm
+using hm::device_l2_bytes;
 
 extern "C" hm_status muon_update_units(const hm_muon_plan* p, const hm_muon_bufs* b, const hm_muon_hparams* hp,
                                        void* workspace, size_t workspace_bytes, int stages, void* stream) {

@@ -180,6 +180,7 @@ constexpr int kRelayoutDst16 = 2;     // dst + dst offset is 16-byte aligned: on
 void note_launch();
 int64_t launches_issued();
 int device_sm_count();
+int64_t device_l2_bytes();
 
 // Grid of a grid-stride kernel: every CTA resident at once (SM count x the
 // CTAs per SM that the kernel's registers, shared memory and block size

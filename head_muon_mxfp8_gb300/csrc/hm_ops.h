@@ -88,6 +88,8 @@ struct ClipArgs {
     int32_t chunks;
     int32_t parts;       // partial sums of every launch of the call together
     int32_t part0;       // this launch's first one
+    int32_t keep_from;   // norm pass: chunks from here on stay in the L2 (set by launch_clip_norm)
+    int32_t pad;
     float max_norm, eps;
     float* stats;
     double* partials;
@@ -95,7 +97,7 @@ struct ClipArgs {
 };
 int clip_chunks(const void* src, int64_t n, int f32);  // of one tensor with n > 0
 int clip_parts(int chunks);            // partial sums of one launch
-cudaError_t launch_clip_norm(const ClipArgs& a, cudaStream_t st);
+cudaError_t launch_clip_norm(ClipArgs& a, cudaStream_t st);
 cudaError_t launch_clip_scale(const ClipArgs& a, cudaStream_t st);
 
 }  // namespace hm
