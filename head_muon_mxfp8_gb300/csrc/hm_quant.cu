@@ -13,8 +13,6 @@
 #include "hm_mx_device.cuh"
 #include "hm_ops.h"
 
-#include <cuda_bf16.h>
-
 namespace hm {
 
 namespace {
@@ -62,10 +60,36 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
 }
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-// elementwise max of magnitudes of two bf16 pairs (a NaN is left out, as by fmaxf)
+// Elementwise max of the magnitudes of two bf16 pairs, up to the sign bits (a
+// NaN is left out, as by fmaxf).
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
-    return *reinterpret_cast<const uint32_t*>(&m);
+    uint32_t m;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+// 2^-e as bf16 for a scale's byte, and the product with it: a power of two, so
+// exact wherever the result is not far below the smallest code.
+__device__ __forceinline__ uint32_t inv_of_byte_bf16(int byte) { return static_cast<uint32_t>(254 - byte) << 7; }
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+__device__ __forceinline__ uint32_t join(uint16_t lo, uint16_t hi) {
+    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// qt's tile leaves through shared memory, [128 columns][128 codes], so that a
+// warp stores four whole lines: stored straight from the column phase, 32 bytes
+// of 32 rows at a time, the transposed output took 36 of 102 us as two 16-byte
+// halves per sector and 25 as one sector per lane.  16-byte piece k of column c
+// sits at piece k ^ key(c): no bank twice, whether lanes hold consecutive
+// columns or every other one.
+__device__ __forceinline__ int stage_key(int c) { return (c + (c >> 3)) & 7; }
+__device__ __forceinline__ void stage_codes32(uint4* stage, int c, int b, const uint32_t (&x)[8]) {
+    const int k = stage_key(c);
+    stage[c * 8 + ((2 * b) ^ k)] = make_uint4(x[0], x[1], x[2], x[3]);
+    stage[c * 8 + ((2 * b + 1) ^ k)] = make_uint4(x[4], x[5], x[6], x[7]);
 }
 
 // The block's scale byte from this lane's amax over 16 of its columns.
@@ -139,14 +163,16 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
                 uint32_t m = 0u;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) m = max_abs2(m, w[k]);
-                const int byte = row_scale(fmaxf(lo_f32(m), hi_f32(m)), p.block);
-                const float sc = mx_inv_of_byte(byte);
+                const int byte = row_scale(fmaxf(fabsf(lo_f32(m)), fabsf(hi_f32(m))), p.block);
+                const uint32_t sc = inv_of_byte_bf16(byte) * 0x10001u;
                 const bool live = q_live && rl < rows;
                 if (live) {
                     uint32_t c[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        c[k] = codes4(lo_f32(w[2 * k]), hi_f32(w[2 * k]), lo_f32(w[2 * k + 1]), hi_f32(w[2 * k + 1]), sc);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t y0 = mul2(w[2 * k], sc), y1 = mul2(w[2 * k + 1], sc);
+                        c[k] = join(cvt_e4m3x2(lo_f32(y0), hi_f32(y0)), cvt_e4m3x2(lo_f32(y1), hi_f32(y1)));
+                    }
                     __stcs(reinterpret_cast<uint4*>(qp + 4 * i * p.ldq), make_uint4(c[0], c[1], c[2], c[3]));
                 }
                 // row rl = rl0 + 4 i of the scale tile: (rl % 32) * 16 + (rl / 32) * 4 + block
@@ -210,7 +236,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
             for (int k = 0; k < 32; ++k) w[k] = tile[(b * 32 + k) * (kQTile / 2) + cp];
 #pragma unroll
             for (int k = 0; k < 32; ++k) m = max_abs2(m, w[k]);
-            float a0 = lo_f32(m), a1 = hi_f32(m);
+            float a0 = fabsf(lo_f32(m)), a1 = fabsf(hi_f32(m));
             if (p.block == 128) {
                 amax_col[b][c] = a0;
                 amax_col[b][c + 1] = a1;
@@ -219,22 +245,21 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
                 a1 = fmaxf(fmaxf(amax_col[0][c + 1], amax_col[1][c + 1]), fmaxf(amax_col[2][c + 1], amax_col[3][c + 1]));
             }
             const int y0 = mx_scale_byte(a0), y1 = mx_scale_byte(a1);
-            const float sc0 = mx_inv_of_byte(y0), sc1 = mx_inv_of_byte(y1);
+            const uint32_t sc = inv_of_byte_bf16(y0) | (inv_of_byte_bf16(y1) << 16);
             const bool row_live = r0 + b * 32 < rows32;
             const bool live0 = row_live && c0 + c < p.cols, live1 = row_live && c0 + c + 1 < p.cols;
-            uint8_t* out = p.qt + (c0 + c) * p.ldqt + r0 + b * 32;
+            uint32_t x[8], y[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t x[4], y[4];
+            for (int k = 0; k < 8; ++k) {
+                uint32_t z[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t* q = w + 16 * h + 4 * k;
-                    x[k] = codes4(lo_f32(q[0]), lo_f32(q[1]), lo_f32(q[2]), lo_f32(q[3]), sc0);
-                    y[k] = codes4(hi_f32(q[0]), hi_f32(q[1]), hi_f32(q[2]), hi_f32(q[3]), sc1);
-                }
-                if (live0) reinterpret_cast<uint4*>(out)[h] = make_uint4(x[0], x[1], x[2], x[3]);
-                if (live1) reinterpret_cast<uint4*>(out + p.ldqt)[h] = make_uint4(y[0], y[1], y[2], y[3]);
+                for (int g = 0; g < 4; ++g) z[g] = mul2(w[4 * k + g], sc);
+                x[k] = join(cvt_e4m3x2(lo_f32(z[0]), lo_f32(z[1])), cvt_e4m3x2(lo_f32(z[2]), lo_f32(z[3])));
+                y[k] = join(cvt_e4m3x2(hi_f32(z[0]), hi_f32(z[1])), cvt_e4m3x2(hi_f32(z[2]), hi_f32(z[3])));
             }
+            __syncthreads();  // the tile has been read
+            stage_codes32(reinterpret_cast<uint4*>(tile), c, b, x);
+            stage_codes32(reinterpret_cast<uint4*>(tile), c + 1, b, y);
             s_col[(c & 31) * 16 + (c >> 5) * 4 + b] = live0 ? static_cast<uint8_t>(y0) : 0;
             s_col[((c + 1) & 31) * 16 + (c >> 5) * 4 + b] = live1 ? static_cast<uint8_t>(y1) : 0;
         } else {
@@ -255,6 +280,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
                 __syncthreads();
                 a[0] = a[1] = fmaxf(amax_col[0][c], amax_col[1][c]);
             }
+            __syncthreads();  // the tile has been read
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int b = 2 * h + j;
@@ -262,21 +288,23 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
                 const float sc = mx_inv_of_byte(byte);
                 const bool live = col_live && r0 + b * 32 < rows32;
                 s_col[(c & 31) * 16 + (c >> 5) * 4 + b] = live ? static_cast<uint8_t>(byte) : 0;
-                if (!live) continue;
-                uint4* out = reinterpret_cast<uint4*>(p.qt + (c0 + c) * p.ldqt + r0 + b * 32);
+                uint32_t x[8];
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t x[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float* q = w[j] + 16 * g + 4 * k;
-                        x[k] = codes4(q[0], q[1], q[2], q[3], sc);
-                    }
-                    out[g] = make_uint4(x[0], x[1], x[2], x[3]);
+                for (int k = 0; k < 8; ++k) {
+                    const float* q = w[j] + 4 * k;
+                    x[k] = codes4(q[0], q[1], q[2], q[3], sc);
                 }
+                stage_codes32(reinterpret_cast<uint4*>(tile), c, b, x);
             }
         }
         __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = k * 32 + (threadIdx.x >> 3), piece = threadIdx.x & 7;
+            if (c0 + c < p.cols && r0 + piece * 16 < rows32)
+                __stcs(reinterpret_cast<uint4*>(p.qt + (c0 + c) * p.ldqt + r0) + piece,
+                       reinterpret_cast<const uint4*>(tile)[c * 8 + (piece ^ stage_key(c))]);
+        }
         if (threadIdx.x < 32) {
             const int64_t row_tiles = (rows32 + 127) / 128;
             reinterpret_cast<uint4*>(p.st + (ct * row_tiles + rt) * 512)[threadIdx.x] = reinterpret_cast<const uint4*>(s_col)[threadIdx.x];
