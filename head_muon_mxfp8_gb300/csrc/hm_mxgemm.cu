@@ -107,32 +107,37 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 // instruction touched 32 lines: adding a 256 x 192 fp32 tile to D took 16,000
 // clocks instead of the 4,100 of a 1024-long chunk of its products.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void store_chunk(const MxGemmArgs& p, int i, int j0, const uint32_t (&r)[32]) {
-    if (i >= p.n || j0 >= p.m) return;
-    if (j0 + 32 > p.m) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j0 + j < p.m) store_one(p, j0 + j, i, __uint_as_float(r[j]));
-        return;
-    }
+template <bool TAIL>
+__device__ __forceinline__ void store_rows(const MxGemmArgs& p, int i, int j0, const uint32_t (&r)[32]) {
+    const int rows = p.m - j0;  // TAIL: fewer than 32
     const int64_t at = static_cast<int64_t>(j0) * p.ldd + i;
     if (!p.d_f32) {
         uint16_t* d = static_cast<uint16_t*>(p.d) + at;
 #pragma unroll
-        for (int j = 0; j < 32; ++j, d += p.ldd) *d = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j])));
-    } else if (!p.accumulate) {
-        float* d = static_cast<float*>(p.d) + at;
-#pragma unroll
-        for (int j = 0; j < 32; ++j, d += p.ldd) *d = __uint_as_float(r[j]);
-    } else {
-        float* d = static_cast<float*>(p.d) + at;
-        float old[32];
-        const float* o = d;
-#pragma unroll
-        for (int j = 0; j < 32; ++j, o += p.ldd) old[j] = *o;
-#pragma unroll
-        for (int j = 0; j < 32; ++j, d += p.ldd) *d = old[j] + __uint_as_float(r[j]);
+        for (int j = 0; j < 32; ++j, d += p.ldd)
+            if (!TAIL || j < rows) *d = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j])));
+        return;
     }
+    float* d = static_cast<float*>(p.d) + at;
+    constexpr int kBatch = TAIL ? 8 : 32;  // a batch's loads before its first store (the tail's short ones save registers)
+#pragma unroll
+    for (int b = 0; b < 32; b += kBatch) {
+        float old[kBatch];
+        if (p.accumulate) {
+            const float* o = d;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j, o += p.ldd) old[j] = !TAIL || b + j < rows ? *o : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j, d += p.ldd)
+            if (!TAIL || b + j < rows) *d = p.accumulate ? old[j] + __uint_as_float(r[b + j]) : __uint_as_float(r[b + j]);
+    }
+}
+
+__device__ __forceinline__ void store_chunk(const MxGemmArgs& p, int i, int j0, const uint32_t (&r)[32]) {
+    if (i >= p.n || j0 >= p.m) return;
+    if (j0 + 32 <= p.m) store_rows<false>(p, i, j0, r);
+    else store_rows<true>(p, i, j0, r);
 }
 
 // ---------------------------------------------------------------------------
@@ -435,10 +440,44 @@ struct SplitCfg {
     static_assert(STAGES * (kPBytes + Q_BYTES) >= BN * 128 * 4, "the ring holds the partial tile");
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
+}
+
+// Four neighbours of one row of D.
+__device__ __forceinline__ void store_four(const MxGemmArgs& p, int row, int col, const float4& v) {
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    const int64_t at = static_cast<int64_t>(row) * p.ldd + col;
+    const bool whole = col + 4 <= p.n;
+    if (p.d_f32) {
+        float* d = static_cast<float*>(p.d) + at;
+        const bool vec = whole && (reinterpret_cast<uintptr_t>(d) & 15) == 0;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.accumulate) {
+            if (vec) o = *reinterpret_cast<const float4*>(d);
+            else o = make_float4(col < p.n ? d[0] : 0.f, col + 1 < p.n ? d[1] : 0.f, col + 2 < p.n ? d[2] : 0.f,
+                                 col + 3 < p.n ? d[3] : 0.f);
+        }
+        const float y[4] = {p.accumulate ? o.x + x[0] : x[0], p.accumulate ? o.y + x[1] : x[1],
+                            p.accumulate ? o.z + x[2] : x[2], p.accumulate ? o.w + x[3] : x[3]};
+        if (vec) *reinterpret_cast<float4*>(d) = make_float4(y[0], y[1], y[2], y[3]);
+        else
+            for (int k = 0; k < 4; ++k)
+                if (col + k < p.n) d[k] = y[k];
+    } else {
+        uint16_t* d = static_cast<uint16_t*>(p.d) + at;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+        const uint32_t w[2] = {*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)};
+        if (whole && (reinterpret_cast<uintptr_t>(d) & 7) == 0) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+        else
+            for (int k = 0; k < 4; ++k)
+                if (col + k < p.n) d[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+    }
 }
 
 template <int BN>
@@ -553,11 +592,14 @@ __global__ void __launch_bounds__(kSplitThreads)
                 tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, r);
                 tmem_ld_wait();
                 tmem_ld_pin(r);
+                if (ck == 1) {
+                    store_chunk(p, col, row0 + c0, r);
+                    continue;
+                }
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     if (c0 + j >= rows) break;
-                    if (ck > 1) part[(c0 + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
-                    else if (col < p.n) store_one(p, row0 + c0 + j, col, __uint_as_float(r[j]));
+                    part[(c0 + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
                 }
             }
         }
@@ -565,13 +607,27 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
     if (ck > 1) {
         cluster_sync_all();
-        // rows of D dealt round-robin over the cluster; every part in rank order
-        if (warp >= 2 && col < p.n) {
-            const uint32_t mine = smem_u32(part) + static_cast<uint32_t>(q * 32 + lane) * 4;
-            for (int c = rank; c < rows; c += ck) {
-                float v = 0.f;
-                for (int k = 0; k < ck; ++k) v += ld_cluster_f32(mapa_shared(mine + c * 512, k));
-                store_one(p, row0 + c, col, v);
+        // rows of D dealt round-robin over the cluster and its CTAs' warps; a lane adds four
+        // columns, every part in rank order, all of a row's parts loaded before the first
+        // addition and two rows at a time
+        const uint32_t mine = smem_u32(part) + static_cast<uint32_t>(lane) * 16;
+        const int col4 = tp * kTileP + lane * 4;
+        const int first = rank + warp * ck, step = ck * (kSplitThreads / 32);
+        for (int c = first; c < rows; c += 2 * step) {
+            float4 x[2][8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < ck && c + h * step < rows) x[h][k] = ld_cluster_f4(mapa_shared(mine + (c + h * step) * 512, k));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (c + h * step >= rows || col4 >= p.n) continue;
+                float4 v = x[h][0];
+#pragma unroll
+                for (int k = 1; k < 8; ++k)
+                    if (k < ck) v = make_float4(v.x + x[h][k].x, v.y + x[h][k].y, v.z + x[h][k].z, v.w + x[h][k].w);
+                store_four(p, row0 + c + h * step, col4, v);
             }
         }
         cluster_sync_all();  // a CTA's part stays until its peers have read it
@@ -630,6 +686,14 @@ cudaError_t allow_smem(Kernel kernel, int bytes, bool (&done)[64]) {
     return cudaSuccess;
 }
 
+// CTAs of a cluster that share a tile's K: enough for two CTAs per SM, at least
+// two stages each.
+int split_for(int64_t tiles, int num_kb) {
+    int split = 1;
+    while (split < 8 && 2 * split * tiles <= 2 * device_sm_count() && 4 * split <= num_kb) split *= 2;
+    return split;
+}
+
 template <int BN>
 cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, MxGemmArgs p, cudaStream_t st) {
     using C = SplitCfg<BN>;
@@ -639,9 +703,7 @@ cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_
     CUtensorMap ma, mb;
     if (!map_codes(&ma, a, p.k, p.m, lda, BN) || !map_codes(&mb, b, p.k, p.n, ldb, kTileP)) return cudaErrorUnknown;
     const int tiles_p = (p.n + kTileP - 1) / kTileP, tiles_q = (p.m + BN - 1) / BN;
-    // enough CTAs for two per SM, at least two stages each
-    int split = 1;
-    while (split < 8 && 2 * split * tiles_p * tiles_q <= 2 * device_sm_count() && 4 * split <= p.num_kb) split *= 2;
+    const int split = split_for(static_cast<int64_t>(tiles_p) * tiles_q, p.num_kb);
     p.split = split;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles_p * split, tiles_q, 1);
@@ -722,13 +784,20 @@ cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int6
     const bool sums = p.d_f32 && p.num_kb > kChunkK / kTileK;
     const int64_t pairs = device_sm_count() / 2;
     int best = 0;
-    int64_t least = 0;
+    double least = 0;
     for (const int bn : {256, 192, 128}) {
         if (bn > 192 && sums) continue;
         const int64_t tiles = static_cast<int64_t>((p.n + 255) / 256) * ((p.m + bn - 1) / bn);
-        const int64_t cost = (tiles + pairs - 1) / pairs * (256 + bn);
+        const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * p.num_kb * (256 + bn) * (0.37 / 512);
         if (!best || cost < least) best = bn, least = cost;
     }
+    // Too few tiles for the pairs: 128 x 128 tiles with K split over clusters, about
+    // 0.32 us per stage of every CTA an SM gets and 3 us for adding the parts.
+    const int64_t small = static_cast<int64_t>((p.n + 127) / 128) * ((p.m + 127) / 128);
+    const int split = split_for(small, p.num_kb);
+    const double split_cost =
+        static_cast<double>((small * split + 2 * pairs - 1) / (2 * pairs)) * ((p.num_kb + split - 1) / split) * 0.32 + 3.0;
+    if (split_cost < least && small <= 65535) return launch_split<128>(a, lda, b, ldb, p, st);
     if (best == 256) return launch_pair_of<256>(a, lda, b, ldb, p, st);
     if (best == 192) return launch_pair_of<192>(a, lda, b, ldb, p, st);
     return launch_pair_of<128>(a, lda, b, ldb, p, st);
