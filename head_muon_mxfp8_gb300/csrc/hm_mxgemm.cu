@@ -13,7 +13,7 @@
 //   mx_gemm_pair_kernel   persistent CTA pairs, tiles of 256 x 128 to 256.
 //   mx_gemm_split_kernel  few rows of A: B's rows take the M side (128 lanes),
 //                    A's rows the N side (16 to 128 columns), and K is split
-//                    over the CTAs of a cluster that add their parts through
+//                    over the CTAs of a cluster (2 to 8) that add their parts through
 //                    distributed shared memory in rank order.
 // Every wait is bounded as in the Newton-Schulz kernels (HM_ERR_TIMEOUT in the
 // device error word).
@@ -23,6 +23,10 @@
 #include "hm_ptx.cuh"
 
 #include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
 
 namespace hm {
 
@@ -428,15 +432,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // of D and a warp's stores of one row of D are contiguous at any alignment.
 // ---------------------------------------------------------------------------
 constexpr int kSplitThreads = 192;
+constexpr double kStageUs = 0.3;
+constexpr int kMaxSplit = 8;
+constexpr int kSplitSumKb = 20;  // K = 2560
 
 template <int BN>
 struct SplitCfg {
     static constexpr int Q_BYTES = BN * kTileK;
-    // two CTAs per SM: up to 113 KB each
+    // two CTAs per SM, so that one's start and reduction overlap the other's loads: with
+    // the whole shared memory for one CTA's ring, 160 tiles at 1 x 20480 x 5120 took
+    // 28.9 us instead of 18.5
     static constexpr int STAGES = BN <= 32 ? 5 : BN == 64 ? 4 : 3;
     static constexpr int SMEM = STAGES * (kPBytes + Q_BYTES + 2 * kSfBytes) + 1024 + 256;
     static constexpr int ACC = BN < 32 ? 32 : BN;
     static constexpr int TMEM = ACC <= 32 ? 64 : 2 * ACC;  // accumulator and two slots of 8 scale columns
+    static_assert(2 * (SMEM + 1024) <= 233472 && 2 * TMEM <= 512, "two CTAs per SM");
     static_assert(STAGES * (kPBytes + Q_BYTES) >= BN * 128 * 4, "the ring holds the partial tile");
 };
 
@@ -480,8 +490,43 @@ __device__ __forceinline__ void store_four(const MxGemmArgs& p, int row, int col
     }
 }
 
+// The sum of a cluster's CK parts: D's rows are dealt round-robin over the CTAs
+// and their warps; a lane adds four columns, every part in rank order.  A warp
+// takes 16 / CK rows at a time, so that each lane has 16 loads from the peers'
+// shared memory in flight (with two rows at a time the latency of those loads
+// made a split in two slower than none: 16.4 us against 14.5 at 355 x 3149 x
+// 4704).
+template <int CK>
+__device__ __forceinline__ void add_parts(const MxGemmArgs& p, const float* part, int rank, int warp, int lane, int col0,
+                                          int row0, int rows) {
+    constexpr int U = 16 / CK;
+    const uint32_t mine = smem_u32(part) + static_cast<uint32_t>(lane) * 16;
+    const int col = col0 + lane * 4;
+    const int step = CK * (kSplitThreads / 32);
+    uint32_t from[CK];
+#pragma unroll
+    for (int k = 0; k < CK; ++k) from[k] = mapa_shared(mine, k);
+    for (int c = rank + warp * CK; c < rows; c += U * step) {
+        float4 x[U][CK];
+#pragma unroll
+        for (int h = 0; h < U; ++h)
+#pragma unroll
+            for (int k = 0; k < CK; ++k)
+                if (c + h * step < rows) x[h][k] = ld_cluster_f4(from[k] + (c + h * step) * 512);
+#pragma unroll
+        for (int h = 0; h < U; ++h) {
+            if (c + h * step >= rows || col >= p.n) continue;
+            float4 v = x[h][0];
+#pragma unroll
+            for (int k = 1; k < CK; ++k)
+                v = make_float4(v.x + x[h][k].x, v.y + x[h][k].y, v.z + x[h][k].z, v.w + x[h][k].w);
+            store_four(p, row0 + c + h * step, col, v);
+        }
+    }
+}
+
 template <int BN>
-__global__ void __launch_bounds__(kSplitThreads)
+__global__ void __launch_bounds__(kSplitThreads, 1)
     mx_gemm_split_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
                          const __grid_constant__ MxGemmArgs p) {
     using C = SplitCfg<BN>;
@@ -607,28 +652,15 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
     if (ck > 1) {
         cluster_sync_all();
-        // rows of D dealt round-robin over the cluster and its CTAs' warps; a lane adds four
-        // columns, every part in rank order, all of a row's parts loaded before the first
-        // addition and two rows at a time
-        const uint32_t mine = smem_u32(part) + static_cast<uint32_t>(lane) * 16;
-        const int col4 = tp * kTileP + lane * 4;
-        const int first = rank + warp * ck, step = ck * (kSplitThreads / 32);
-        for (int c = first; c < rows; c += 2 * step) {
-            float4 x[2][8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < ck && c + h * step < rows) x[h][k] = ld_cluster_f4(mapa_shared(mine + (c + h * step) * 512, k));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (c + h * step >= rows || col4 >= p.n) continue;
-                float4 v = x[h][0];
-#pragma unroll
-                for (int k = 1; k < 8; ++k)
-                    if (k < ck) v = make_float4(v.x + x[h][k].x, v.y + x[h][k].y, v.z + x[h][k].z, v.w + x[h][k].w);
-                store_four(p, row0 + c + h * step, col4, v);
-            }
+        const int c0 = tp * kTileP;
+        switch (ck) {
+            case 2: add_parts<2>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 3: add_parts<3>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 4: add_parts<4>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 5: add_parts<5>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 6: add_parts<6>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 7: add_parts<7>(p, part, rank, warp, lane, c0, row0, rows); break;
+            default: add_parts<8>(p, part, rank, warp, lane, c0, row0, rows); break;
         }
         cluster_sync_all();  // a CTA's part stays until its peers have read it
     } else {
@@ -686,37 +718,83 @@ cudaError_t allow_smem(Kernel kernel, int bytes, bool (&done)[64]) {
     return cudaSuccess;
 }
 
-// CTAs of a cluster that share a tile's K: enough for two CTAs per SM, at least
-// two stages each.
-int split_for(int64_t tiles, int num_kb) {
-    int split = 1;
-    while (split < 8 && 2 * split * tiles <= 2 * device_sm_count() && 4 * split <= num_kb) split *= 2;
-    return split;
+template <int BN>
+void split_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int tiles_p, int tiles_q, int split, cudaStream_t st) {
+    cfg = {};
+    cfg.gridDim = dim3(tiles_p * split, tiles_q, 1);
+    cfg.blockDim = dim3(kSplitThreads, 1, 1);
+    cfg.dynamicSmemBytes = SplitCfg<BN>::SMEM;
+    cfg.stream = st;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = split;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+}
+
+// Clusters of `split` CTAs that run at once, asked once per device.  The query counts
+// one CTA per SM for a kernel that allocates TMEM (152, 76, 36 and 15 clusters of 1, 2,
+// 4 and 8); two were seen to run (40 clusters of 4 in the time of one round).
+template <int BN>
+int resident_clusters(int split) {
+    static std::atomic<int> cached[64][kMaxSplit + 1];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && cached[dev][split].load(std::memory_order_relaxed)) return cached[dev][split].load(std::memory_order_relaxed);
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    split_config<BN>(cfg, attr, 1, 1, split, nullptr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_split_kernel<BN>, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = std::max(1, device_sm_count() / (2 * split));
+    }
+    n *= 2;
+    if (keep) cached[dev][split].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// CTAs of a cluster that share a tile's K, and the estimated time in us: rounds of
+// resident clusters x stages x the time of a stage, and the addition of the parts.
+// Measured: a stage takes 0.3 us in a CTA that has its SM to itself (128 x 128 tiles,
+// 37 stages in 11.4 us; 128 x 16, 40 in 11.1), 0.45 us where two share an SM, or
+// what the CTAs get of B from HBM together; adding 128 rows of parts takes 4.5 us, one
+// row 0.7; a round starts and ends in 3.
+template <int BN>
+int split_for(int tiles_p, int tiles_q, const MxGemmArgs& p, double* cost) {
+    const int rows = p.m, num_kb = p.num_kb;
+    const double bytes = kPBytes + SplitCfg<BN>::Q_BYTES + 2 * kSfBytes;
+    const int64_t tiles = static_cast<int64_t>(tiles_p) * tiles_q;
+    // fp32 D: no part sums more than kSplitSumKb stages (the truncation that SUMS is about)
+    const int least = p.d_f32 ? std::min(kMaxSplit, (num_kb + kSplitSumKb - 1) / kSplitSumKb) : 1;
+    int best = 0;
+    for (int s = least; s <= kMaxSplit && s <= num_kb; ++s) {
+        const int cap = resident_clusters<BN>(s);
+        const double ctas = static_cast<double>(std::min<int64_t>(tiles, cap) * s);
+        const double stage = std::max({kStageUs, bytes * std::ceil(ctas / device_sm_count()) / 0.15e6,
+                                       (kPBytes + kSfBytes) * ctas / tiles_q / 6.5e6});
+        const double rounds = static_cast<double>((tiles + cap - 1) / cap);
+        const double c = rounds * (((num_kb + s - 1) / s) * stage + 3.0 + (s > 1 ? 0.7 + 0.03 * std::min(rows, BN) : 0.0));
+        if (!best || c < *cost) *cost = c, best = s;
+    }
+    return best;
 }
 
 template <int BN>
 cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, MxGemmArgs p, cudaStream_t st) {
-    using C = SplitCfg<BN>;
     static bool done[64] = {false};
-    cudaError_t e = allow_smem(mx_gemm_split_kernel<BN>, C::SMEM, done);
+    cudaError_t e = allow_smem(mx_gemm_split_kernel<BN>, SplitCfg<BN>::SMEM, done);
     if (e != cudaSuccess) return e;
     CUtensorMap ma, mb;
     if (!map_codes(&ma, a, p.k, p.m, lda, BN) || !map_codes(&mb, b, p.k, p.n, ldb, kTileP)) return cudaErrorUnknown;
     const int tiles_p = (p.n + kTileP - 1) / kTileP, tiles_q = (p.m + BN - 1) / BN;
-    const int split = split_for(static_cast<int64_t>(tiles_p) * tiles_q, p.num_kb);
-    p.split = split;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles_p * split, tiles_q, 1);
-    cfg.blockDim = dim3(kSplitThreads, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    double cost;
+    p.split = split_for<BN>(tiles_p, tiles_q, p, &cost);
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    split_config<BN>(cfg, attr, tiles_p, tiles_q, p.split, st);
     note_launch();
     return cudaLaunchKernelEx(&cfg, mx_gemm_split_kernel<BN>, ma, mb, p);
 }
@@ -774,13 +852,18 @@ cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int6
     p.num_kb = (p.k + kTileK - 1) / kTileK;
     p.last_nk = (p.k - (p.num_kb - 1) * kTileK) / 32;
     p.err = device_error_word();
-    if (p.m <= 16) return launch_split<16>(a, lda, b, ldb, p, st);
-    if (p.m <= 32) return launch_split<32>(a, lda, b, ldb, p, st);
-    if (p.m <= 64) return launch_split<64>(a, lda, b, ldb, p, st);
-    if (p.m <= 128) return launch_split<128>(a, lda, b, ldb, p, st);
+    // fp32 D over a K that eight parts of kSplitSumKb stages do not cover: the pair kernel's sums
+    const bool long_sum = p.d_f32 && p.num_kb > kMaxSplit * kSplitSumKb;
+    if (!long_sum) {
+        if (p.m <= 16) return launch_split<16>(a, lda, b, ldb, p, st);
+        if (p.m <= 32) return launch_split<32>(a, lda, b, ldb, p, st);
+        if (p.m <= 64) return launch_split<64>(a, lda, b, ldb, p, st);
+        if (p.m <= 128) return launch_split<128>(a, lda, b, ldb, p, st);
+    }
     // The tile width that leaves the least time to the pair with the most tiles.  A
     // stage's time goes with the rows it loads (256 + BN): 128-wide tiles took 0.79 of
-    // the time of 256-wide ones (293 and 371 ns per stage, K = 5120, 640 tiles of 256).
+    // the time of 256-wide ones (293 and 371 ns per stage, K = 5120, 640 tiles of 256);
+    // a tile's epilogue takes about 2.2 us, filling and emptying the pipeline 4.
     const bool sums = p.d_f32 && p.num_kb > kChunkK / kTileK;
     const int64_t pairs = device_sm_count() / 2;
     int best = 0;
@@ -788,16 +871,19 @@ cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int6
     for (const int bn : {256, 192, 128}) {
         if (bn > 192 && sums) continue;
         const int64_t tiles = static_cast<int64_t>((p.n + 255) / 256) * ((p.m + bn - 1) / bn);
-        const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * p.num_kb * (256 + bn) * (0.37 / 512);
+        const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * std::max(p.num_kb * (256 + bn) * (0.37 / 512), 2.2) + 4.0;
         if (!best || cost < least) best = bn, least = cost;
     }
-    // Too few tiles for the pairs: 128 x 128 tiles with K split over clusters, about
-    // 0.32 us per stage of every CTA an SM gets and 3 us for adding the parts.
-    const int64_t small = static_cast<int64_t>((p.n + 127) / 128) * ((p.m + 127) / 128);
-    const int split = split_for(small, p.num_kb);
-    const double split_cost =
-        static_cast<double>((small * split + 2 * pairs - 1) / (2 * pairs)) * ((p.num_kb + split - 1) / split) * 0.32 + 3.0;
-    if (split_cost < least && small <= 65535) return launch_split<128>(a, lda, b, ldb, p, st);
+    // Too few tiles for the pairs: 128 x 128 tiles with K split over clusters.
+    const int64_t small_q = (static_cast<int64_t>(p.m) + 127) / 128;
+    if (small_q <= 65535 && !long_sum) {
+        static bool done[64] = {false};
+        const cudaError_t e = allow_smem(mx_gemm_split_kernel<128>, SplitCfg<128>::SMEM, done);  // before its occupancy is asked
+        if (e != cudaSuccess) return e;
+        double split_cost;
+        split_for<128>((p.n + 127) / 128, static_cast<int>(small_q), p, &split_cost);
+        if (split_cost < least) return launch_split<128>(a, lda, b, ldb, p, st);
+    }
     if (best == 256) return launch_pair_of<256>(a, lda, b, ldb, p, st);
     if (best == 192) return launch_pair_of<192>(a, lda, b, ldb, p, st);
     return launch_pair_of<128>(a, lda, b, ldb, p, st);

@@ -628,3 +628,23 @@ def test_product_tile_widths(hm, dev, m, n, k, out):
         tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()
     assert bool(((d.double() - ref).abs() <= tol).all())
     assert hm.hm_device_error() == 0
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 300, 12288), (40, 200, 24576), (300, 260, 8192)])
+def test_product_long_fp32_sums(hm, dev, m, n, k):
+    """fp32 D over a long K, operands of one sign (every truncation of the accumulator goes the
+    same way): no chain of tensor-core additions is longer than 2560, so the error stays
+    within (2560 / 32 + 33) 2u of the sum plus one rounding per part."""
+    g = torch.Generator(device=dev)
+    g.manual_seed(k)
+    ops = []
+    for rows in (m, n):
+        codes = torch.randint(0x30, 0x40, (rows, k), generator=g, device=dev, dtype=torch.uint8)
+        sf = torch.full((rows, k // 32), 127, device=dev, dtype=torch.uint8)
+        tiled = torch.from_numpy(OX.scale_tile_128x4(sf.cpu().numpy())).to(dev)
+        ops.append((codes, tiled, codes.view(torch.float8_e4m3fn).double()))
+    (qa, ta, va), (qb, tb, vb) = ops
+    d = torch.zeros(m, n, device=dev)
+    _gemm(hm, qa, ta, qb, tb, m, n, k, d)
+    ref = va @ vb.t()
+    assert bool(((d.double() - ref).abs() <= ((2560 / 32 + 33) * 2 + k / 2048 + 8) * U * ref).all())
