@@ -74,6 +74,7 @@ class MuonSession:
         self.ws_bytes = int(self.info.workspace_bytes)
         self._ws_buf, self.ws = aligned_empty(self.ws_bytes, dev)
         abi.muon_plan_upload(self.plan, self.ws, self.ws_bytes, _stream_handle(None))
+        self._clip = None
         self.bufs = abi.hm_muon_bufs(self.w.data_ptr(), self.m.data_ptr(), self.g.data_ptr(), self.u.data_ptr(),
                                      self.v.data_ptr(), self.q.data_ptr(), self.s.data_ptr())
 
@@ -156,6 +157,26 @@ class MuonSession:
     def run(self, hp: "abi.hm_muon_hparams", stages: int = abi.HM_STAGE_ALL,
             stream: Optional[torch.cuda.Stream] = None) -> None:
         abi.muon_update_units(self.plan, self.bufs, hp, self.ws, self.ws_bytes, stages, _stream_handle(stream))
+
+    def grad_list(self):
+        """(src, dst, elements, dtype) of every rank segment of the main gradient, in place:
+        entries for abi.grad_list."""
+        return [(self.g.data_ptr() + 4 * b, self.g.data_ptr() + 4 * b, n, abi.HM_F32)
+                for b, n in zip(self.bases, self.lens) if n]
+
+    def clip_grad_norm(self, max_norm: float, eps: float = 1e-6, tensors=None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """Clips the main gradient (or the given (src, dst, elements, dtype) entries) by its
+        global norm, between the reduce-scatter and the update.  Returns the device
+        tensor (norm, coefficient) of the last call; canary gaps are not touched."""
+        key = tuple(tensors) if tensors is not None else None
+        if self._clip is None or self._clip[0] != key:
+            lst = abi.grad_list(list(tensors) if tensors is not None else self.grad_list())
+            ws = torch.empty(max(16, abi.grad_norm_clip_workspace(lst)), dtype=torch.uint8, device=self.device)
+            self._clip = (key, lst, ws, torch.zeros(2, dtype=torch.float32, device=self.device))
+        _, lst, ws, stats = self._clip
+        abi.grad_norm_clip(lst, max_norm, eps, stats.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle(stream))
+        return stats
 
     def staging(self, unit: int):
         """Device views of a straddling unit's u / v staging."""
