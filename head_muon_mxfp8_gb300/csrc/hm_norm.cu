@@ -22,6 +22,8 @@ namespace hm {
 namespace {
 
 constexpr int kMaxRowThreads = 512;
+constexpr int kWarpRows = 8;       // rows per CTA where a row is one warp's
+constexpr int kWarpMaxD = 1024;
 constexpr int kMaxGradStages = 16;
 constexpr int kGradRing = 208 * 1024;  // bytes of rows in flight per SM; a stage is at most 3 x 64 KB
 
@@ -89,12 +91,17 @@ __device__ __forceinline__ void load_f8(const float* p, float (&v)[8]) {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// Sum over the block, the same in every thread: warp sums, then every thread
-// adds the warps' in order.  `red` alternates between two rows of 16, so one
-// barrier per sum is enough.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// Sum over the warp, the same in every lane.
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sum over the block, the same in every thread: warp sums, then every thread
+// adds the warps' in order.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+    v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     float t = 0.f;
@@ -103,17 +110,21 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return t;
 }
 
-// One row per CTA; a thread owns V vectors of 8 columns, vector i * blockDim + t.
-template <bool F32, int V>
+// A row per CTA, or per warp (8 rows per CTA) where a row has at most 1024
+// columns: its sum then needs no barrier (32768 x 256 bf16: 19.0 us with a CTA
+// per row, 10.4 with a warp; x 1024: 41.6 and 37.7).  A thread owns V vectors of 8 columns,
+// vector i * (threads of the row) + t.
+template <bool F32, int V, bool WARP>
 __global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_kernel(const __grid_constant__ RmsArgs p) {
     __shared__ float red[16];
-    const int64_t row = blockIdx.x;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
+    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     const int nv = p.d >> 3;
     const int lane = threadIdx.x & 31;
     const int64_t col_tiles = (p.d + 127) >> 7;
     uint8_t* srow = p.s + (row >> 7) * col_tiles * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4;
     if (row >= p.rows) {  // padding of the last scale tiles
-        for (int64_t j = threadIdx.x; j < col_tiles; j += blockDim.x) *reinterpret_cast<uint32_t*>(srow + j * 512) = 0u;
+        for (int64_t j = t; j < col_tiles; j += threads) *reinterpret_cast<uint32_t*>(srow + j * 512) = 0u;
         return;
     }
     float h[V][8];
@@ -121,7 +132,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_kernel(const __grid_co
     Vec8<F32> x[V], r[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int j = i * blockDim.x + threadIdx.x;
+        const int j = i * threads + t;
         if (j < nv) {
             x[i].load(p.x, row * p.ldx + j * 8);
             if (p.res) r[i].load(p.res, row * p.ldh + j * 8);
@@ -129,7 +140,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_kernel(const __grid_co
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int j = i * blockDim.x + threadIdx.x;
+        const int j = i * threads + t;
         if (j < nv) {
             x[i].get(h[i]);
             if (p.res) {
@@ -144,11 +155,11 @@ __global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_kernel(const __grid_co
             for (int k = 0; k < 8; ++k) sq = fmaf(h[i][k], h[i][k], sq);
         }
     }
-    const float rstd = 1.0f / sqrtf(block_sum(sq, red) / static_cast<float>(p.d) + p.eps);
-    if (threadIdx.x == 0) p.rstd[row] = rstd;
+    const float rstd = 1.0f / sqrtf((WARP ? warp_sum(sq) : block_sum(sq, red)) / static_cast<float>(p.d) + p.eps);
+    if (t == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int j = i * blockDim.x + threadIdx.x;
+        const int j = i * threads + t;
         float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (j < nv) {
             float gm[8];
@@ -308,6 +319,105 @@ __global__ void __launch_bounds__(T, B) rmsnorm_grad_kernel(const __grid_constan
     }
 }
 
+// Gradient of rows of at most 1024 columns: a warp per row, no barrier until the
+// end (32768 x 256 bf16: 73.6 us through the ring, 15.4; x 1024: 83.5 and 51.9), the next row's vectors loaded before this one's are used (V <= 2; more
+// would not leave registers); the warps' parts of dgamma are added in order.
+template <bool F32, int V>
+__global__ void __launch_bounds__(32 * kWarpRows) rmsnorm_grad_warp_kernel(const __grid_constant__ RmsGradArgs p) {
+    __shared__ __align__(16) float part[kWarpRows][V * 256];
+    constexpr bool kAhead = V <= 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nv = p.d >> 3;
+    float dg[V][8], gamma[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int j = i * 32 + lane;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dg[i][k] = gamma[i][k] = 0.f;
+        if (kAhead && j < nv) load_f8(p.gamma + j * 8, gamma[i]);
+    }
+    Vec8<F32> dy[V], h[V], dr[V], dy1[V], h1[V], dr1[V];
+    auto fetch = [&](int64_t row, Vec8<F32>(&a)[V], Vec8<F32>(&b)[V], Vec8<F32>(&c)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int j = i * 32 + lane;
+            if (j < nv) {
+                a[i].load(p.dy, row * p.lddy + j * 8);
+                b[i].load(p.h, row * p.ldh + j * 8);
+                if (p.dres) c[i].load(p.dres, row * p.ldh + j * 8);
+            }
+        }
+    };
+    const float inv_d = 1.0f / static_cast<float>(p.d);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarpRows;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kWarpRows + warp;
+    float rstd1 = 0.f;
+    if (row < p.rows) {
+        fetch(row, dy, h, dr);
+        rstd1 = __ldg(p.rstd + row);
+    }
+    for (; row < p.rows; row += step) {
+        const float rstd = rstd1;
+        const bool more = row + step < p.rows;
+        if (more) {
+            rstd1 = __ldg(p.rstd + row + step);
+            if (kAhead) fetch(row + step, dy1, h1, dr1);
+        }
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int j = i * 32 + lane;
+            if (j < nv) {
+                float y[8], x[8];
+                if (!kAhead) load_f8(p.gamma + j * 8, gamma[i]);
+                dy[i].get(y);
+                h[i].get(x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float yx = y[k] * (x[k] * rstd);
+                    dg[i][k] += yx;
+                    dot = fmaf(yx, gamma[i][k], dot);
+                }
+            }
+        }
+        const float back = -rstd * (warp_sum(dot) * inv_d);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int j = i * 32 + lane;
+            if (j < nv) {
+                float y[8], x[8], o[8], rv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (!kAhead) load_f8(p.gamma + j * 8, gamma[i]);
+                dy[i].get(y);
+                h[i].get(x);
+                if (p.dres) dr[i].get(rv);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = fmaf(x[k] * rstd, back, fmaf(y[k] * gamma[i][k], rstd, rv[k]));
+                Vec8<F32>::put(p.dx, row * p.ldh + j * 8, o);
+            }
+        }
+        if (!more) break;
+        if (kAhead) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) dy[i] = dy1[i], h[i] = h1[i], dr[i] = dr1[i];
+        } else {
+            fetch(row + step, dy, h, dr);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float4* q = reinterpret_cast<float4*>(&part[warp][(i * 32 + lane) * 8]);
+        q[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+        q[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.d; c += 32 * kWarpRows) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarpRows; ++w) s += part[w][c];
+        p.partials[static_cast<int64_t>(blockIdx.x) * p.d + c] = s;
+    }
+}
+
 // dgamma from the CTAs' partials: 32 columns per CTA, 32 threads per column each
 // adding every 32nd partial in order, then the 32 in order.
 __global__ void __launch_bounds__(1024) dgamma_kernel(const float* __restrict__ partials, int parts, int d,
@@ -328,17 +438,22 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* __restrict__ 
     }
 }
 
-int row_vectors(int64_t d) { return d <= 4096 ? 1 : d <= 8192 ? 2 : 4; }
-int row_threads(int64_t d, int v) { return static_cast<int>(((d / 8 + v - 1) / v + 31) / 32 * 32); }
-
 template <bool F32>
 cudaError_t launch_fwd(const RmsArgs& a, cudaStream_t st) {
-    const int v = row_vectors(a.d), threads = row_threads(a.d, v);
-    const unsigned grid = static_cast<unsigned>((a.rows + 127) / 128 * 128);
+    const unsigned rows = static_cast<unsigned>((a.rows + 127) / 128 * 128);
     note_launch();
-    if (v == 1) rmsnorm_kernel<F32, 1><<<grid, threads, 0, st>>>(a);
-    else if (v == 2) rmsnorm_kernel<F32, 2><<<grid, threads, 0, st>>>(a);
-    else rmsnorm_kernel<F32, 4><<<grid, threads, 0, st>>>(a);
+    if (a.d <= kWarpMaxD) {
+        const unsigned grid = rows / kWarpRows;
+        if (a.d <= 256) rmsnorm_kernel<F32, 1, true><<<grid, 32 * kWarpRows, 0, st>>>(a);
+        else if (a.d <= 512) rmsnorm_kernel<F32, 2, true><<<grid, 32 * kWarpRows, 0, st>>>(a);
+        else rmsnorm_kernel<F32, 4, true><<<grid, 32 * kWarpRows, 0, st>>>(a);
+    } else {
+        // two vectors per thread up to 8192 columns (8192 x 4096 bf16: 40.9 us with one, 30.8 with two)
+        const int v = a.d <= 8192 ? 2 : 4;
+        const int threads = ((a.d / 8 + v - 1) / v + 31) / 32 * 32;
+        if (v == 2) rmsnorm_kernel<F32, 2, false><<<rows, threads, 0, st>>>(a);
+        else rmsnorm_kernel<F32, 4, false><<<rows, threads, 0, st>>>(a);
+    }
     return cudaGetLastError();
 }
 
@@ -366,14 +481,20 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
     RmsGradArgs a = a0;
     a.err = device_error_word();
     // Two CTAs per SM where half the ring still holds two rows: one computes while
-    // the other stands at its barrier (8192 x 5120 bf16: 71 us with one, {TWO} with two).
+    // the other stands at its barrier (8192 x 5120 bf16: 71 us with one, 55 with two).
     const int stage = a.d * (F32 ? 4 : 2) * (a.dres ? 3 : 2);
     const bool two = a.d <= 8192 && 2 * stage <= kGradRing / 2;
     const int most = rmsnorm_grad_parts(a.rows, a.d);
-    const int parts = two ? most : std::min(most, device_sm_count());
+    const int parts = a.d <= kWarpMaxD ? most : std::min(most, (two ? 2 : 1) * device_sm_count());
     if (parts) {
-        cudaError_t e;
-        if (a.d <= 4096) e = two ? launch_grad<F32, 1, 512, 2>(a, parts, stage, st) : launch_grad<F32, 1, 512, 1>(a, parts, stage, st);
+        cudaError_t e = cudaSuccess;
+        if (a.d <= kWarpMaxD) {
+            note_launch();
+            if (a.d <= 256) rmsnorm_grad_warp_kernel<F32, 1><<<parts, 32 * kWarpRows, 0, st>>>(a);
+            else if (a.d <= 512) rmsnorm_grad_warp_kernel<F32, 2><<<parts, 32 * kWarpRows, 0, st>>>(a);
+            else rmsnorm_grad_warp_kernel<F32, 4><<<parts, 32 * kWarpRows, 0, st>>>(a);
+            e = cudaGetLastError();
+        } else if (a.d <= 4096) e = two ? launch_grad<F32, 1, 512, 2>(a, parts, stage, st) : launch_grad<F32, 1, 512, 1>(a, parts, stage, st);
         else if (a.d <= 5120 && two) e = launch_grad<F32, 2, 320, 2>(a, parts, stage, st);
         else if (a.d <= 8192) e = two ? launch_grad<F32, 2, 512, 2>(a, parts, stage, st) : launch_grad<F32, 2, 512, 1>(a, parts, stage, st);
         else e = launch_grad<F32, 2, 1024, 1>(a, parts, stage, st);
@@ -387,9 +508,9 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
 }  // namespace
 
 int rmsnorm_grad_parts(int64_t rows, int64_t d) {
-    (void)d;
-    const int64_t most = 2 * static_cast<int64_t>(device_sm_count());
-    return static_cast<int>(rows < most ? rows : most);
+    const int64_t sms = device_sm_count();
+    if (d <= kWarpMaxD) return static_cast<int>(std::min((rows + kWarpRows - 1) / kWarpRows, (d <= 256 ? 4 : 2) * sms));
+    return static_cast<int>(std::min(rows, 2 * sms));
 }
 
 cudaError_t launch_rmsnorm(const RmsArgs& a, int f32, cudaStream_t st) {

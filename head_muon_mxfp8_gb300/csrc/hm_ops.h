@@ -39,6 +39,8 @@ struct QuantArgs {
     uint8_t* st;
     int32_t block;       // 32 or 128
     int32_t vec;         // x's rows are 16-byte aligned
+    int32_t col_vec;     // there are column factors, 16-byte aligned
+    int32_t pad;
 };
 cudaError_t launch_quantize(const QuantArgs& a, int f32, cudaStream_t st);
 

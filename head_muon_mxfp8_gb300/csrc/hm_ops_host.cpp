@@ -127,6 +127,7 @@ extern "C" hm_status mxfp8_quantize(const void* x, hm_dtype x_dtype, int64_t row
     a.st = st;
     a.block = block;
     a.vec = aligned(x, 16) && ldx * es % 16 == 0;
+    a.col_vec = col_mul && aligned(col_mul, 16);
     return cuda_status(hm::launch_quantize(a, x_dtype == HM_F32, static_cast<cudaStream_t>(stream)));
 }
 

@@ -9,6 +9,10 @@
 // A CTA takes a 128 x 128 tile: the tile's scales are then one 512-byte tile of
 // either scale layout.  Memory-bound: bf16 x with both outputs moves
 // 2 + 2 (1 + 1/32) bytes per element.
+// 8192 x 15360 bf16 to both outputs takes 81 us (6.3 TB/s, 0.93 of the measured
+// copy rate); a 14336 x 4096 fp32 weight to its transpose 63 us (4.7 TB/s), where
+// registers for the loads leave two CTAs per SM (a third CTA's spill: 92 us;
+// 512 threads per CTA: 66 us).
 #include "hm_internal.h"
 #include "hm_mx_device.cuh"
 #include "hm_ops.h"
@@ -20,40 +24,55 @@ namespace {
 constexpr int kQThreads = 256;
 constexpr int kQTile = 128;
 
+// 16 elements of a row of x as loaded, those from `left` on being zero.
 template <bool F32>
-__device__ __forceinline__ void load16(const void* x, int64_t at, int left, bool vec, float (&v)[16]) {
-    // elements at .. at + 15, those from `left` on being zero
-    if (F32) {
-        const float* p = static_cast<const float*>(x) + at;
+struct Raw16 {
+    static constexpr int N = F32 ? 4 : 2;
+    uint4 w[N];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < N; ++k) w[k] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void load(const void* x, int64_t at, int left, bool vec) {
         if (vec && left == 16) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at * (F32 ? 4 : 2));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float4 a = __ldcs(reinterpret_cast<const float4*>(p) + k);
-                v[4 * k] = a.x; v[4 * k + 1] = a.y; v[4 * k + 2] = a.z; v[4 * k + 3] = a.w;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = k < left ? p[k] : 0.f;
+            for (int k = 0; k < N; ++k) w[k] = __ldcs(p + k);
+            return;
         }
-    } else {
-        const uint16_t* p = static_cast<const uint16_t*>(x) + at;
-        if (vec && left == 16) {
+        uint32_t h[16];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p) + j);
-                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        for (int k = 0; k < 16; ++k)
+            h[k] = k >= left ? 0u
+                   : F32     ? static_cast<const uint32_t*>(x)[at + k]
+                             : static_cast<uint32_t>(static_cast<const uint16_t*>(x)[at + k]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
-                    v[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        for (int k = 0; k < N; ++k)
+            w[k] = F32 ? make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3])
+                       : make_uint4(h[(8 * k) & 15] | (h[(8 * k + 1) & 15] << 16), h[(8 * k + 2) & 15] | (h[(8 * k + 3) & 15] << 16),
+                                    h[(8 * k + 4) & 15] | (h[(8 * k + 5) & 15] << 16), h[(8 * k + 6) & 15] | (h[(8 * k + 7) & 15] << 16));
+    }
+    __device__ __forceinline__ void get(float (&v)[16]) const {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (F32) {
+                    v[(4 * k + j) & 15] = __uint_as_float(u[j]);
+                } else {
+                    v[(8 * k + 2 * j) & 15] = __uint_as_float(u[j] << 16);
+                    v[(8 * k + 2 * j + 1) & 15] = __uint_as_float(u[j] & 0xFFFF0000u);
                 }
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = k < left ? __uint_as_float(static_cast<uint32_t>(p[k]) << 16) : 0.f;
         }
     }
-}
+};
+
+// Where the fp32 tile keeps 16-byte piece k of a row: no bank twice, neither for the
+// row phase's lanes (64 bytes apart) nor for a column's readers (the exchange
+// stays inside 128 bytes).
+__device__ __forceinline__ int swizzled(int k) { return k ^ (k >> 3); }
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float sc) {
     return cvt_e4m3x2(a * sc, b * sc) | (static_cast<uint32_t>(cvt_e4m3x2(c * sc, d * sc)) << 16);
@@ -111,9 +130,9 @@ __device__ __forceinline__ int row_scale(float amax, int block) {
 //   PACKED (bf16 x, no factors): y is x, so the tile stays in bf16 pairs --
 //     half the shared memory and half its traffic, and magnitudes are compared
 //     two at a time; a thread's column work is a pair of columns x 32 rows.
-//   else: y in fp32; a thread's column work is one column x 2 x 32 rows.
+//   else: y in fp32 (swizzled); a thread's column work is one column x 32 rows.
 template <bool F32, bool PACKED, bool COL>
-__global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_constant__ QuantArgs p) {
+__global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(const __grid_constant__ QuantArgs p) {
     extern __shared__ __align__(16) uint32_t tile[];  // [128][64] bf16 pairs or [128][128] fp32
     __shared__ __align__(16) uint8_t s_row[512];
     __shared__ __align__(16) uint8_t s_col[512];
@@ -124,42 +143,31 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
     const int64_t cols32 = (p.cols + 31) / 32 * 32, rows32 = (p.rows + 31) / 32 * 32;
     const int c16 = (lane & 7) * 16;
     const int left = static_cast<int>(min(static_cast<int64_t>(16), max(static_cast<int64_t>(0), p.cols - (c0 + c16))));
-    const int rl0 = warp * 16 + (lane >> 3);                                        // this lane's rows: rl0 + 4 i
+    constexpr int kSteps = 128 * 32 / kQThreads / 4;  // rows per warp, four at a time
+    const int rl0 = warp * (4 * kSteps) + (lane >> 3);         // this lane's rows: rl0 + 4 i
     const int rows = static_cast<int>(min(static_cast<int64_t>(kQTile), p.rows - r0));  // of the tile
     const bool q_live = p.q && c0 + c16 < cols32;
     const int flip = (lane >> 2) & 1;  // which of its two 16-byte pieces a lane stores first: no bank twice
     uint8_t* qp = p.q + (r0 + rl0) * p.ldq + c0 + c16;
 
     if constexpr (PACKED) {
-        uint4 raw[4][2];
-        const uint16_t* src = static_cast<const uint16_t*>(p.x) + (r0 + rl0) * p.ldx + c0 + c16;
+        Raw16<false> raw[kSteps];
 #pragma unroll
-        for (int i = 0; i < 4; ++i, src += 4 * p.ldx) {
-            raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (rl0 + 4 * i < rows && left > 0) {
-                if (p.vec && left == 16) {
-                    raw[i][0] = __ldcs(reinterpret_cast<const uint4*>(src));
-                    raw[i][1] = __ldcs(reinterpret_cast<const uint4*>(src) + 1);
-                } else {
-                    uint32_t h[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) h[k] = k < left ? src[k] : 0u;
-                    raw[i][0] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
-                    raw[i][1] = make_uint4(h[8] | (h[9] << 16), h[10] | (h[11] << 16), h[12] | (h[13] << 16), h[14] | (h[15] << 16));
-                }
-            }
+        for (int i = 0; i < kSteps; ++i) {
+            raw[i].clear();
+            if (rl0 + 4 * i < rows && left > 0) raw[i].load(p.x, (r0 + rl0 + 4 * i) * p.ldx + c0 + c16, left, p.vec);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kSteps; ++i) {
             const int rl = rl0 + 4 * i;
             if (COL) {
                 uint4* t4 = reinterpret_cast<uint4*>(tile + rl * (kQTile / 2) + c16 / 2);
-                t4[flip] = flip ? raw[i][1] : raw[i][0];
-                t4[flip ^ 1] = flip ? raw[i][0] : raw[i][1];
+                t4[flip] = flip ? raw[i].w[1] : raw[i].w[0];
+                t4[flip ^ 1] = flip ? raw[i].w[0] : raw[i].w[1];
             }
             if (p.q) {
-                const uint32_t w[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
-                                       raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
+                const uint32_t w[8] = {raw[i].w[0].x, raw[i].w[0].y, raw[i].w[0].z, raw[i].w[0].w,
+                                       raw[i].w[1].x, raw[i].w[1].y, raw[i].w[1].z, raw[i].w[1].w};
                 uint32_t m = 0u;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) m = max_abs2(m, w[k]);
@@ -181,43 +189,57 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
         }
     } else {
         float cm[16];
+        if (p.col_vec && left == 16) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) cm[k] = p.col_mul && k < left ? p.col_mul[c0 + c16 + k] : 1.f;
-        float v[4][16];
+            for (int k = 0; k < 4; ++k) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(p.col_mul + c0 + c16) + k);
+                cm[4 * k] = f.x; cm[4 * k + 1] = f.y; cm[4 * k + 2] = f.z; cm[4 * k + 3] = f.w;
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[i][k] = 0.f;
-            if (rl0 + 4 * i < rows && left > 0) load16<F32>(p.x, (r0 + rl0 + 4 * i) * p.ldx + c0 + c16, left, p.vec, v[i]);
+            for (int k = 0; k < 16; ++k) cm[k] = p.col_mul && k < left ? p.col_mul[c0 + c16 + k] : 1.f;
         }
+        Raw16<F32> raw[kSteps];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int rl = rl0 + 4 * i;
-            if (rl < rows) {  // outside x the zeros stay +0 whatever the factors' signs
-                const float rm = p.row_mul ? p.row_mul[r0 + rl] : 1.f;
+        for (int j = 0; j < kSteps; ++j) {
+            raw[j].clear();
+            if (rl0 + 4 * j < rows && left > 0) raw[j].load(p.x, (r0 + rl0 + 4 * j) * p.ldx + c0 + c16, left, p.vec);
+        }
+        {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[i][k] = k < left ? v[i][k] * rm * cm[k] : 0.f;
-            }
-            if (COL) {
-                float4* t4 = reinterpret_cast<float4*>(tile + rl * kQTile + c16);
+            for (int j = 0; j < kSteps; ++j) {
+                const int rl = rl0 + 4 * j;
+                float v[16];
+                raw[j].get(v);
+                if (rl < rows) {  // outside x the zeros stay +0 whatever the factors' signs
+                    const float rm = p.row_mul ? p.row_mul[r0 + rl] : 1.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    t4[k] = make_float4(v[i][4 * k], v[i][4 * k + 1], v[i][4 * k + 2], v[i][4 * k + 3]);
-            }
-            if (p.q) {
-                float amax = 0.f;
+                    for (int k = 0; k < 16; ++k) v[k] = v[k] * rm * cm[k];
+                    if (left < 16)
 #pragma unroll
-                for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(v[i][k]));
-                const int byte = row_scale(amax, p.block);
-                const float sc = mx_inv_of_byte(byte);
-                const bool live = q_live && rl < rows;
-                if (live) {
-                    uint32_t c[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) c[k] = codes4(v[i][4 * k], v[i][4 * k + 1], v[i][4 * k + 2], v[i][4 * k + 3], sc);
-                    __stcs(reinterpret_cast<uint4*>(qp + 4 * i * p.ldq), make_uint4(c[0], c[1], c[2], c[3]));
+                        for (int k = 0; k < 16; ++k) v[k] = k < left ? v[k] : 0.f;
                 }
-                if (!(lane & 1)) s_row[(rl & 31) * 16 + (rl >> 5) * 4 + ((lane & 7) >> 1)] = live ? static_cast<uint8_t>(byte) : 0;
+                if (COL) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<float4*>(tile + rl * kQTile + 4 * swizzled(c16 / 4 + k)) =
+                            make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                }
+                if (p.q) {
+                    float amax = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(v[k]));
+                    const int byte = row_scale(amax, p.block);
+                    const float sc = mx_inv_of_byte(byte);
+                    const bool live = q_live && rl < rows;
+                    if (live) {
+                        uint32_t c[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) c[k] = codes4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], sc);
+                        __stcs(reinterpret_cast<uint4*>(qp + 4 * j * p.ldq), make_uint4(c[0], c[1], c[2], c[3]));
+                    }
+                    if (!(lane & 1)) s_row[(rl & 31) * 16 + (rl >> 5) * 4 + ((lane & 7) >> 1)] = live ? static_cast<uint8_t>(byte) : 0;
+                }
             }
         }
     }
@@ -264,43 +286,44 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
             s_col[((c + 1) & 31) * 16 + (c >> 5) * 4 + b] = live1 ? static_cast<uint8_t>(y1) : 0;
         } else {
             const float* y = reinterpret_cast<const float*>(tile);
-            const int c = threadIdx.x & 127, h = threadIdx.x >> 7;
-            const bool col_live = c0 + c < p.cols;
-            float w[2][32], a[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                a[j] = 0.f;
-#pragma unroll
-                for (int k = 0; k < 32; ++k) w[j][k] = y[((2 * h + j) * 32 + k) * kQTile + c];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) a[j] = fmaxf(a[j], fabsf(w[j][k]));
-            }
+            constexpr int kBlocks = 4 * kQTile / kQThreads;  // 32-row blocks of its column per thread
+            const int c = threadIdx.x & 127, b0 = (threadIdx.x >> 7) * kBlocks;
+            const float* col = y + b0 * 32 * kQTile + 4 * swizzled(c >> 2) + (c & 3);
+            float most = 0.f;
             if (p.block == 128) {
-                amax_col[h][c] = fmaxf(a[0], a[1]);
+                float m = 0.f;
+#pragma unroll 16
+                for (int k = 0; k < 32 * kBlocks; ++k) m = fmaxf(m, fabsf(col[k * kQTile]));
+                amax_col[threadIdx.x >> 7][c] = m;
                 __syncthreads();
-                a[0] = a[1] = fmaxf(amax_col[0][c], amax_col[1][c]);
+#pragma unroll
+                for (int k = 0; k < 4 / kBlocks; ++k) most = fmaxf(most, amax_col[k][c]);
+            }
+            uint32_t x[kBlocks][8];
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j) {
+                float w[32], amax = most;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) w[k] = col[(j * 32 + k) * kQTile];
+                if (p.block != 128) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) amax = fmaxf(amax, fabsf(w[k]));
+                }
+                const int byte = mx_scale_byte(amax);
+                const float sc = mx_inv_of_byte(byte);
+                s_col[(c & 31) * 16 + (c >> 5) * 4 + b0 + j] =
+                    c0 + c < p.cols && r0 + (b0 + j) * 32 < rows32 ? static_cast<uint8_t>(byte) : 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[j][k] = codes4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3], sc);
             }
             __syncthreads();  // the tile has been read
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int b = 2 * h + j;
-                const int byte = mx_scale_byte(a[j]);
-                const float sc = mx_inv_of_byte(byte);
-                const bool live = col_live && r0 + b * 32 < rows32;
-                s_col[(c & 31) * 16 + (c >> 5) * 4 + b] = live ? static_cast<uint8_t>(byte) : 0;
-                uint32_t x[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float* q = w[j] + 4 * k;
-                    x[k] = codes4(q[0], q[1], q[2], q[3], sc);
-                }
-                stage_codes32(reinterpret_cast<uint4*>(tile), c, b, x);
-            }
+            for (int j = 0; j < kBlocks; ++j) stage_codes32(reinterpret_cast<uint4*>(tile), c, b0 + j, x[j]);
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int c = k * 32 + (threadIdx.x >> 3), piece = threadIdx.x & 7;
+        for (int k = 0; k < kQTile; k += kQThreads / 8) {
+            const int c = k + (threadIdx.x >> 3), piece = threadIdx.x & 7;
             if (c0 + c < p.cols && r0 + piece * 16 < rows32)
                 __stcs(reinterpret_cast<uint4*>(p.qt + (c0 + c) * p.ldqt + r0) + piece,
                        reinterpret_cast<const uint4*>(tile)[c * 8 + (piece ^ stage_key(c))]);
