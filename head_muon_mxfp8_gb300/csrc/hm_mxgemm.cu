@@ -662,7 +662,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
             case 7: add_parts<7>(p, part, rank, warp, lane, c0, row0, rows); break;
             default: add_parts<8>(p, part, rank, warp, lane, c0, row0, rows); break;
         }
-        cluster_sync_all();  // a CTA's part stays until its peers have read it
+        __syncwarp();
+        cluster_arrive_relaxed();  // a CTA's part stays until its peers have read it
+        cluster_wait();
     } else {
         __syncthreads();
     }

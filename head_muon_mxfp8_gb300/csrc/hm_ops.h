@@ -76,8 +76,10 @@ struct RmsGradArgs {
 int rmsnorm_grad_parts(int64_t rows, int64_t d);
 cudaError_t launch_rmsnorm_grad(const RmsGradArgs& a, int f32, cudaStream_t st);
 
-// One launch handles up to kClipTensors tensors, passed by value.
+// A launch takes its tensors by value: up to kClipTensors, or up to kClipFew in
+// the one-launch form for little data.
 constexpr int kClipTensors = 256;
+constexpr int kClipFew = 16;
 struct ClipTensor {
     const void* src;
     void* dst;           // nullptr: only counted
@@ -85,7 +87,7 @@ struct ClipTensor {
     int32_t first;       // chunks before this tensor
     int32_t f32;
 };
-struct ClipArgs {
+struct ClipHead {
     int32_t n;           // tensors
     int32_t chunks;
     int32_t parts;       // partial sums of every launch of the call together
@@ -95,11 +97,19 @@ struct ClipArgs {
     float max_norm, eps;
     float* stats;
     double* partials;
-    ClipTensor t[kClipTensors];
 };
-int clip_chunks(const void* src, int64_t n, int f32);  // of one tensor with n > 0
-int clip_parts(int chunks);            // partial sums of one launch
-cudaError_t launch_clip_norm(ClipArgs& a, cudaStream_t st);
-cudaError_t launch_clip_scale(const ClipArgs& a, cudaStream_t st);
+template <int CAP>
+struct ClipArgs {
+    ClipHead h;
+    ClipTensor t[CAP];
+};
+constexpr int kClipChunkVecs = 4096;       // 16-byte vectors per chunk
+constexpr int kClipFewChunkVecs = 1024;    // in the one-launch form,
+constexpr int kClipFewChunks = 64;         // which takes at most so many (1 MB)
+int clip_chunks(const void* src, int64_t n, int f32, int vecs);  // of one tensor with n > 0
+int clip_parts(int chunks);                                      // partial sums of one launch
+cudaError_t launch_clip_norm(ClipArgs<kClipTensors>& a, cudaStream_t st);
+cudaError_t launch_clip_scale(const ClipArgs<kClipTensors>& a, cudaStream_t st);
+cudaError_t launch_clip_few(const ClipArgs<kClipFew>& a, cudaStream_t st);
 
 }  // namespace hm

@@ -237,6 +237,17 @@ extern "C" hm_status rmsnorm_backward(const void* dy, int64_t lddy, const void* 
 
 namespace {
 
+// Appends a tensor to a launch's table; returns the chunks with it.
+int64_t add_tensor(hm::ClipHead& h, hm::ClipTensor* table, const hm_grad_tensor& x, int64_t chunks, int vecs) {
+    hm::ClipTensor& t = table[h.n++];
+    t.src = x.src;
+    t.dst = x.dst;
+    t.n = x.n;
+    t.first = static_cast<int32_t>(chunks);
+    t.f32 = x.dtype == HM_F32;
+    return chunks + hm::clip_chunks(x.src, x.n, t.f32, vecs);
+}
+
 // Checks the list and counts its non-empty tensors and the partial sums of all launches.
 hm_status clip_layout(const hm_grad_tensor* t, int n, int64_t* live, int64_t* parts) {
     *live = *parts = 0;
@@ -255,7 +266,7 @@ hm_status clip_layout(const hm_grad_tensor* t, int n, int64_t* live, int64_t* pa
             *parts += hm::clip_parts(static_cast<int>(chunks));
             chunks = in_launch = 0;
         }
-        chunks += hm::clip_chunks(t[i].src, t[i].n, es == 4);
+        chunks += hm::clip_chunks(t[i].src, t[i].n, es == 4, hm::kClipChunkVecs);
         if (chunks > INT32_MAX) return HM_ERR_GEOMETRY;
         ++in_launch;
         ++*live;
@@ -286,36 +297,37 @@ extern "C" hm_status grad_norm_clip(const hm_grad_tensor* tensors, int n, float 
     if (parts && (!workspace || workspace_bytes < parts * sizeof(double))) return HM_ERR_WORKSPACE;
     if ((ok = hm::check_arch()) != HM_OK) return ok;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    hm::ClipHead head;
+    std::memset(&head, 0, sizeof(head));
+    head.parts = static_cast<int32_t>(parts);
+    head.max_norm = max_norm;
+    head.eps = eps;
+    head.stats = stats;
+    head.partials = static_cast<double*>(workspace);
+    if (live <= hm::kClipFew) {
+        // little data: one launch
+        hm::ClipArgs<hm::kClipFew> a;
+        a.h = head;
+        int64_t chunks = 0;
+        for (int i = 0; i < n && chunks <= hm::kClipFewChunks; ++i)
+            if (tensors[i].n) chunks = add_tensor(a.h, a.t, tensors[i], chunks, hm::kClipFewChunkVecs);
+        a.h.chunks = static_cast<int32_t>(chunks);
+        if (chunks <= hm::kClipFewChunks) return cuda_status(hm::launch_clip_few(a, st));
+    }
     // two passes over the groups of kClipTensors: every norm launch before the first scaling
     for (int pass = 0; pass < 2; ++pass) {
         int i = 0, part0 = 0;
         do {
-            hm::ClipArgs a;
-            std::memset(&a, 0, offsetof(hm::ClipArgs, t));
+            hm::ClipArgs<hm::kClipTensors> a;
+            a.h = head;
             int64_t chunks = 0;
-            for (; i < n && a.n < hm::kClipTensors; ++i) {
-                if (!tensors[i].n) continue;
-                hm::ClipTensor& t = a.t[a.n++];
-                t.src = tensors[i].src;
-                t.dst = tensors[i].dst;
-                t.n = tensors[i].n;
-                t.first = static_cast<int32_t>(chunks);
-                t.f32 = tensors[i].dtype == HM_F32;
-                chunks += hm::clip_chunks(t.src, t.n, t.f32);
-            }
-            a.chunks = static_cast<int32_t>(chunks);
-            a.parts = static_cast<int32_t>(parts);
-            a.part0 = part0;
-            a.max_norm = max_norm;
-            a.eps = eps;
-            a.stats = stats;
-            a.partials = static_cast<double*>(workspace);
-            if (pass == 0) {
-                if (chunks && hm::launch_clip_norm(a, st) != cudaSuccess) return HM_ERR_CUDA;
-            } else if ((chunks || part0 == 0) && hm::launch_clip_scale(a, st) != cudaSuccess) {
-                return HM_ERR_CUDA;
-            }
-            if (chunks) part0 += hm::clip_parts(a.chunks);
+            for (; i < n && a.h.n < hm::kClipTensors; ++i)
+                if (tensors[i].n) chunks = add_tensor(a.h, a.t, tensors[i], chunks, hm::kClipChunkVecs);
+            if (!chunks) break;  // only empty tensors were left
+            a.h.chunks = static_cast<int32_t>(chunks);
+            a.h.part0 = part0;
+            if ((pass == 0 ? hm::launch_clip_norm(a, st) : hm::launch_clip_scale(a, st)) != cudaSuccess) return HM_ERR_CUDA;
+            part0 += hm::clip_parts(a.h.chunks);
         } while (i < n);
     }
     return HM_OK;

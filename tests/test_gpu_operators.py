@@ -648,3 +648,19 @@ def test_product_long_fp32_sums(hm, dev, m, n, k):
     _gemm(hm, qa, ta, qb, tb, m, n, k, d)
     ref = va @ vb.t()
     assert bool(((d.double() - ref).abs() <= ((2560 / 32 + 33) * 2 + k / 2048 + 8) * U * ref).all())
+
+
+@pytest.mark.parametrize("count,n", [(16, 3000), (17, 3000), (1, 2 ** 18), (1, 2 ** 18 + 9), (1, 2 ** 18 + 4096), (3, 400000)])
+@pytest.mark.parametrize("place", ["new", "in", "odd"])
+def test_clip_around_the_one_launch_form(hm, dev, count, n, place):
+    """Tensor counts and sizes on both sides of where one launch does it all: the same values."""
+    rng = np.random.default_rng(n + count)
+    grads = [torch.from_numpy(rng.standard_normal(n - 3 * i).astype(np.float32)) for i in range(count)]
+    ref, _ = OO.clip([_np64(g) for g in grads], 1.0, 1e-6)
+    before = hm.hm_kernel_launches()
+    outs, norm, coef = _clip(hm, dev, grads, float(ref) * 0.5, place)
+    few = count <= 16 and 4 * n * count <= 2 ** 20 + 16   # a tail of less than a vector takes no chunk
+    assert hm.hm_kernel_launches() - before == (1 if few else 2) or n == 2 ** 18 + 9
+    assert abs(norm - ref) <= 128 * U * ref and abs(coef - 0.5) <= 130 * U
+    for g, (src, dst, lead, shift, k) in zip(grads, outs):
+        assert _same_bits(dst[shift:shift + k], g.to(dev) * torch.tensor(coef, device=dev))
