@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                     umma_mx_pair(d, pd + 2 * kk, qd + 2 * kk, mx_idesc(256, BN) | sf_id(kk), tsf,
                                                  tsf + 4 + sfq_col, (kb - kb0) | kk);
                             umma_commit_pair(smem_u32(&empty[s]));
-                            if (kb + 1 == kb1) umma_commit_pair(smem_u32(&tfull[u & 1]));
+                            if (kb + 1 == kb1 && !p.inject) umma_commit_pair(smem_u32(&tfull[u & 1]));
                         }
                         __syncwarp();
                         slot ^= 1;
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         }
         // also covers every MMA issued before an early exit
         if (elect_one()) {
-            umma_commit(smem_u32(tfull));
+            if (!p.inject) umma_commit(smem_u32(tfull));
             mbar_wait(smem_u32(tfull), 0, p.err, bail, false);
         }
     }
@@ -854,6 +854,7 @@ cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int6
     p.num_kb = (p.k + kTileK - 1) / kTileK;
     p.last_nk = (p.k - (p.num_kb - 1) * kTileK) / 32;
     p.err = device_error_word();
+    p.inject = inject_mx_timeout();
     // fp32 D over a K that eight parts of kSplitSumKb stages do not cover: the pair kernel's sums
     const bool long_sum = p.d_f32 && p.num_kb > kMaxSplit * kSplitSumKb;
     if (!long_sum) {

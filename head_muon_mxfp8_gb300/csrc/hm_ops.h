@@ -21,8 +21,13 @@ struct MxGemmArgs {
     int32_t last_nk;     // blocks of 32 in the last stage
     int32_t tiles_p, tiles_q;  // pair kernel: tiles along n and m
     int32_t split;       // CTAs of a cluster that share K
+    int32_t inject;      // failure test: never signal an accumulator as ready
     int32_t* err;
 };
+// Failure-detection test hook: HM_INJECT_MX_WAIT_TIMEOUT=1 in the environment makes
+// the waits of the product and of the norm's gradient run out (bounded), so that
+// they record HM_ERR_TIMEOUT.
+bool inject_mx_timeout();
 cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, const MxGemmArgs& args,
                            cudaStream_t st);
 
@@ -70,6 +75,7 @@ struct RmsGradArgs {
     float* dgamma;
     float* partials;     // [CTAs][d]
     int32_t stages;      // rows in flight per CTA (set by launch_rmsnorm_grad, as err)
+    int32_t inject;      // failure test: never load a row
     int32_t* err;
 };
 // CTAs (= partial rows of dgamma) that launch_rmsnorm_grad uses, at most

@@ -4,7 +4,7 @@
 #include "hm_internal.h"
 #include "hm_ops.h"
 
-#include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 namespace {
@@ -37,6 +37,11 @@ constexpr int64_t kMaxDim = INT32_MAX - 256;   // tile coordinates and row count
 constexpr int64_t kMaxPitch = int64_t(1) << 40;  // byte offsets of any element stay in 63 bits
 
 }  // namespace
+
+bool hm::inject_mx_timeout() {
+    const char* v = std::getenv("HM_INJECT_MX_WAIT_TIMEOUT");
+    return v && v[0] == '1';
+}
 
 extern "C" hm_status mxfp8_tiled_scale_bytes(int64_t rows, int64_t k, size_t* bytes) {
     if (!bytes || rows < 0 || k < 0) return HM_ERR_ARG;

@@ -42,29 +42,42 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// Suspends the thread up to 20 us (it resumes when the phase completes): with the
-// default limit the waiting warps of an MXFP8 product polled enough to cost 0.8 % of
-// its rate under the power cap.
+// PARK: the thread may be suspended up to 20 us (it resumes when the phase
+// completes) instead of the short default.  Fewer polls by the waiting warps of an
+// MXFP8 product gave 0.8 % of its rate under the power cap (weight gradient 93.2 ->
+// 91.3 us); where all threads of a CTA wait for a row the short polls are faster
+// (norm gradient 55.0 us against 57.8).
+template <bool PARK = true>
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if (PARK)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 // Bounded wait.  Gives up when another role of the CTA has given up (bail)
 // or after kWaitNs; the first give-up records HM_ERR_TIMEOUT.
+template <bool PARK = true>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t* err, volatile int* bail,
                                           bool honour_bail = true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait<PARK>(bar, parity)) return true;
     const unsigned long long t0 = globaltimer();
     while (true) {
         for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+            if (mbar_try_wait<PARK>(bar, parity)) return true;
         if (honour_bail && *bail) return false;
         if (globaltimer() - t0 > kWaitNs) {
             *bail = 1;

@@ -664,3 +664,51 @@ def test_clip_around_the_one_launch_form(hm, dev, count, n, place):
     assert abs(norm - ref) <= 128 * U * ref and abs(coef - 0.5) <= 130 * U
     for g, (src, dst, lead, shift, k) in zip(grads, outs):
         assert _same_bits(dst[shift:shift + k], g.to(dev) * torch.tensor(coef, device=dev))
+
+
+@pytest.mark.parametrize("which", ["pair", "sums", "split", "one", "norm_grad"])
+def test_injected_wait_timeout_is_reported_and_recovered(hm, dev, which):
+    """An accumulator that is never marked ready (pair: CTA pairs, sums: with K in chunks, split:
+    a cluster per tile, one: a CTA per tile), or rows that never arrive: the bounded waits
+    give up, record HM_ERR_TIMEOUT and return; the next call is right."""
+    import os
+    rng = np.random.default_rng(5)
+    if which == "norm_grad":
+        rows, d = 40, 2048
+        dy, h = (torch.randn(rows, d, device=dev) for _ in range(2))
+        gamma, rstd = torch.ones(d, device=dev), torch.ones(rows, device=dev)
+        dx, dg = torch.zeros(rows, d, device=dev), torch.zeros(d, device=dev)
+        ws = torch.empty(hm.rmsnorm_backward_workspace(rows, d), dtype=torch.uint8, device=dev)
+        ref = OO.rms_norm_grad(_np64(dy), _np64(h), _np64(gamma), _np64(rstd))[0]
+
+        def call():
+            hm.rmsnorm_backward(dy.data_ptr(), d, 0, h.data_ptr(), dx.data_ptr(), d, hm.HM_F32, rows, d, gamma.data_ptr(),
+                                rstd.data_ptr(), dg.data_ptr(), False, ws.data_ptr(), ws.numel())
+
+        def right():
+            return np.allclose(_np64(dx), ref, rtol=1e-5, atol=1e-4)
+    else:
+        m, n, k, t = {"pair": (2304, 3264, 1056, "bf16"), "sums": (1024, 6400, 2208, "f32"), "split": (5, 256, 2048, "f32"),
+                      "one": (5, 256, 64, "f32")}[which]
+        a = torch.full((m, k), 0x38, dtype=torch.uint8, device=dev)   # 1.0
+        b = torch.full((n, k), 0x38, dtype=torch.uint8, device=dev)
+        sa, sb = (torch.full((hm.mxfp8_tiled_scale_bytes(r, k),), 127, dtype=torch.uint8, device=dev) for r in (m, n))
+        d = torch.zeros(m, n, dtype=_dt(hm, t)[0], device=dev)
+
+        def call():
+            _gemm(hm, a, sa, b, sb, m, n, k, d)
+
+        def right():
+            return bool((d == k).all())
+    assert hm.hm_device_error() == 0
+    os.environ["HM_INJECT_MX_WAIT_TIMEOUT"] = "1"
+    try:
+        call()
+        torch.cuda.synchronize()                  # returns: the waits are bounded
+    finally:
+        del os.environ["HM_INJECT_MX_WAIT_TIMEOUT"]
+    assert hm.hm_device_error() == hm.HM_ERR_TIMEOUT
+    assert hm.hm_device_error() == 0              # read-and-clear
+    call()
+    torch.cuda.synchronize()
+    assert hm.hm_device_error() == 0 and right()
