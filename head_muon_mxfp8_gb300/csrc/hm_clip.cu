@@ -203,8 +203,8 @@ __device__ __forceinline__ float coefficient(const ClipHead& h, double sum, bool
     // one rounding of the sum and the root's in fp32 wherever it holds the sum
     const float f = static_cast<float>(sum);
     const float norm = f >= 0x1p-100f && f <= 0x1p100f ? sqrtf(f) : static_cast<float>(sqrt(sum));
-    const float c = h.max_norm / (norm + h.eps);
-    const float coef = c >= 1.f ? 1.f : c;  // a NaN stays
+    // a NaN norm compares false and stays; an infinite max_norm never clips
+    const float coef = norm + h.eps <= h.max_norm ? 1.f : h.max_norm / (norm + h.eps);
     if (write) {
         h.stats[0] = norm;
         h.stats[1] = coef;

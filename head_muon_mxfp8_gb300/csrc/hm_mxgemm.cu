@@ -708,18 +708,6 @@ bool map_scales(CUtensorMap* m, const uint8_t* base, int num_kb, int64_t rows, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class Kernel>
-cudaError_t allow_smem(Kernel kernel, int bytes, bool (&done)[64]) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) done[dev] = true;
-    }
-    return cudaSuccess;
-}
-
 template <int BN>
 void split_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int tiles_p, int tiles_q, int split, cudaStream_t st) {
     cfg = {};
@@ -786,7 +774,7 @@ int split_for(int tiles_p, int tiles_q, const MxGemmArgs& p, double* cost) {
 
 template <int BN>
 cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, MxGemmArgs p, cudaStream_t st) {
-    static bool done[64] = {false};
+    static PerDevice done;
     cudaError_t e = allow_smem(mx_gemm_split_kernel<BN>, SplitCfg<BN>::SMEM, done);
     if (e != cudaSuccess) return e;
     CUtensorMap ma, mb;
@@ -804,7 +792,7 @@ cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_
 template <int BN, bool SUMS>
 cudaError_t launch_pair(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, MxGemmArgs p, cudaStream_t st) {
     using C = PairMx<BN>;
-    static bool done[64] = {false};
+    static PerDevice done;
     cudaError_t e = allow_smem(mx_gemm_pair_kernel<BN, SUMS>, C::SMEM, done);
     if (e != cudaSuccess) return e;
     CUtensorMap mp, mq, msp, msq;
@@ -880,7 +868,7 @@ cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int6
     // Too few tiles for the pairs: 128 x 128 tiles with K split over clusters.
     const int64_t small_q = (static_cast<int64_t>(p.m) + 127) / 128;
     if (small_q <= 65535 && !long_sum) {
-        static bool done[64] = {false};
+        static PerDevice done;
         const cudaError_t e = allow_smem(mx_gemm_split_kernel<128>, SplitCfg<128>::SMEM, done);  // before its occupancy is asked
         if (e != cudaSuccess) return e;
         double split_cost;

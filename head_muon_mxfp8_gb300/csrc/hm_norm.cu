@@ -466,15 +466,9 @@ template <bool F32, int V, int T, int B>
 cudaError_t launch_grad(RmsGradArgs a, int parts, int stage, cudaStream_t st) {
     constexpr int ring = kGradRing / B;
     a.stages = std::min(kMaxGradStages, ring / stage);
-    static bool done[64] = {false};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(rmsnorm_grad_kernel<F32, V, T, B>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) done[dev] = true;
-    }
+    static PerDevice done;
+    const cudaError_t e = allow_smem(rmsnorm_grad_kernel<F32, V, T, B>, ring, done);
+    if (e != cudaSuccess) return e;
     const int threads = ((a.d / 8 + V - 1) / V + 31) / 32 * 32;
     note_launch();
     rmsnorm_grad_kernel<F32, V, T, B><<<parts, threads, a.stages * stage, st>>>(a);

@@ -3,11 +3,25 @@
 // Not part of the C ABI.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
 
 namespace hm {
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device.
+using PerDevice = std::atomic<bool>[64];
+template <class Kernel>
+inline cudaError_t allow_smem(Kernel kernel, int bytes, PerDevice& done) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && keep) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
 
 struct MxGemmArgs {
     const uint8_t* sa;   // tiled scales

@@ -338,14 +338,10 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
 template <bool F32, bool PACKED, bool COL>
 cudaError_t launch(const QuantArgs& a, cudaStream_t st) {
     constexpr int smem = !COL ? 0 : kQTile * kQTile * (PACKED ? 2 : 4);
-    static bool done[64] = {false};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (smem && (dev < 0 || dev >= 64 || !done[dev])) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(quantize_kernel<F32, PACKED, COL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (smem) {
+        static PerDevice done;
+        const cudaError_t e = allow_smem(quantize_kernel<F32, PACKED, COL>, smem, done);
         if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) done[dev] = true;
     }
     const dim3 grid(static_cast<unsigned>((a.cols + 127) / 128), static_cast<unsigned>((a.rows + 127) / 128));
     note_launch();

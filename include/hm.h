@@ -408,6 +408,10 @@ hm_status reduce_scatter_grad(const hm_chain* chain, const float* parts, int n_p
  * blocks, so every reader of the layout takes both.  Scale rule and rounding
  * are G's.  A NaN quantizes to the NaN code, an infinity to +-448.
  *
+ * None of these calls allocates or synchronises, and each launches only kernels,
+ * so they can be captured into a CUDA graph; make the first call of a kind on a
+ * device outside a capture (its kernels are loaded and configured then).
+ *
  * Bytes of the tiled scales of a [rows][k] operand (k a multiple of 32, else
  * HM_ERR_ALIGN): 512 * ceil(rows / 128) * ceil(k / 128). */
 hm_status mxfp8_tiled_scale_bytes(int64_t rows, int64_t k, size_t* bytes);
@@ -497,7 +501,7 @@ hm_status rmsnorm_backward(const void* dy, int64_t lddy, const void* dres, const
  * order.  A finite gradient has a finite norm unless the norm itself leaves
  * fp32; a NaN makes norm, coef and every dst NaN; an infinite norm gives
  * coef 0 (dst: 0, and NaN where src is infinite).  max_norm > 0 (infinity:
- * never clips), eps >= 0 (HM_ERR_ARG).  dst overlapping its own src other
+ * coef is 1 unless the norm is NaN), eps >= 0 (HM_ERR_ARG).  dst overlapping its own src other
  * than exactly, or any other tensor's memory, is the caller's error.
  * workspace: 16-byte aligned, grad_norm_clip_workspace bytes
  * (HM_ERR_WORKSPACE), contents need not be kept; calls that share one must

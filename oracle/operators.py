@@ -73,5 +73,5 @@ def clip(grads, max_norm, eps):
     """(norm, coefficient) of a list of arrays."""
     with np.errstate(all="ignore"):
         norm = np.sqrt(sum((float(np.sum(np.asarray(g, dtype=np.float64) ** 2)) for g in grads), 0.0))
-        c = np.float64(max_norm) / (norm + eps) if norm + eps != 0 else np.inf
-    return norm, (c if np.isnan(c) else min(1.0, c))
+        c = 1.0 if norm + eps <= max_norm else np.float64(max_norm) / (norm + eps)
+    return norm, c

@@ -712,3 +712,35 @@ def test_injected_wait_timeout_is_reported_and_recovered(hm, dev, which):
     call()
     torch.cuda.synchronize()
     assert hm.hm_device_error() == 0 and right()
+
+
+def test_clip_infinite_max_norm(hm, dev):
+    """An infinite max_norm never clips, whatever the norm; a NaN still shows."""
+    g = torch.ones(100)
+    g[7] = float("inf")
+    outs, norm, coef = _clip(hm, dev, [g], float("inf"), "new")
+    assert np.isinf(norm) and coef == 1.0 and torch.equal(outs[0][1][outs[0][3]:outs[0][3] + 100].cpu(), g)
+    g[8] = float("nan")
+    _, norm, coef = _clip(hm, dev, [g], float("inf"), "new")
+    assert np.isnan(norm) and np.isnan(coef)
+
+
+@pytest.mark.parametrize("factors", [False, True])
+def test_quantize_bf16_nan_inf_and_zeros(hm, dev, factors):
+    """The same special values in bf16, with and without factors."""
+    x = torch.zeros(64, 64, device=dev, dtype=torch.bfloat16)
+    x[0, 0], x[1, 1], x[2, 2] = float("nan"), float("inf"), -float("inf")
+    x[0, 1], x[3, 3] = 1.0, 2.0 ** -133    # the smallest subnormal: 2^-133 2^127 = 2^-6
+    one = torch.ones(64, device=dev)
+    q, s = _poison(dev, 64, 64), _poison(dev, 512)
+    qt, st = _poison(dev, 64, 64), _poison(dev, 512)
+    f = one.data_ptr() if factors else 0
+    hm.mxfp8_quantize(x.data_ptr(), hm.HM_BF16, 64, 64, 64, f, f, 32, q.data_ptr(), 64, s.data_ptr(), qt.data_ptr(), 64,
+                      st.data_ptr())
+    q, qt = q.cpu().numpy(), qt.cpu().numpy()
+    assert q[0, 0] & 0x7F == 0x7F and qt[0, 0] & 0x7F == 0x7F          # NaN stays NaN
+    assert q[0, 1] == 0x78                                              # 1 = 256 * 2^-8
+    assert q[1, 1] == 0x7E and q[2, 2] == 0xFE and qt[1, 1] == 0x7E    # +-448
+    assert q[3, 3] == 0x08 and qt[3, 3] == 0x08                        # 2^-6, the smallest normal code
+    assert (q[4:] == 0).all() and (qt[4:] == 0).all()
+    assert s.cpu().numpy()[4 * 16] == 0
