@@ -177,6 +177,7 @@ __device__ __forceinline__ double end_squares(const ClipTensor& t, const Place& 
 
 __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_constant__ ClipArgs<kClipTensors> a) {
     double sum = 0.0;
+    wait_for_earlier_kernels();
     for (int ch = blockIdx.x; ch < a.h.chunks; ch += gridDim.x) {
         const ClipTensor& t = a.t[find_tensor(a, ch)];
         const Place c = place_of<kChunkVecs>(t, ch);
@@ -265,6 +266,7 @@ __device__ __forceinline__ bool to_scale(const ClipTensor& t, float coef) {
 __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_constant__ ClipArgs<kClipTensors> a) {
     __shared__ float s_coef;
     double sum = 0.0;
+    wait_for_earlier_kernels();
     if (threadIdx.x < 32) {  // one warp: the SM's double units would hold up four CTAs' worth of more
         for (int k = threadIdx.x; k < a.h.parts; k += 32) sum += a.h.partials[k];
 #pragma unroll
@@ -295,6 +297,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads)
     clip_few_kernel(const __grid_constant__ ClipArgs<kClipFew> a) {
     __shared__ double s_part;
     __shared__ float s_coef;
+    wait_for_earlier_kernels();
     const int tid = threadIdx.x % kClipThreads;
     const int group = blockIdx.x + kFewCtas * (threadIdx.x / kClipThreads);
     uint4 x[kFewPerGroup][kFewVecs];
@@ -387,20 +390,17 @@ int clip_parts(int chunks) {
 cudaError_t launch_clip_norm(ClipArgs<kClipTensors>& a, cudaStream_t st) {
     a.h.keep_from = static_cast<int32_t>(std::max<int64_t>(0, a.h.chunks - device_l2_bytes() / 2 / (kChunkVecs * 16)));
     note_launch();
-    clip_norm_kernel<<<clip_parts(a.h.chunks), kClipThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(clip_norm_kernel, clip_parts(a.h.chunks), kClipThreads, 0, st, a);
 }
 
 cudaError_t launch_clip_scale(const ClipArgs<kClipTensors>& a, cudaStream_t st) {
     note_launch();
-    clip_scale_kernel<<<a.h.chunks ? clip_parts(a.h.chunks) : 1, kClipThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(clip_scale_kernel, clip_parts(a.h.chunks), kClipThreads, 0, st, a);
 }
 
 cudaError_t launch_clip_few(const ClipArgs<kClipFew>& a, cudaStream_t st) {
     note_launch();
-    clip_few_kernel<<<kFewCtas, kFewThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(clip_few_kernel, kFewCtas, kFewThreads, 0, st, a);
 }
 
 }  // namespace hm

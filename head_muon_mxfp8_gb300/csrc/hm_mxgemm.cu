@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
+    wait_for_earlier_kernels();
     const uint32_t tmem = *tmem_slot;
     const int total = p.tiles_p * p.tiles_q;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -564,6 +565,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_earlier_kernels();
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0) {
@@ -676,6 +678,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 
 // K = 0: the sum is empty.
 __global__ void __launch_bounds__(256) mx_gemm_zero_kernel(const __grid_constant__ MxGemmArgs p) {
+    wait_for_earlier_kernels();
     const int64_t total = static_cast<int64_t>(p.m) * p.n;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll)
         store_one(p, static_cast<int>(i / p.n), static_cast<int>(i % p.n), 0.f);
@@ -708,19 +711,26 @@ bool map_scales(CUtensorMap* m, const uint8_t* base, int num_kb, int64_t rows, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of `size` CTAs, set up while the kernel before drains (launch_early's rule).
+void cluster_early(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int size) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+}
+
 template <int BN>
-void split_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int tiles_p, int tiles_q, int split, cudaStream_t st) {
+void split_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int tiles_p, int tiles_q, int split, cudaStream_t st) {
     cfg = {};
     cfg.gridDim = dim3(tiles_p * split, tiles_q, 1);
     cfg.blockDim = dim3(kSplitThreads, 1, 1);
     cfg.dynamicSmemBytes = SplitCfg<BN>::SMEM;
     cfg.stream = st;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = split;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cluster_early(cfg, attr, split);
 }
 
 // Clusters of `split` CTAs that run at once, asked once per device.  The query counts
@@ -734,7 +744,7 @@ int resident_clusters(int split) {
     const bool keep = dev >= 0 && dev < 64;
     if (keep && cached[dev][split].load(std::memory_order_relaxed)) return cached[dev][split].load(std::memory_order_relaxed);
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr;
+    cudaLaunchAttribute attr[2];
     split_config<BN>(cfg, attr, 1, 1, split, nullptr);
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_split_kernel<BN>, &cfg) != cudaSuccess || n < 1) {
@@ -783,7 +793,7 @@ cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_
     double cost;
     p.split = split_for<BN>(tiles_p, tiles_q, p, &cost);
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr;
+    cudaLaunchAttribute attr[2];
     split_config<BN>(cfg, attr, tiles_p, tiles_q, p.split, st);
     note_launch();
     return cudaLaunchKernelEx(&cfg, mx_gemm_split_kernel<BN>, ma, mb, p);
@@ -808,13 +818,8 @@ cudaError_t launch_pair(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t
     cfg.blockDim = dim3(kPairThreads, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2];
+    cluster_early(cfg, attr, 2);
     note_launch();
     return cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<BN, SUMS>, mp, mq, msp, msq, p);
 }

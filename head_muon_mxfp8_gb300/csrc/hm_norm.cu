@@ -124,6 +124,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 template <bool F32, int V, bool WARP>
 __global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_kernel(const __grid_constant__ RmsArgs p) {
     __shared__ float red[16];
+    wait_for_earlier_kernels();
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
     const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     const int nv = p.d >> 3;
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(T, B) rmsnorm_grad_kernel(const __grid_constan
         fence_mbar_init();
     }
     __syncthreads();
+    wait_for_earlier_kernels();
     if (threadIdx.x == 0 && !p.inject)
         for (int s = 0; s < stages && s < mine; ++s)
             fill_stage<F32>(p, ring + s * stage_bytes, &full[s], blockIdx.x + static_cast<int64_t>(s) * gridDim.x);
@@ -331,6 +333,7 @@ template <bool F32, int V>
 __global__ void __launch_bounds__(32 * kWarpRows) rmsnorm_grad_warp_kernel(const __grid_constant__ RmsGradArgs p) {
     __shared__ __align__(16) float part[kWarpRows][V * 256];
     constexpr bool kAhead = V <= 2;
+    wait_for_earlier_kernels();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nv = p.d >> 3;
     float dg[V][8], gamma[V][8];
@@ -428,6 +431,7 @@ __global__ void __launch_bounds__(32 * kWarpRows) rmsnorm_grad_warp_kernel(const
 __global__ void __launch_bounds__(1024) dgamma_kernel(const float* __restrict__ partials, int parts, int d,
                                                       int accumulate, float* __restrict__ dgamma) {
     __shared__ float red[32][33];
+    wait_for_earlier_kernels();
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + c;
     float s = 0.f;
@@ -449,17 +453,16 @@ cudaError_t launch_fwd(const RmsArgs& a, cudaStream_t st) {
     note_launch();
     if (a.d <= kWarpMaxD) {
         const unsigned grid = rows / kWarpRows;
-        if (a.d <= 256) rmsnorm_kernel<F32, 1, true><<<grid, 32 * kWarpRows, 0, st>>>(a);
-        else if (a.d <= 512) rmsnorm_kernel<F32, 2, true><<<grid, 32 * kWarpRows, 0, st>>>(a);
-        else rmsnorm_kernel<F32, 4, true><<<grid, 32 * kWarpRows, 0, st>>>(a);
+        if (a.d <= 256) return launch_early(rmsnorm_kernel<F32, 1, true>, grid, 32 * kWarpRows, 0, st, a);
+        else if (a.d <= 512) return launch_early(rmsnorm_kernel<F32, 2, true>, grid, 32 * kWarpRows, 0, st, a);
+        else return launch_early(rmsnorm_kernel<F32, 4, true>, grid, 32 * kWarpRows, 0, st, a);
     } else {
         // two vectors per thread up to 8192 columns (8192 x 4096 bf16: 40.9 us with one, 30.8 with two)
         const int v = a.d <= 8192 ? 2 : 4;
         const int threads = ((a.d / 8 + v - 1) / v + 31) / 32 * 32;
-        if (v == 2) rmsnorm_kernel<F32, 2, false><<<rows, threads, 0, st>>>(a);
-        else rmsnorm_kernel<F32, 4, false><<<rows, threads, 0, st>>>(a);
+        if (v == 2) return launch_early(rmsnorm_kernel<F32, 2, false>, rows, threads, 0, st, a);
+        else return launch_early(rmsnorm_kernel<F32, 4, false>, rows, threads, 0, st, a);
     }
-    return cudaGetLastError();
 }
 
 template <bool F32, int V, int T, int B>
@@ -471,8 +474,7 @@ cudaError_t launch_grad(RmsGradArgs a, int parts, int stage, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int threads = ((a.d / 8 + V - 1) / V + 31) / 32 * 32;
     note_launch();
-    rmsnorm_grad_kernel<F32, V, T, B><<<parts, threads, a.stages * stage, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(rmsnorm_grad_kernel<F32, V, T, B>, parts, threads, a.stages * stage, st, a);
 }
 
 template <bool F32>
@@ -490,10 +492,10 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
         cudaError_t e = cudaSuccess;
         if (a.d <= kWarpMaxD) {
             note_launch();
-            if (a.d <= 256) rmsnorm_grad_warp_kernel<F32, 1><<<parts, 32 * kWarpRows, 0, st>>>(a);
-            else if (a.d <= 512) rmsnorm_grad_warp_kernel<F32, 2><<<parts, 32 * kWarpRows, 0, st>>>(a);
-            else rmsnorm_grad_warp_kernel<F32, 4><<<parts, 32 * kWarpRows, 0, st>>>(a);
-            e = cudaGetLastError();
+            const auto kernel = a.d <= 256   ? rmsnorm_grad_warp_kernel<F32, 1>
+                                : a.d <= 512 ? rmsnorm_grad_warp_kernel<F32, 2>
+                                             : rmsnorm_grad_warp_kernel<F32, 4>;
+            e = launch_early(kernel, parts, 32 * kWarpRows, 0, st, a);
         } else if (a.d <= 4096) e = two ? launch_grad<F32, 1, 512, 2>(a, parts, stage, st) : launch_grad<F32, 1, 512, 1>(a, parts, stage, st);
         else if (a.d <= 5120 && two) e = launch_grad<F32, 2, 320, 2>(a, parts, stage, st);
         else if (a.d <= 8192) e = two ? launch_grad<F32, 2, 512, 2>(a, parts, stage, st) : launch_grad<F32, 2, 512, 1>(a, parts, stage, st);
@@ -501,8 +503,7 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     note_launch();
-    dgamma_kernel<<<a.d / 32, 1024, 0, st>>>(a.partials, parts, a.d, a.accumulate, a.dgamma);
-    return cudaGetLastError();
+    return launch_early(dgamma_kernel, a.d / 32, 1024, 0, st, a.partials, parts, a.d, a.accumulate, a.dgamma);
 }
 
 }  // namespace

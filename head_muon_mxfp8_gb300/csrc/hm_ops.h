@@ -23,6 +23,26 @@ inline cudaError_t allow_smem(Kernel kernel, int bytes, PerDevice& done) {
     return e;
 }
 
+// A launch that may be set up while the kernel before it drains; the kernel calls
+// wait_for_earlier_kernels() before it touches global memory.  One call after
+// another: RMS norm 8192 x 5120 49.0 -> 46.0 us, its gradient (two kernels) 59.9 ->
+// 54.8, quantization 8192 x 15360 81.9 -> 79.6, clipping of 200,000 elements 10.2 ->
+// 8.2.
+template <class... Params, class... Args>
+inline cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t st, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct MxGemmArgs {
     const uint8_t* sa;   // tiled scales
     const uint8_t* sb;

@@ -20,6 +20,10 @@ __device__ __forceinline__ unsigned long long globaltimer() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
+// Waits until the kernels before this one in the stream have finished and their
+// writes are visible (launch_early); nothing before it may touch global memory
+// that they write.
+__device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // True in one lane of a converged warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;

@@ -16,6 +16,7 @@
 #include "hm_internal.h"
 #include "hm_mx_device.cuh"
 #include "hm_ops.h"
+#include "hm_ptx.cuh"
 
 namespace hm {
 
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
     __shared__ __align__(16) uint8_t s_row[512];
     __shared__ __align__(16) uint8_t s_col[512];
     __shared__ float amax_col[4][kQTile];
+    wait_for_earlier_kernels();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t ct = blockIdx.x, rt = blockIdx.y;
     const int64_t r0 = rt * kQTile, c0 = ct * kQTile;
@@ -345,8 +347,7 @@ cudaError_t launch(const QuantArgs& a, cudaStream_t st) {
     }
     const dim3 grid(static_cast<unsigned>((a.cols + 127) / 128), static_cast<unsigned>((a.rows + 127) / 128));
     note_launch();
-    quantize_kernel<F32, PACKED, COL><<<grid, kQThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(quantize_kernel<F32, PACKED, COL>, grid, kQThreads, smem, st, a);
 }
 
 }  // namespace
