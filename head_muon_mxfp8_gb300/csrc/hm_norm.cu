@@ -105,16 +105,29 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum over the block, the same in every thread: warp sums, then every thread
-// adds the warps' in order.
+// Sum over the block, the same in every thread: warp sums, then the same tree
+// over them in every warp.
 __device__ __forceinline__ float block_sum(float v, float* red) {
     v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    float t = 0.f;
-    const int warps = blockDim.x >> 5;
-    for (int k = 0; k < warps; ++k) t += red[k];
-    return t;
+    return warp_sum((threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : 0.f);
+}
+
+// 1 / sqrt(sum / d + eps), off by little more than its own rounding: the quotient's
+// and the sum's remainders are carried along (a product's or a quotient's remainder
+// is one fma), and one Newton step on 1/sqrt removes its error.  Four roundings
+// in a row instead moved 1.5 times as many codes off their 64-bit values.
+__device__ __forceinline__ float inv_root(float sum, float d, float eps) {
+    const float q = sum / d;
+    const float a = q + eps;
+    if (!(a >= 0x1p-100f && a <= 0x1p100f)) return 1.0f / sqrtf(a);  // the step below would leave fp32
+    const float big = fmaxf(q, eps), small = fminf(q, eps);
+    const float low = (small - (a - big)) + fmaf(-q, d, sum) / d;  // sum / d + eps - a
+    const float y = rsqrtf(a);
+    const float t = a * y;
+    const float e = fmaf(-t, y, 1.0f) - fmaf(fmaf(a, y, -t), y, low * y * y);  // 1 - (a + low) y^2
+    return fmaf(0.5f * e, y, y);
 }
 
 // A row per CTA, or per warp (8 rows per CTA) where a row has at most 1024
@@ -136,7 +149,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_kernel(const __grid_co
         return;
     }
     float h[V][8];
-    float sq = 0.f;
+    float sq = 0.f;  // pairs first, so that no chain of additions is longer than V
     Vec8<F32> x[V], r[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -158,11 +171,13 @@ __global__ void __launch_bounds__(kMaxRowThreads) rmsnorm_kernel(const __grid_co
                 for (int k = 0; k < 8; ++k) h[i][k] += rv[k];
             }
             Vec8<F32>::round(p.h, row * p.ldh + j * 8, h[i]);
+            float p4[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sq = fmaf(h[i][k], h[i][k], sq);
+            for (int k = 0; k < 4; ++k) p4[k] = fmaf(h[i][2 * k + 1], h[i][2 * k + 1], h[i][2 * k] * h[i][2 * k]);
+            sq += (p4[0] + p4[1]) + (p4[2] + p4[3]);
         }
     }
-    const float rstd = 1.0f / sqrtf((WARP ? warp_sum(sq) : block_sum(sq, red)) / static_cast<float>(p.d) + p.eps);
+    const float rstd = inv_root(WARP ? warp_sum(sq) : block_sum(sq, red), static_cast<float>(p.d), p.eps);
     if (t == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
