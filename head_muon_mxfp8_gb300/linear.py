@@ -44,6 +44,15 @@ def _ptr(t: Optional[torch.Tensor]) -> int:
     return t.data_ptr() if t is not None else 0
 
 
+def _need(name: str, t, shape: Tuple[int, int], dtype, device) -> None:
+    """The kernels take addresses: t has to be what they will read there."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor is expected, not {type(t).__name__}")
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor {list(shape)} on {device} is expected, not {t.dtype} "
+                         f"{list(t.shape)} with strides {list(t.stride())} on {t.device}")
+
+
 class NormLinear:
     def __init__(self, tokens: int, d_in: int, d_out: int, eps: float = 1e-5, block: int = 32, device="cuda"):
         if d_in % 32 or d_out % 32:
@@ -76,6 +85,9 @@ class NormLinear:
         self.session.m.zero_()
 
     def load_weight(self, w: torch.Tensor) -> None:
+        """w [d_out][d_in], any floating type, layout and device (ValueError for another shape)."""
+        if tuple(w.shape) != (self.d_out, self.d_in):
+            raise ValueError(f"w: [{self.d_out}, {self.d_in}] is expected, not {list(w.shape)}")
         self.w.copy_(w)
         abi.mxfp8_requant_packed(_ptr(self.w), _ptr(self._q), _ptr(self._s), [(0, 0, 0, self.d_out, self.d_in)], _stream())
         self._weight_operands()
@@ -87,7 +99,11 @@ class NormLinear:
                            self.wt.k, _ptr(self.wt.s), _stream())
 
     def forward(self, x: torch.Tensor, res: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
-        """x, res: bf16 [tokens][d_in], contiguous -> (y bf16 [tokens][d_out], h = x + res)."""
+        """x, res: bf16 [tokens][d_in], contiguous -> (y bf16 [tokens][d_out], h = x + res).
+        Other shapes, types, layouts and devices are refused (ValueError), here and in backward."""
+        for name, t in (("x", x), ("res", res)):
+            if t is not None or name == "x":
+                _need(name, t, (self.tokens, self.d_in), torch.bfloat16, self.gamma.device)
         st, d = _stream(), self.d_in
         abi.rmsnorm_mxfp8(_ptr(x), d, _ptr(res), _ptr(self.h), d, abi.HM_BF16, self.tokens, d, _ptr(self.gamma), self.eps,
                           self.block, _ptr(self.rstd), _ptr(self.x8.q), _ptr(self.x8.s), st)
@@ -97,6 +113,9 @@ class NormLinear:
 
     def backward(self, dy: torch.Tensor, dres: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """dy bf16 [tokens][d_out], dres bf16 [tokens][d_in] -> (dx, dgamma); adds dW to self.g."""
+        _need("dy", dy, (self.tokens, self.d_out), torch.bfloat16, self.gamma.device)
+        if dres is not None:
+            _need("dres", dres, (self.tokens, self.d_in), torch.bfloat16, self.gamma.device)
         st, m, k, n = _stream(), self.tokens, self.d_in, self.d_out
         abi.mxfp8_quantize(_ptr(dy), abi.HM_BF16, m, n, n, 0, 0, self.block, _ptr(self.dy8.q), self.dy8.k, _ptr(self.dy8.s),
                            _ptr(self.dyt8.q), self.dyt8.k, _ptr(self.dyt8.s), st)
