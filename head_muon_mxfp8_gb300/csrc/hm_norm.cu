@@ -93,9 +93,11 @@ struct Vec8<false> {
     }
 };
 
+// (Ordinary loads: gamma, rstd and the partials may come from the kernel right
+// before, which still runs when these start.)
 __device__ __forceinline__ void load_f8(const float* p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = reinterpret_cast<const float4*>(p)[0];
+    const float4 b = reinterpret_cast<const float4*>(p)[1];
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
@@ -269,12 +271,12 @@ __global__ void __launch_bounds__(T, B) rmsnorm_grad_kernel(const __grid_constan
     const float inv_d = 1.0f / static_cast<float>(p.d);
     int s = 0;
     uint32_t ph = 0;
-    float rstd_next = mine > 0 ? __ldg(p.rstd + blockIdx.x) : 0.f;
+    float rstd_next = mine > 0 ? p.rstd[blockIdx.x] : 0.f;
     int64_t it = 0;
     for (; it < mine; ++it) {
         const int64_t row = blockIdx.x + it * gridDim.x;
         const float rstd = rstd_next;
-        if (it + 1 < mine) rstd_next = __ldg(p.rstd + row + gridDim.x);
+        if (it + 1 < mine) rstd_next = p.rstd[row + gridDim.x];
         const int ok = mbar_wait<false>(smem_u32(&full[s]), ph, p.err, bail);
         const uint8_t* stage = ring + s * stage_bytes;
         Vec8<F32> dy[V], h[V], dr[V];
@@ -380,13 +382,13 @@ __global__ void __launch_bounds__(32 * kWarpRows) rmsnorm_grad_warp_kernel(const
     float rstd1 = 0.f;
     if (row < p.rows) {
         fetch(row, dy, h, dr);
-        rstd1 = __ldg(p.rstd + row);
+        rstd1 = p.rstd[row];
     }
     for (; row < p.rows; row += step) {
         const float rstd = rstd1;
         const bool more = row + step < p.rows;
         if (more) {
-            rstd1 = __ldg(p.rstd + row + step);
+            rstd1 = p.rstd[row + step];
             if (kAhead) fetch(row + step, dy1, h1, dr1);
         }
         float dot = 0.f;
@@ -446,8 +448,8 @@ __global__ void __launch_bounds__(32 * kWarpRows) rmsnorm_grad_warp_kernel(const
 
 // dgamma from the CTAs' partials: 32 columns per CTA, 32 threads per column each
 // adding every 32nd partial in order, then the 32 in order.
-__global__ void __launch_bounds__(1024) dgamma_kernel(const float* __restrict__ partials, int parts, int d,
-                                                      int accumulate, float* __restrict__ dgamma) {
+__global__ void __launch_bounds__(1024) dgamma_kernel(const float* partials, int parts, int d, int accumulate,
+                                                      float* dgamma) {
     __shared__ float red[32][33];
     wait_for_earlier_kernels();
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;

@@ -24,7 +24,9 @@ inline cudaError_t allow_smem(Kernel kernel, int bytes, PerDevice& done) {
 }
 
 // A launch that may be set up while the kernel before it drains; the kernel calls
-// wait_for_earlier_kernels() before it touches global memory.  One call after
+// wait_for_earlier_kernels() before it touches global memory, and reads it with
+// ordinary loads: the read-only path (__ldg, const __restrict__) is for data that
+// nobody writes while the kernel runs.  One call after
 // another: RMS norm 8192 x 5120 49.0 -> 46.0 us, its gradient (two kernels) 59.9 ->
 // 54.8, quantization 8192 x 15360 81.9 -> 79.6, clipping of 200,000 elements 10.2 ->
 // 8.2.

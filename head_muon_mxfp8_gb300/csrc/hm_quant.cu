@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
         if (p.col_vec && left == 16) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(p.col_mul + c0 + c16) + k);
+                const float4 f = reinterpret_cast<const float4*>(p.col_mul + c0 + c16)[k];
                 cm[4 * k] = f.x; cm[4 * k + 1] = f.y; cm[4 * k + 2] = f.z; cm[4 * k + 3] = f.w;
             }
         } else {
