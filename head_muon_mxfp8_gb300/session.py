@@ -8,6 +8,7 @@ host data into the segments and back (`load` / `fetch`) is test and bench
 set-up, done with plain tensor copies."""
 from __future__ import annotations
 
+from collections import OrderedDict
 from typing import Dict, Optional, Sequence, Tuple
 
 import numpy as np
@@ -41,6 +42,8 @@ def aligned_empty(nbytes: int, device, align: int = 1024) -> Tuple[torch.Tensor,
 
 
 class MuonSession:
+    CLIP_LISTS = 8   # (tensor list, stream) pairs whose clipping buffers are kept
+
     def __init__(self, numel: int, units: Sequence[Tuple[int, int, int]], so: int, sw: int, sg: int,
                  device="cuda", edges: Optional[Sequence[int]] = None,
                  edge_shift: Optional[Sequence[int]] = None, canaries: bool = True):
@@ -74,7 +77,7 @@ class MuonSession:
         self.ws_bytes = int(self.info.workspace_bytes)
         self._ws_buf, self.ws = aligned_empty(self.ws_bytes, dev)
         abi.muon_plan_upload(self.plan, self.ws, self.ws_bytes, _stream_handle(None))
-        self._clip = None
+        self._clip = OrderedDict()
         self.bufs = abi.hm_muon_bufs(self.w.data_ptr(), self.m.data_ptr(), self.g.data_ptr(), self.u.data_ptr(),
                                      self.v.data_ptr(), self.q.data_ptr(), self.s.data_ptr())
 
@@ -168,13 +171,28 @@ class MuonSession:
                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """Clips the main gradient (or the given (src, dst, elements, dtype) entries) by its
         global norm, between the reduce-scatter and the update.  Returns the device
-        tensor (norm, coefficient) of the last call; canary gaps are not touched."""
-        key = tuple(tensors) if tensors is not None else None
-        if self._clip is None or self._clip[0] != key:
+        tensor (norm, coefficient) of the last call for these tensors on this stream; canary
+        gaps are not touched.
+
+        Everything runs on `stream` (the current one by default): the workspace and the
+        result are that stream's own memory, so no work of another stream can still be
+        using it or be handed it, and nothing is enqueued anywhere else.  Ordering `stream`
+        after what wrote the gradient, and readers of the result after `stream`, is the
+        caller's.  Buffers are kept for the last CLIP_LISTS pairs of list and stream; a CUDA
+        graph that holds such a call needs its pair to stay among them."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        key = (tuple(tensors) if tensors is not None else None, _stream_handle(stream))
+        if key not in self._clip:
             lst = abi.grad_list(list(tensors) if tensors is not None else self.grad_list())
-            ws = torch.empty(max(16, abi.grad_norm_clip_workspace(lst)), dtype=torch.uint8, device=self.device)
-            self._clip = (key, lst, ws, torch.zeros(2, dtype=torch.float32, device=self.device))
-        _, lst, ws, stats = self._clip
+            with torch.cuda.stream(stream):   # the kernels write both values of the result
+                ws = torch.empty(max(16, abi.grad_norm_clip_workspace(lst)), dtype=torch.uint8, device=self.device)
+                stats = torch.empty(2, dtype=torch.float32, device=self.device)
+            self._clip[key] = (lst, ws, stats)
+            if len(self._clip) > self.CLIP_LISTS:
+                self._clip.popitem(last=False)
+        self._clip.move_to_end(key)
+        lst, ws, stats = self._clip[key]
         abi.grad_norm_clip(lst, max_norm, eps, stats.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle(stream))
         return stats
 

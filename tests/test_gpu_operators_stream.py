@@ -57,3 +57,56 @@ def test_chain_gives_the_bits_of_separate_calls(hm, dev, rows, d):
     want = run(True)
     for _ in range(3):
         assert all(np.array_equal(a, b) for a, b in zip(run(False), want))
+
+
+def _session(dev):
+    import workloads
+    from head_muon_mxfp8_gb300.session import MuonSession
+    cfg = workloads.get("tiny_ragged")
+    s = MuonSession.from_config(cfg, device=dev)
+    data = workloads.generate(cfg, seed=4)
+    s.load("g", data["g"])
+    torch.cuda.synchronize()
+    return s, np.asarray(data["g"], dtype=np.float64)
+
+
+def test_clip_on_another_stream_while_the_current_one_is_behind(hm, dev):
+    """The current stream is busy, with memory to free and fill behind that: nothing that it
+    still has to do reaches the clipping's result or its sums."""
+    s, g = _session(dev)
+    side = torch.cuda.Stream()
+    norm = np.sqrt((g * g).sum())
+    held = [torch.ones(64, dtype=torch.uint8, device=dev) for _ in range(64)]   # small blocks to be reused
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    for t in held:
+        t.fill_(0xFF)
+    del held, t
+    stats = s.clip_grad_norm(float(norm) * 0.25, stream=side)
+    side.synchronize()
+    with torch.cuda.stream(side):
+        early = stats.clone()
+    torch.cuda.synchronize()
+    for got in (early.cpu().numpy(), stats.cpu().numpy()):
+        assert abs(got[0] - norm) < 1e-5 * norm and abs(got[1] - 0.25) < 1e-5
+    assert np.array_equal(s.fetch("g").numpy(), g.astype(np.float32) * stats.cpu().numpy()[1])
+    s.close()
+
+
+def test_clip_with_two_lists_on_two_streams(hm, dev):
+    """Two lists in turn on two streams, nothing waiting in between: every result is its own."""
+    s, _ = _session(dev)
+    a = torch.randn(300_001, device=dev)
+    b = torch.randn(1_700_000, device=dev)
+    lists = [[(t.data_ptr(), 0, t.numel(), hm.HM_F32)] for t in (a, b)]
+    want = [float(t.double().norm()) for t in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for k in range(20):
+        got.append((k % 2, s.clip_grad_norm(1.0, tensors=lists[k % 2], stream=streams[(k // 2) % 2])))
+    torch.cuda.synchronize()
+    assert len({t.data_ptr() for _, t in got}) == 4
+    for which, t in got:
+        assert abs(float(t[0]) - want[which]) < 1e-5 * want[which]
+    s.close()
