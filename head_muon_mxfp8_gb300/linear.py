@@ -5,7 +5,7 @@ gradient lands in the session's main gradient.
     layer = NormLinear(tokens=4096, d_in=5120, d_out=15360)
     layer.load_weight(w)                       # fp32 main weight [d_out][d_in]
     y, h = layer.forward(x, res)               # h = x + res, y = norm(h) W^T
-    dx, dgamma = layer.backward(dy, dres)      # dW is added to the main gradient
+    dx, dgamma = layer.backward(dy, dres)      # dW and dgamma add up until the next step()
     layer.step(muon_hparams, max_norm=1.0)     # clip, Muon update, requantize
 
 Buffers are allocated once; every computation runs in libhm's kernels on the
@@ -54,6 +54,8 @@ def _need(name: str, t, shape: Tuple[int, int], dtype, device) -> None:
 
 
 class NormLinear:
+    _summed = False   # whether dgamma holds a backward pass since the gradients were cleared
+
     def __init__(self, tokens: int, d_in: int, d_out: int, eps: float = 1e-5, block: int = 32, device="cuda"):
         if d_in % 32 or d_out % 32:
             raise ValueError("d_in and d_out are multiples of 32 (MX blocks)")
@@ -81,8 +83,14 @@ class NormLinear:
         self.dx = torch.empty(tokens, d_in, **bf16)
         self._ws = torch.empty(abi.rmsnorm_backward_workspace(tokens, d_in), dtype=torch.uint8, device=dev)
         self._clip = self.session.grad_list() + [(_ptr(self.dgamma), _ptr(self.dgamma), d_in, abi.HM_F32)]
-        self.g.zero_()
+        self.zero_grad()
         self.session.m.zero_()
+
+    def zero_grad(self) -> None:
+        """Starts the gradients of a new step: clears dW; the next backward pass overwrites
+        dgamma (which stays readable until then) and later ones add to it."""
+        self.g.zero_()
+        self._summed = False
 
     def load_weight(self, w: torch.Tensor) -> None:
         """w [d_out][d_in], any floating type, layout and device (ValueError for another shape)."""
@@ -112,7 +120,8 @@ class NormLinear:
         return self.y, self.h
 
     def backward(self, dy: torch.Tensor, dres: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
-        """dy bf16 [tokens][d_out], dres bf16 [tokens][d_in] -> (dx, dgamma); adds dW to self.g."""
+        """dy bf16 [tokens][d_out], dres bf16 [tokens][d_in] -> (dx, dgamma).  Adds dW to
+        self.g and dgamma to self.dgamma, so several micro-batches make one step's gradient."""
         _need("dy", dy, (self.tokens, self.d_out), torch.bfloat16, self.gamma.device)
         if dres is not None:
             _need("dres", dres, (self.tokens, self.d_in), torch.bfloat16, self.gamma.device)
@@ -127,18 +136,19 @@ class NormLinear:
         abi.mxfp8_gemm(_ptr(self.dyt8.q), self.dyt8.k, _ptr(self.dyt8.s), _ptr(self.xt8.q), self.xt8.k, _ptr(self.xt8.s), n,
                        k, self.dyt8.k, _ptr(self.g), k, abi.HM_F32, True, st)
         abi.rmsnorm_backward(_ptr(self.dn), k, _ptr(dres), _ptr(self.h), _ptr(self.dx), k, abi.HM_BF16, m, k,
-                             _ptr(self.gamma), _ptr(self.rstd), _ptr(self.dgamma), False, _ptr(self._ws), self._ws.numel(),
-                             st)
+                             _ptr(self.gamma), _ptr(self.rstd), _ptr(self.dgamma), self._summed, _ptr(self._ws),
+                             self._ws.numel(), st)
+        self._summed = True
         return self.dx, self.dgamma
 
     def step(self, hp: "abi.hm_muon_hparams", max_norm: float = 1.0) -> torch.Tensor:
         """Clips dW and dgamma by their global norm, runs the Muon update of W (which requantizes
-        it) and clears the main gradient.  Returns (norm, coefficient) on the device; gamma is
-        the caller's (AdamW on self.dgamma, say)."""
+        it) and starts new gradients (zero_grad).  Returns (norm, coefficient) on the device; gamma
+        is the caller's (AdamW on self.dgamma, say, before the next backward pass)."""
         stats = self.session.clip_grad_norm(max_norm, tensors=self._clip)
         self.session.run(hp, abi.HM_STAGE_ALL, torch.cuda.current_stream())
         self._weight_operands()
-        self.g.zero_()
+        self.zero_grad()
         return stats
 
     def close(self) -> None:

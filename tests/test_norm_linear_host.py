@@ -90,3 +90,29 @@ def test_right_tensors_are_taken(layer):
     x.backward(dy, inp)
     x.load_weight(torch.zeros(D_OUT, D_IN, dtype=torch.float64))
     assert [c[0] for c in calls].count("mxfp8_gemm") == 6
+
+
+def _accumulates(calls):
+    return [c[1][12] for c in calls if c[0] == "rmsnorm_backward"]
+
+
+def test_dgamma_adds_up_like_dw(layer, monkeypatch):
+    """One step's micro-batches add to both gradients; a step, or clearing, starts both anew."""
+    x, calls = layer
+    x.session = types.SimpleNamespace(clip_grad_norm=lambda *a, **kw: None, run=lambda *a: None)
+    x._clip = []
+    monkeypatch.setattr(linear.torch.cuda, "current_stream", lambda *a: None)
+    dy = torch.zeros(TOKENS, D_OUT, dtype=BF16)
+    for _ in range(3):
+        x.backward(dy)
+    assert _accumulates(calls) == [False, True, True]
+    x.step(None)
+    x.backward(dy)
+    x.backward(dy)
+    assert _accumulates(calls)[3:] == [False, True]
+    x.g.fill_(1.0)
+    x.zero_grad()
+    x.backward(dy)
+    assert _accumulates(calls)[5:] == [False] and (x.g == 0).all()
+    dw = [c[1][12] for c in calls if c[0] == "mxfp8_gemm" and c[1][11] == linear.abi.HM_F32]
+    assert dw == [True] * 6
