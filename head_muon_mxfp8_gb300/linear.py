@@ -15,6 +15,7 @@ weight and scales, main gradient) and section 3.4 (the update's place in a
 step)."""
 from __future__ import annotations
 
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -40,6 +41,15 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _on_its_device(method):
+    """Runs a layer's method with the layer's device current: its streams and launches."""
+    @functools.wraps(method)
+    def run(self, *args, **kw):
+        with torch.cuda.device_of(self.gamma):
+            return method(self, *args, **kw)
+    return run
+
+
 def _ptr(t: Optional[torch.Tensor]) -> int:
     return t.data_ptr() if t is not None else 0
 
@@ -57,10 +67,16 @@ class NormLinear:
     _summed = False   # whether dgamma holds a backward pass since the gradients were cleared
 
     def __init__(self, tokens: int, d_in: int, d_out: int, eps: float = 1e-5, block: int = 32, device="cuda"):
+        """Buffers for `tokens` rows on `device`, which need not be the current one."""
         if d_in % 32 or d_out % 32:
             raise ValueError("d_in and d_out are multiples of 32 (MX blocks)")
         self.tokens, self.d_in, self.d_out, self.eps, self.block = tokens, d_in, d_out, eps, block
         dev = self.device = torch.device(device)
+        self.gamma = torch.ones(d_in, dtype=torch.float32, device=dev)
+        self._allocate(tokens, d_in, d_out, dev)
+
+    @_on_its_device
+    def _allocate(self, tokens: int, d_in: int, d_out: int, dev) -> None:
         self.session = MuonSession(d_out * d_in, [(0, d_out, d_in)], so=1, sw=1, sg=1, device=dev)
         base, n = self.session.bases[0], d_out * d_in
         self.w = self.session.w[base:base + n].view(d_out, d_in)   # fp32 main weight
@@ -69,7 +85,6 @@ class NormLinear:
         self._s = self.session.s[base // 32:(base + n) // 32]      # its K-major scales
         self._s_tiled = torch.zeros(abi.mxfp8_tiled_scale_bytes(d_out, d_in), dtype=torch.uint8, device=dev)
         self.wt = MxBuffer(d_in, d_out, dev)                       # W^T, for the gradient of x
-        self.gamma = torch.ones(d_in, dtype=torch.float32, device=dev)
         self.dgamma = torch.zeros(d_in, dtype=torch.float32, device=dev)
         bf16 = dict(dtype=torch.bfloat16, device=dev)
         self.h = torch.empty(tokens, d_in, **bf16)
@@ -86,12 +101,14 @@ class NormLinear:
         self.zero_grad()
         self.session.m.zero_()
 
+    @_on_its_device
     def zero_grad(self) -> None:
         """Starts the gradients of a new step: clears dW; the next backward pass overwrites
         dgamma (which stays readable until then) and later ones add to it."""
         self.g.zero_()
         self._summed = False
 
+    @_on_its_device
     def load_weight(self, w: torch.Tensor) -> None:
         """w [d_out][d_in], any floating type, layout and device (ValueError for another shape)."""
         if tuple(w.shape) != (self.d_out, self.d_in):
@@ -106,6 +123,7 @@ class NormLinear:
         abi.mxfp8_quantize(_ptr(self.w), abi.HM_F32, self.d_out, self.d_in, self.d_in, 0, 0, 32, 0, 0, 0, _ptr(self.wt.q),
                            self.wt.k, _ptr(self.wt.s), _stream())
 
+    @_on_its_device
     def forward(self, x: torch.Tensor, res: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """x, res: bf16 [tokens][d_in], contiguous -> (y bf16 [tokens][d_out], h = x + res).
         Other shapes, types, layouts and devices are refused (ValueError), here and in backward."""
@@ -119,6 +137,7 @@ class NormLinear:
                        d, _ptr(self.y), self.d_out, abi.HM_BF16, False, st)
         return self.y, self.h
 
+    @_on_its_device
     def backward(self, dy: torch.Tensor, dres: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """dy bf16 [tokens][d_out], dres bf16 [tokens][d_in] -> (dx, dgamma).  Adds dW to
         self.g and dgamma to self.dgamma, so several micro-batches make one step's gradient."""
@@ -141,6 +160,7 @@ class NormLinear:
         self._summed = True
         return self.dx, self.dgamma
 
+    @_on_its_device
     def step(self, hp: "abi.hm_muon_hparams", max_norm: float = 1.0) -> torch.Tensor:
         """Clips dW and dgamma by their global norm, runs the Muon update of W (which requantizes
         it) and starts new gradients (zero_grad).  Returns (norm, coefficient) on the device; gamma

@@ -116,3 +116,31 @@ def test_dgamma_adds_up_like_dw(layer, monkeypatch):
     assert _accumulates(calls)[5:] == [False] and (x.g == 0).all()
     dw = [c[1][12] for c in calls if c[0] == "mxfp8_gemm" and c[1][11] == linear.abi.HM_F32]
     assert dw == [True] * 6
+
+
+def test_every_call_runs_on_the_layers_device(layer, monkeypatch):
+    """Another device being current changes nothing: launches and streams are the layer's device's."""
+    x, calls = layer
+    current, seen = ["another"], []
+
+    class of:
+        def __init__(self, t):
+            assert t is x.gamma
+
+        def __enter__(self):
+            current.append("the layer's")
+
+        def __exit__(self, *exc):
+            current.pop()
+    monkeypatch.setattr(linear.torch.cuda, "device_of", of)
+    monkeypatch.setattr(linear.torch.cuda, "current_stream", lambda *a: None)
+    monkeypatch.setattr(linear, "_stream", lambda *a: seen.append(current[-1]) or 0)
+    monkeypatch.setattr(type(linear.abi), "__getattr__", lambda rec, name: lambda *a: seen.append(current[-1]))
+    note = lambda *a, **kw: seen.append(current[-1])  # noqa: E731
+    x.session, x._clip = types.SimpleNamespace(clip_grad_norm=note, run=note), []
+    inp, dy = torch.zeros(TOKENS, D_IN, dtype=BF16), torch.zeros(TOKENS, D_OUT, dtype=BF16)
+    x.load_weight(torch.zeros(D_OUT, D_IN))
+    x.forward(inp, inp)
+    x.backward(dy, inp)
+    x.step(None)
+    assert len(seen) > 15 and set(seen) == {"the layer's"} and current == ["another"]
