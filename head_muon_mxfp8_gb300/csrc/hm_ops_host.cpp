@@ -34,7 +34,13 @@ bool elem_size(hm_dtype t, int64_t* es) {
 }
 
 constexpr int64_t kMaxDim = INT32_MAX - 256;   // tile coordinates and row counts stay in 32 bits
-constexpr int64_t kMaxPitch = int64_t(1) << 40;  // byte offsets of any element stay in 63 bits
+constexpr int64_t kMaxPitch = int64_t(1) << 40;
+
+// Whether [rows][ld] of `elem` bytes is larger than any address space (2^56 bytes), so
+// that offsets and the ends of spans would leave 64 bits.
+bool too_far(int64_t rows, int64_t ld, int64_t elem) {
+    return rows > 0 && ld > 0 && ld > (int64_t(1) << 56) / elem / rows;
+}
 
 }  // namespace
 
@@ -57,7 +63,8 @@ extern "C" hm_status mxfp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_
     int64_t es = 0;
     if (m < 0 || n < 0 || k < 0) return HM_ERR_ARG;
     if (!elem_size(d_dtype, &es) || (accumulate && d_dtype != HM_F32)) return HM_ERR_DTYPE;
-    if (m > kMaxDim || n > kMaxDim || k > kMaxDim || lda > kMaxDim || ldb > kMaxDim || ldd > kMaxPitch)
+    if (m > kMaxDim || n > kMaxDim || k > kMaxDim || lda > kMaxDim || ldb > kMaxDim || ldd > kMaxPitch ||
+        too_far(m, lda, 1) || too_far(n, ldb, 1) || too_far(m, ldd, es))
         return HM_ERR_GEOMETRY;
     if (m == 0 || n == 0) return HM_OK;
     if (!d || ldd < n || (k && (!a || !a_scales || !b || !b_scales || lda < k || ldb < k))) return HM_ERR_ARG;
@@ -96,7 +103,8 @@ extern "C" hm_status mxfp8_quantize(const void* x, hm_dtype x_dtype, int64_t row
     if (rows < 0 || cols < 0 || (block != 32 && block != 128)) return HM_ERR_ARG;
     if (!elem_size(x_dtype, &es)) return HM_ERR_DTYPE;
     if ((!q && !qt) || !q != !s || !qt != !st) return HM_ERR_ARG;
-    if (rows > (int64_t(1) << 22) || cols > (int64_t(1) << 30) || ldx > kMaxPitch || ldq > kMaxPitch || ldqt > kMaxPitch)
+    if (rows > (int64_t(1) << 22) || cols > (int64_t(1) << 30) || ldx > kMaxPitch || ldq > kMaxPitch || ldqt > kMaxPitch ||
+        too_far(rows, ldx, es) || too_far(rows, ldq, 1) || too_far(cols, ldqt, 1))
         return HM_ERR_GEOMETRY;
     if (rows == 0 || cols == 0) return HM_OK;
     const int64_t cols32 = up(cols, 32), rows32 = up(rows, 32);
@@ -142,7 +150,9 @@ extern "C" hm_status rmsnorm_mxfp8(const void* x, int64_t ldx, const void* res, 
     int64_t es = 0;
     if (rows < 0 || d < 0 || (block != 32 && block != 128) || !(eps >= 0.f)) return HM_ERR_ARG;
     if (!elem_size(dtype, &es)) return HM_ERR_DTYPE;
-    if (d > HM_RMSNORM_MAX_D || rows > kMaxDim || ldx > kMaxPitch || ldh > kMaxPitch) return HM_ERR_GEOMETRY;
+    if (d > HM_RMSNORM_MAX_D || rows > kMaxDim || ldx > kMaxPitch || ldh > kMaxPitch || too_far(rows, ldx, es) ||
+        too_far(rows, ldh, es))
+        return HM_ERR_GEOMETRY;
     if (rows == 0 || d == 0) return HM_OK;
     if (!x || !gamma || !rstd || !q || !s || ldx < d || ((res || h) && ldh < d) || (res && !h)) return HM_ERR_ARG;
     if (d % HM_MX_BLOCK || ldx % 8 || ((res || h) && ldh % 8)) return HM_ERR_ALIGN;
@@ -197,7 +207,9 @@ extern "C" hm_status rmsnorm_backward(const void* dy, int64_t lddy, const void* 
     int64_t es = 0;
     if (rows < 0 || d < 0) return HM_ERR_ARG;
     if (!elem_size(dtype, &es)) return HM_ERR_DTYPE;
-    if (d > HM_RMSNORM_MAX_D || rows > kMaxDim || lddy > kMaxPitch || ldh > kMaxPitch) return HM_ERR_GEOMETRY;
+    if (d > HM_RMSNORM_MAX_D || rows > kMaxDim || lddy > kMaxPitch || ldh > kMaxPitch || too_far(rows, lddy, es) ||
+        too_far(rows, ldh, es))
+        return HM_ERR_GEOMETRY;
     if (d == 0) return HM_OK;
     if (!dgamma) return HM_ERR_ARG;
     if (rows && (!dy || !h || !dx || !gamma || !rstd || lddy < d || ldh < d)) return HM_ERR_ARG;

@@ -408,6 +408,7 @@ hm_status reduce_scatter_grad(const hm_chain* chain, const float* parts, int n_p
  * blocks, so every reader of the layout takes both.  Scale rule and rounding
  * are G's.  A NaN quantizes to the NaN code, an infinity to +-448.
  *
+ * A matrix whose rows x pitch pass 2^56 bytes is HM_ERR_GEOMETRY in all of them.
  * None of these calls allocates or synchronises, and each launches only kernels,
  * so they can be captured into a CUDA graph; make the first call of a kind on a
  * device outside a capture (its kernels are loaded and configured then).
