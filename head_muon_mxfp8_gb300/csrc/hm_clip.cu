@@ -338,6 +338,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads)
     }
     sum = block_sum<kFewThreads>(sum);
     if (threadIdx.x == 0) s_part = sum;
+    __syncwarp();
     cluster_sync_all();
     if (threadIdx.x == 0) {
         double part[kFewCtas];

@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tmem_alloc_pair(smem_u32(tmem_slot), 512);
         tmem_relinquish_pair();
     }
+    __syncwarp();  // thread 0's set-up is behind its warp: the barrier is taken by whole warps
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
@@ -387,6 +388,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             uint32_t r[16];
+                            __syncwarp();
                             tmem_ld16(acc + ch * 32 + h * 16, r);
                             tmem_ld_wait();
                             tmem_ld_pin16(r);
@@ -399,6 +401,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         continue;
                     }
                     uint32_t r[32];
+                    __syncwarp();  // lanes past the last column left the chunk before early
                     tmem_ld32(acc + ch * 32, r);
                     tmem_ld_wait();
                     tmem_ld_pin(r);
@@ -641,6 +644,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 #pragma unroll 1
             for (int c0 = 0; c0 < rows; c0 += 32) {
                 uint32_t r[32];
+                __syncwarp();
                 tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, r);
                 tmem_ld_wait();
                 tmem_ld_pin(r);
@@ -658,6 +662,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         tc_fence_before();
     }
     if (ck > 1) {
+        __syncwarp();
         cluster_sync_all();
         const int c0 = tp * kTileP;
         switch (ck) {

@@ -39,3 +39,21 @@ def test_every_kernel_waits_for_the_ones_before(name):
     """Each kernel of such a file waits (griddepcontrol.wait) in its body."""
     bodies = _code(name).split("__global__")[1:]
     assert bodies and all("wait_for_earlier_kernels()" in b.split("\n}\n")[0] for b in bodies)
+
+
+@pytest.mark.parametrize("name", EARLY)
+def test_warps_converge_before_aligned_instructions(name):
+    """tcgen05.ld and the aligned cluster barriers take all lanes of a warp at the same
+    instruction; after code that lanes leave at different points (a store past the last
+    column, one thread's work) only a warp or block barrier brings them together."""
+    lines = [x.strip() for x in _code(name).splitlines() if x.strip()]
+    loose = []
+    for k, line in enumerate(lines):
+        if not re.match(r"(tmem_ld(16|32)|cluster_sync_all|cluster_arrive_relaxed|cluster_wait)\(", line):
+            continue
+        before = k - 1
+        while re.match(r"(tc_fence_(before|after)\(\);|uint32_t r\[\d+\];)$", lines[before]):
+            before -= 1
+        if not re.match(r"(__syncwarp|__syncthreads|cluster_arrive_relaxed)\(\);$", lines[before]):
+            loose.append((lines[before], line))
+    assert loose == []
