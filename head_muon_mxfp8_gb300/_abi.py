@@ -133,6 +133,7 @@ _SIGS = {
     "mxfp8_tiled_scale_bytes": (C.c_int, [C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
     "mxfp8_gemm": (C.c_int, [_P, C.c_int64, _P, _P, C.c_int64, _P, C.c_int64, C.c_int64, C.c_int64, _P, C.c_int64,
                              C.c_int, C.c_int, _P]),
+    "mxfp8_gemm_form": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.c_int, _I32P, _I32P, _I32P]),
     "mxfp8_quantize": (C.c_int, [_P, C.c_int, C.c_int64, C.c_int64, C.c_int64, _P, _P, C.c_int, _P, C.c_int64, _P, _P,
                                  C.c_int64, _P, _P]),
     "rmsnorm_mxfp8": (C.c_int, [_P, C.c_int64, _P, _P, C.c_int64, C.c_int, C.c_int64, C.c_int64, _P, C.c_float,
@@ -345,6 +346,13 @@ def mxfp8_gemm(a: int, lda: int, a_scales: int, b: int, ldb: int, b_scales: int,
     """D[m][n] (+)= A[m][k] B[n][k]^T of MXFP8 operands (see include/hm.h)."""
     check("mxfp8_gemm", lib().mxfp8_gemm(a, lda, a_scales, b, ldb, b_scales, m, n, k, d, ldd, d_dtype, accumulate,
                                          stream))
+
+
+def mxfp8_gemm_form(m: int, n: int, k: int, d_dtype: int):
+    """(tile, parts, sums): the kernel that a product takes (see include/hm.h)."""
+    v = [C.c_int32(0) for _ in range(3)]
+    check("mxfp8_gemm_form", lib().mxfp8_gemm_form(m, n, k, d_dtype, *[C.byref(x) for x in v]))
+    return tuple(x.value for x in v)
 
 
 def mxfp8_quantize(x: int, x_dtype: int, rows: int, cols: int, ldx: int, row_mul: int, col_mul: int, block: int,

@@ -792,19 +792,25 @@ int split_for(int tiles_p, int tiles_q, const MxGemmArgs& p, double* cost) {
     return best;
 }
 
+// The split kernel with BN rows of A per tile: its parts and what they are estimated to take.
 template <int BN>
-cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, MxGemmArgs p, cudaStream_t st) {
+cudaError_t split_form(const MxGemmArgs& p, MxGemmForm* f, double* cost) {
     static PerDevice done;
-    cudaError_t e = allow_smem(mx_gemm_split_kernel<BN>, SplitCfg<BN>::SMEM, done);
+    const cudaError_t e = allow_smem(mx_gemm_split_kernel<BN>, SplitCfg<BN>::SMEM, done);  // before its occupancy is asked
     if (e != cudaSuccess) return e;
+    f->tile = BN;
+    f->parts = split_for<BN>((p.n + kTileP - 1) / kTileP, (p.m + BN - 1) / BN, p, cost);
+    f->sums = 0;
+    return cudaSuccess;
+}
+
+template <int BN>
+cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, const MxGemmArgs& p, cudaStream_t st) {
     CUtensorMap ma, mb;
     if (!map_codes(&ma, a, p.k, p.m, lda, BN) || !map_codes(&mb, b, p.k, p.n, ldb, kTileP)) return cudaErrorUnknown;
-    const int tiles_p = (p.n + kTileP - 1) / kTileP, tiles_q = (p.m + BN - 1) / BN;
-    double cost;
-    p.split = split_for<BN>(tiles_p, tiles_q, p, &cost);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    split_config<BN>(cfg, attr, tiles_p, tiles_q, p.split, st);
+    split_config<BN>(cfg, attr, (p.n + kTileP - 1) / kTileP, (p.m + BN - 1) / BN, p.split, st);
     note_launch();
     return cudaLaunchKernelEx(&cfg, mx_gemm_split_kernel<BN>, ma, mb, p);
 }
@@ -834,15 +840,46 @@ cudaError_t launch_pair(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t
     return cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<BN, SUMS>, mp, mq, msp, msq, p);
 }
 
-template <int BN>
-cudaError_t launch_pair_of(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, const MxGemmArgs& p, cudaStream_t st) {
-    // the sums in registers take disjoint accumulators
-    if constexpr (BN <= 192)
-        if (p.d_f32 && p.num_kb > kChunkK / kTileK) return launch_pair<BN, true>(a, lda, b, ldb, p, st);
-    return launch_pair<BN, false>(a, lda, b, ldb, p, st);
-}
-
 }  // namespace
+
+// k > 0.  The kernel, its tile width, the split of K and whether K is summed in chunks.
+cudaError_t mx_gemm_form(const MxGemmArgs& args, MxGemmForm* f) {
+    MxGemmArgs p = args;
+    p.num_kb = (p.k + kTileK - 1) / kTileK;
+    double cost;
+    // fp32 D over a K that eight parts of kSplitSumKb stages do not cover: the pair kernel's sums
+    const bool long_sum = p.d_f32 && p.num_kb > kMaxSplit * kSplitSumKb;
+    if (!long_sum) {
+        if (p.m <= 16) return split_form<16>(p, f, &cost);
+        if (p.m <= 32) return split_form<32>(p, f, &cost);
+        if (p.m <= 64) return split_form<64>(p, f, &cost);
+        if (p.m <= 128) return split_form<128>(p, f, &cost);
+    }
+    // The tile width that leaves the least time to the pair with the most tiles.  A
+    // stage's time goes with the rows it loads (256 + BN): 128-wide tiles took 0.79 of
+    // the time of 256-wide ones (293 and 371 ns per stage, K = 5120, 640 tiles of 256);
+    // a tile's epilogue takes about 2.2 us, filling and emptying the pipeline 4.
+    // The sums in registers take disjoint accumulators: at most 192.
+    const bool sums = p.d_f32 && p.num_kb > kChunkK / kTileK;
+    const int64_t pairs = device_sm_count() / 2;
+    int best = 0;
+    double least = 0;
+    for (const int bn : {256, 192, 128}) {
+        if (bn > 192 && sums) continue;
+        const int64_t tiles = static_cast<int64_t>((p.n + 255) / 256) * ((p.m + bn - 1) / bn);
+        const double c = static_cast<double>((tiles + pairs - 1) / pairs) * std::max(p.num_kb * (256 + bn) * (0.37 / 512), 2.2) + 4.0;
+        if (!best || c < least) best = bn, least = c;
+    }
+    // Too few tiles for the pairs: 128 x 128 tiles with K split over clusters.
+    if ((static_cast<int64_t>(p.m) + 127) / 128 <= 65535 && !long_sum) {
+        const cudaError_t e = split_form<128>(p, f, &cost);
+        if (e != cudaSuccess || cost < least) return e;
+    }
+    f->tile = best;
+    f->parts = 0;
+    f->sums = sums;
+    return cudaSuccess;
+}
 
 cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, const MxGemmArgs& args,
                            cudaStream_t st) {
@@ -858,41 +895,19 @@ cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int6
     p.last_nk = (p.k - (p.num_kb - 1) * kTileK) / 32;
     p.err = device_error_word();
     p.inject = inject_mx_timeout();
-    // fp32 D over a K that eight parts of kSplitSumKb stages do not cover: the pair kernel's sums
-    const bool long_sum = p.d_f32 && p.num_kb > kMaxSplit * kSplitSumKb;
-    if (!long_sum) {
-        if (p.m <= 16) return launch_split<16>(a, lda, b, ldb, p, st);
-        if (p.m <= 32) return launch_split<32>(a, lda, b, ldb, p, st);
-        if (p.m <= 64) return launch_split<64>(a, lda, b, ldb, p, st);
-        if (p.m <= 128) return launch_split<128>(a, lda, b, ldb, p, st);
+    MxGemmForm f;
+    const cudaError_t e = mx_gemm_form(p, &f);
+    if (e != cudaSuccess) return e;
+    p.split = f.parts;
+    if (f.parts) {
+        if (f.tile == 16) return launch_split<16>(a, lda, b, ldb, p, st);
+        if (f.tile == 32) return launch_split<32>(a, lda, b, ldb, p, st);
+        if (f.tile == 64) return launch_split<64>(a, lda, b, ldb, p, st);
+        return launch_split<128>(a, lda, b, ldb, p, st);
     }
-    // The tile width that leaves the least time to the pair with the most tiles.  A
-    // stage's time goes with the rows it loads (256 + BN): 128-wide tiles took 0.79 of
-    // the time of 256-wide ones (293 and 371 ns per stage, K = 5120, 640 tiles of 256);
-    // a tile's epilogue takes about 2.2 us, filling and emptying the pipeline 4.
-    const bool sums = p.d_f32 && p.num_kb > kChunkK / kTileK;
-    const int64_t pairs = device_sm_count() / 2;
-    int best = 0;
-    double least = 0;
-    for (const int bn : {256, 192, 128}) {
-        if (bn > 192 && sums) continue;
-        const int64_t tiles = static_cast<int64_t>((p.n + 255) / 256) * ((p.m + bn - 1) / bn);
-        const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * std::max(p.num_kb * (256 + bn) * (0.37 / 512), 2.2) + 4.0;
-        if (!best || cost < least) best = bn, least = cost;
-    }
-    // Too few tiles for the pairs: 128 x 128 tiles with K split over clusters.
-    const int64_t small_q = (static_cast<int64_t>(p.m) + 127) / 128;
-    if (small_q <= 65535 && !long_sum) {
-        static PerDevice done;
-        const cudaError_t e = allow_smem(mx_gemm_split_kernel<128>, SplitCfg<128>::SMEM, done);  // before its occupancy is asked
-        if (e != cudaSuccess) return e;
-        double split_cost;
-        split_for<128>((p.n + 127) / 128, static_cast<int>(small_q), p, &split_cost);
-        if (split_cost < least) return launch_split<128>(a, lda, b, ldb, p, st);
-    }
-    if (best == 256) return launch_pair_of<256>(a, lda, b, ldb, p, st);
-    if (best == 192) return launch_pair_of<192>(a, lda, b, ldb, p, st);
-    return launch_pair_of<128>(a, lda, b, ldb, p, st);
+    if (f.tile == 256) return launch_pair<256, false>(a, lda, b, ldb, p, st);
+    if (f.tile == 192) return f.sums ? launch_pair<192, true>(a, lda, b, ldb, p, st) : launch_pair<192, false>(a, lda, b, ldb, p, st);
+    return f.sums ? launch_pair<128, true>(a, lda, b, ldb, p, st) : launch_pair<128, false>(a, lda, b, ldb, p, st);
 }
 
 }  // namespace hm

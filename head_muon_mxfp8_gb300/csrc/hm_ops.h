@@ -56,10 +56,16 @@ struct MxGemmArgs {
     int32_t num_kb;      // stages of 128 along K
     int32_t last_nk;     // blocks of 32 in the last stage
     int32_t tiles_p, tiles_q;  // pair kernel: tiles along n and m
-    int32_t split;       // CTAs of a cluster that share K
+    int32_t split;       // split kernel: CTAs of a cluster that share K
     int32_t inject;      // failure test: never signal an accumulator as ready
     int32_t* err;
 };
+// Which kernel a product takes: `tile` rows of A per tile, K over `parts` CTAs of a
+// cluster (0: the pair kernel), there with `sums` of chunks of K in registers.
+struct MxGemmForm {
+    int32_t tile, parts, sums;
+};
+cudaError_t mx_gemm_form(const MxGemmArgs& p, MxGemmForm* f);  // m, n, k, d_f32 of p, k > 0
 // Failure-detection test hook: HM_INJECT_MX_WAIT_TIMEOUT=1 in the environment makes
 // the waits of the product and of the norm's gradient run out (bounded), so that
 // they record HM_ERR_TIMEOUT.

@@ -96,6 +96,27 @@ extern "C" hm_status mxfp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_
     return cuda_status(hm::launch_mx_gemm(a, lda, b, ldb, p, static_cast<cudaStream_t>(stream)));
 }
 
+extern "C" hm_status mxfp8_gemm_form(int64_t m, int64_t n, int64_t k, hm_dtype d_dtype, int32_t* tile, int32_t* parts,
+                                     int32_t* sums) {
+    int64_t es = 0;
+    if (!tile || !parts || !sums || m <= 0 || n <= 0 || k <= 0) return HM_ERR_ARG;
+    if (!elem_size(d_dtype, &es)) return HM_ERR_DTYPE;
+    if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return HM_ERR_GEOMETRY;
+    if (k % HM_MX_BLOCK) return HM_ERR_ALIGN;
+    const hm_status st = hm::check_arch();
+    if (st != HM_OK) return st;
+    hm::MxGemmArgs p;
+    std::memset(&p, 0, sizeof(p));
+    p.m = static_cast<int32_t>(m);
+    p.n = static_cast<int32_t>(n);
+    p.k = static_cast<int32_t>(k);
+    p.d_f32 = d_dtype == HM_F32;
+    hm::MxGemmForm f;
+    const hm_status ok = cuda_status(hm::mx_gemm_form(p, &f));
+    if (ok == HM_OK) *tile = f.tile, *parts = f.parts, *sums = f.sums;
+    return ok;
+}
+
 extern "C" hm_status mxfp8_quantize(const void* x, hm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx,
                                     const float* row_mul, const float* col_mul, int block, uint8_t* q, int64_t ldq,
                                     uint8_t* s, uint8_t* qt, int64_t ldqt, uint8_t* st, void* stream) {

@@ -439,6 +439,13 @@ hm_status mxfp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_scales, con
                      const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, void* d, int64_t ldd,
                      hm_dtype d_dtype, int accumulate, void* stream);
 
+/* Which kernel such a product takes on the current device, for tests and profiles (m, n,
+ * k > 0): `tile` rows of A per tile; K split over `parts` CTAs of a cluster, or parts = 0
+ * for the kernel on CTA pairs; `sums` = 1 where that one adds chunks of K outside the
+ * tensor core (fp32 D, long K). */
+hm_status mxfp8_gemm_form(int64_t m, int64_t n, int64_t k, hm_dtype d_dtype, int32_t* tile, int32_t* parts,
+                          int32_t* sums);
+
 /* Quantizes x [rows][ldx] (HM_BF16 or HM_F32) to MXFP8 along its columns
  * and / or along its rows, reading x once:
  *   y[r][c] = x[r][c] * row_mul[r] * col_mul[c]   (fp32, in this order; a NULL
