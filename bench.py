@@ -84,17 +84,29 @@ def straddling_elems(cfg, plan_info) -> int:
 # workload with f2 and G folded into its last products (the timed update's
 # second call: the one-launch head-class kernel and 15 CTA-pair GEMMs): an ncu
 # launch list of dram__bytes_read.sum + dram__bytes_write.sum over the timed
-# update of one Video-DiT layer (18.84 GB), scaled by the units processed (x8);
-# valid only for the kernel source it was measured on (sha256 prefix of hm_ns.cu).
-NS_STAGE_TRAFFIC = {"workload": "video_dit", "bytes": 1.507e+11, "hm_ns_sha256": "ac4f979a729147d1",
+# update of one Video-DiT layer (18.86 GB), scaled by the units processed (x8);
+# valid only for the kernels' code it was measured on (ns_source_hash).
+NS_STAGE_TRAFFIC = {"workload": "video_dit", "bytes": 1.509e+11, "source_hash": "e4c65f67f35349c1",
                     "how": "one Video-DiT layer measured, x8 by units"}
+CSRC = os.path.join(ROOT, "head_muon_mxfp8_gb300", "csrc")
+NS_SOURCES = ("hm_ns.cu", "hm_ptx.cuh", "hm_mx_device.cuh")
+
+
+def ns_source_hash(csrc: str = CSRC) -> str:
+    """sha256 prefix of the Newton-Schulz kernels' device code, comments and white space left out."""
+    import hashlib
+    import re
+    h = hashlib.sha256()
+    for name in NS_SOURCES:
+        with open(os.path.join(csrc, name)) as f:
+            code = re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+        h.update("\n".join(" ".join(line.split()) for line in code.splitlines() if line.strip()).encode())
+        h.update(b"\n")
+    return h.hexdigest()[:16]
 
 
 def ns_stage_traffic(cfg):
-    import hashlib
-    src = os.path.join(ROOT, "head_muon_mxfp8_gb300", "csrc", "hm_ns.cu")
-    sha = hashlib.sha256(open(src, "rb").read()).hexdigest()[:16]
-    if cfg.name != NS_STAGE_TRAFFIC["workload"] or sha != NS_STAGE_TRAFFIC["hm_ns_sha256"]:
+    if cfg.name != NS_STAGE_TRAFFIC["workload"] or ns_source_hash() != NS_STAGE_TRAFFIC["source_hash"]:
         return None
     return NS_STAGE_TRAFFIC["bytes"]
 
