@@ -333,6 +333,14 @@ extern "C" hm_status grad_norm_clip(const hm_grad_tensor* tensors, int n, float 
     if (ok != HM_OK) return ok;
     if (parts > INT32_MAX) return HM_ERR_GEOMETRY;
     if (parts && (!workspace || workspace_bytes < parts * sizeof(double))) return HM_ERR_WORKSPACE;
+    // the scaling reads the sums while it writes the tensors and stats
+    const Span sums = span(workspace, 1, 0, parts * static_cast<int64_t>(sizeof(double)), 1), result = span(stats, 1, 0, 8, 1);
+    if (overlap(sums, result)) return HM_ERR_OVERLAP;
+    for (int i = 0; i < n; ++i) {
+        const int64_t bytes = tensors[i].n * (tensors[i].dtype == HM_F32 ? 4 : 2);
+        const Span src = span(tensors[i].src, 1, 0, bytes, 1), dst = span(tensors[i].dst, 1, 0, bytes, 1);
+        if (overlap(sums, src) || overlap(sums, dst) || overlap(result, src) || overlap(result, dst)) return HM_ERR_OVERLAP;
+    }
     if ((ok = hm::check_arch()) != HM_OK) return ok;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     hm::ClipHead head;

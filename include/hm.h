@@ -408,7 +408,8 @@ hm_status reduce_scatter_grad(const hm_chain* chain, const float* parts, int n_p
  * blocks, so every reader of the layout takes both.  Scale rule and rounding
  * are G's.  A NaN quantizes to the NaN code, an infinity to +-448.
  *
- * A matrix whose rows x pitch pass 2^56 bytes is HM_ERR_GEOMETRY in all of them.
+ * Overlap is judged by the span from a matrix's first byte to its last, gaps
+ * between rows included.  A matrix whose rows x pitch pass 2^56 bytes is HM_ERR_GEOMETRY in all of them.
  * None of these calls allocates or synchronises, and each launches only kernels,
  * so they can be captured into a CUDA graph; make the first call of a kind on a
  * device outside a capture (its kernels are loaded and configured then).
@@ -510,7 +511,8 @@ hm_status rmsnorm_backward(const void* dy, int64_t lddy, const void* dres, const
  * fp32; a NaN makes norm, coef and every dst NaN; an infinite norm gives
  * coef 0 (dst: 0, and NaN where src is infinite).  max_norm > 0 (infinity:
  * coef is 1 unless the norm is NaN), eps >= 0 (HM_ERR_ARG).  dst overlapping its own src other
- * than exactly, or any other tensor's memory, is the caller's error.
+ * than exactly (HM_ERR_OVERLAP), or any other tensor's memory, is the caller's error; a
+ * tensor that overlaps stats or the workspace, or these each other, is HM_ERR_OVERLAP.
  * workspace: 16-byte aligned, grad_norm_clip_workspace bytes
  * (HM_ERR_WORKSPACE), contents need not be kept; calls that share one must
  * not overlap. */
