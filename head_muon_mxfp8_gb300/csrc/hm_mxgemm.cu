@@ -95,17 +95,6 @@ __host__ __device__ constexpr uint32_t mx_idesc(int m, int n) {
 }
 __device__ __forceinline__ uint32_t sf_id(int kk) { return (static_cast<uint32_t>(kk) << 4) | (static_cast<uint32_t>(kk) << 29); }
 
-// One element of D, row-major.
-__device__ __forceinline__ void store_one(const MxGemmArgs& p, int64_t row, int col, float v) {
-    const int64_t at = row * p.ldd + col;
-    if (p.d_f32) {
-        float* d = static_cast<float*>(p.d) + at;
-        *d = p.accumulate ? *d + v : v;
-    } else {
-        static_cast<uint16_t*>(p.d)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    }
-}
-
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ---------------------------------------------------------------------------
@@ -686,12 +675,13 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     }
 }
 
-// K = 0: the sum is empty.
+// K = 0: the sum is empty (and D unchanged when accumulating: no launch).
 __global__ void __launch_bounds__(256) mx_gemm_zero_kernel(const __grid_constant__ MxGemmArgs p) {
     wait_for_earlier_kernels();
     const int64_t total = static_cast<int64_t>(p.m) * p.n;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll)
-        store_one(p, static_cast<int>(i / p.n), static_cast<int>(i % p.n), 0.f);
+        if (p.d_f32) static_cast<float*>(p.d)[i / p.n * p.ldd + i % p.n] = 0.f;
+        else static_cast<uint16_t*>(p.d)[i / p.n * p.ldd + i % p.n] = 0u;
 }
 
 // Codes [rows][ld], k of them used: boxes of box_rows x 128 bytes, zero outside.

@@ -505,6 +505,8 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
     // Two CTAs per SM where half the ring still holds two rows: one computes while
     // the other stands at its barrier (8192 x 5120 bf16: 71 us with one, 55 with two).
     const int stage = a.d * (F32 ? 4 : 2) * (a.dres ? 3 : 2);
+    // Up to 8192 columns that is always so in bf16, up to 4096 in fp32.
+    static_assert(2 * 8192 * 2 * 3 <= kGradRing / 2 && 2 * 4096 * 4 * 3 <= kGradRing / 2, "two rows in half the ring");
     const bool two = a.d <= 8192 && 2 * stage <= kGradRing / 2;
     const int most = rmsnorm_grad_parts(a.rows, a.d);
     const int parts = a.d <= kWarpMaxD ? most : std::min(most, (two ? 2 : 1) * device_sm_count());
@@ -516,10 +518,11 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
                                 : a.d <= 512 ? rmsnorm_grad_warp_kernel<F32, 2>
                                              : rmsnorm_grad_warp_kernel<F32, 4>;
             e = launch_early(kernel, parts, 32 * kWarpRows, 0, st, a);
-        } else if (a.d <= 4096) e = two ? launch_grad<F32, 1, 512, 2>(a, parts, stage, st) : launch_grad<F32, 1, 512, 1>(a, parts, stage, st);
-        else if (a.d <= 5120 && two) e = launch_grad<F32, 2, 320, 2>(a, parts, stage, st);
-        else if (a.d <= 8192) e = two ? launch_grad<F32, 2, 512, 2>(a, parts, stage, st) : launch_grad<F32, 2, 512, 1>(a, parts, stage, st);
-        else e = launch_grad<F32, 2, 1024, 1>(a, parts, stage, st);
+        } else if (a.d <= 4096) e = launch_grad<F32, 1, 512, 2>(a, parts, stage, st);
+        else if (a.d > 8192) e = launch_grad<F32, 2, 1024, 1>(a, parts, stage, st);
+        else if (F32 && !two) e = launch_grad<true, 2, 512, 1>(a, parts, stage, st);
+        else if (a.d <= 5120) e = launch_grad<F32, 2, 320, 2>(a, parts, stage, st);
+        else e = launch_grad<F32, 2, 512, 2>(a, parts, stage, st);
         if (e != cudaSuccess) return e;
     }
     note_launch();
