@@ -6,14 +6,16 @@
 // chunk also takes the elements before that boundary and its last one those
 // after the last whole vector, so any element alignment runs on vector loads.
 // A thread adds the squares of one chunk's 16 vectors in fp32 and carries its
-// sum from chunk to chunk in double; CTA sums are doubles too, added in a fixed
-// order.  Two launches (one for little data, at the end): the norm pass, and a pass that
+// sum from chunk to chunk in double; a warp's 32 sums are joined in fp32 (five
+// roundings) where all are well inside its range, else in double; the warps' and
+// CTAs' sums are doubles.  All in a fixed order.  Two launches (one for little data, at the end): the norm pass, and a pass that
 // adds the CTA sums (every CTA the same way) and scales.  The second pass has to read the gradient again; it
 // walks the chunks backwards, and the norm pass marks all but the last ones
 // (as much as half the L2 holds) evict-first, so those come from the L2.
 // A thread's fp32 sum that overflowed or may have underflowed (squares
 // leave fp32 for |g| > 2^63 or < 2^-63) is formed again in double.
-// Memory-bound: 131 M fp32 elements in 48 tensors take 252 us out of place.
+// Memory-bound: 131 M fp32 elements in 48 tensors take 252 us out of place, the same
+// in bf16 120.
 #include "hm_internal.h"
 #include "hm_ops.h"
 #include "hm_ptx.cuh"

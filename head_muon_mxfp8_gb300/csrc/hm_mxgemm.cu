@@ -837,7 +837,9 @@ cudaError_t mx_gemm_form(const MxGemmArgs& args, MxGemmForm* f) {
     MxGemmArgs p = args;
     p.num_kb = (p.k + kTileK - 1) / kTileK;
     double cost;
-    // fp32 D over a K that eight parts of kSplitSumKb stages do not cover: the pair kernel's sums
+    // fp32 D over a K that eight parts of kSplitSumKb stages do not cover: the pair kernel's
+    // sums, however few the rows (5 x 5120: K = 20480 in eight parts 22.2 us, 24576 on
+    // pairs 52.5)
     const bool long_sum = p.d_f32 && p.num_kb > kMaxSplit * kSplitSumKb;
     if (!long_sum) {
         if (p.m <= 16) return split_form<16>(p, f, &cost);
@@ -849,7 +851,8 @@ cudaError_t mx_gemm_form(const MxGemmArgs& args, MxGemmForm* f) {
     // stage's time goes with the rows it loads (256 + BN): 128-wide tiles took 0.79 of
     // the time of 256-wide ones (293 and 371 ns per stage, K = 5120, 640 tiles of 256);
     // a tile's epilogue takes about 2.2 us, filling and emptying the pipeline 4.
-    // The sums in registers take disjoint accumulators: at most 192.
+    // With sums at most 192: a thread of the eight epilogue warps would hold 128 of
+    // them at 256, and ten warps leave it 168 registers (192 takes all, 28 bytes spilled).
     const bool sums = p.d_f32 && p.num_kb > kChunkK / kTileK;
     const int64_t pairs = device_sm_count() / 2;
     int best = 0;
@@ -860,7 +863,12 @@ cudaError_t mx_gemm_form(const MxGemmArgs& args, MxGemmForm* f) {
         const double c = static_cast<double>((tiles + pairs - 1) / pairs) * std::max(p.num_kb * (256 + bn) * (0.37 / 512), 2.2) + 4.0;
         if (!best || c < least) best = bn, least = c;
     }
-    // Too few tiles for the pairs: 128 x 128 tiles with K split over clusters.
+    // Too few tiles for the pairs: 128 x 128 tiles with K split over clusters.  Both
+    // forms measured for 129 to 1024 rows at n x k = 5120 x 5120, 20480 x 5120,
+    // 4096 x 4096 and 1408 x 2048, bf16 and fp32 D: the chosen one is the faster or
+    // within 4 % of it (129 x 5120 x 5120 bf16 12.4 us split, 14.1 on pairs; 512 rows 17.1
+    // and 15.5), but for 300 and 384 x 20480 x 5120 bf16, where two rounds of
+    // undivided tiles take 48 us that the estimate puts at 42, and pairs 38.
     if ((static_cast<int64_t>(p.m) + 127) / 128 <= 65535 && !long_sum) {
         const cudaError_t e = split_form<128>(p, f, &cost);
         if (e != cudaSuccess || cost < least) return e;

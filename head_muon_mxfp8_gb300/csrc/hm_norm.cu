@@ -8,8 +8,11 @@
 // the stored h, differentiates exactly the function the forward pass computed.
 // Memory-bound; a row stays in registers between its reduction and its output,
 // so every tensor is read and written once.  8192 x 5120 bf16 with residual: norm
-// 46.1 us (6.4 TB/s, 0.94 of the measured copy rate), gradient 54.4 us (6.2 TB/s,
-// dgamma's second launch included).
+// 46.1 us (6.4 TB/s, 0.94 of the measured copy rate), gradient 54.6 us (6.1 TB/s,
+// dgamma's second launch included); in fp32 81.7 and 100.3 us (6.7 TB/s both).
+// Far from it are the gradient's fp32 forms whose registers spill: 8192 rows of 6656
+// columns without a residual's gradient 183 us (3.6 TB/s), of 16384 558 us with it and
+// 439 without (3.8 and 3.7 TB/s).
 #include "hm_internal.h"
 #include "hm_mx_device.cuh"
 #include "hm_ops.h"
@@ -512,6 +515,9 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
     const int parts = a.d <= kWarpMaxD ? most : std::min(most, (two ? 2 : 1) * device_sm_count());
     if (parts) {
         cudaError_t e = cudaSuccess;
+        // Up to 5120 columns 320 threads hold two vectors each; told so, the compiler has
+        // the registers to keep gamma (8192 x 5120 bf16 55.0 us against 65.2 with the bound
+        // of 512 threads, 4608 50.4 and 61.2, fp32 5120 without residual 92.3 and 136.7).
         if (a.d <= kWarpMaxD) {
             note_launch();
             const auto kernel = a.d <= 256   ? rmsnorm_grad_warp_kernel<F32, 1>

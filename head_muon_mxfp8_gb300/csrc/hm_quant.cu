@@ -12,7 +12,8 @@
 // 8192 x 15360 bf16 to both outputs takes 80 us (6.4 TB/s, 0.94 of the measured
 // copy rate); a 14336 x 4096 fp32 weight to its transpose 63 us (4.7 TB/s), where
 // registers for the loads leave two CTAs per SM (a third CTA's spill: 92 us;
-// 512 threads per CTA: 66 us).
+// 512 threads per CTA: 66 us); 8192 x 5120 bf16 with both factors, the fp32 tile too,
+// 35.2 us to its transpose (3.6 TB/s) and 45.8 both ways.
 #include "hm_internal.h"
 #include "hm_mx_device.cuh"
 #include "hm_ops.h"
