@@ -45,6 +45,12 @@ HM_STAGE_SCRATCH = 64
 HM_STAGE_STEP = 127
 HM_RMSNORM_MAX_D = 16384
 HM_RS_FP32, HM_RS_BF16, HM_RS_BF16_SR = 0, 1, 2
+HM_EPI_FORWARD, HM_EPI_GATED, HM_EPI_GRADIENT, HM_EPI_GATED_GRADIENT = 0, 1, 2, 3
+HM_ACT_NONE, HM_ACT_RELU, HM_ACT_GELU, HM_ACT_GELU_TANH, HM_ACT_SILU = 0, 1, 2, 3, 4
+HM_HEAD_MAX_DIM = 512
+HM_HEAD_GROUPS = 4
+HM_ROPE_HALF, HM_ROPE_PAIRS = 0, 1
+HM_ROPE_UNSCALED, HM_ROPE_LINEAR, HM_ROPE_BASE, HM_ROPE_YARN = 0, 1, 2, 3
 
 
 class hm_fragment(C.Structure):
@@ -92,6 +98,29 @@ class hm_grad_tensor(C.Structure):
     _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32), ("pad", C.c_int32)]
 
 
+class hm_epilogue(C.Structure):
+    _fields_ = [("form", C.c_int32), ("activation", C.c_int32), ("bias", C.c_void_p), ("in_", C.c_void_p),
+                ("ld_in", C.c_int64), ("in2", C.c_void_p), ("ld_in2", C.c_int64), ("out2", C.c_void_p),
+                ("ld_out2", C.c_int64)]
+
+
+class hm_rotation(C.Structure):
+    _fields_ = [("turns", C.c_void_p), ("positions", C.c_void_p), ("scale", C.c_float), ("rot_dim", C.c_int32),
+                ("layout", C.c_int32), ("pad", C.c_int32)]
+
+
+class hm_head_group(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("x_row", C.c_int64), ("x_head", C.c_int64), ("y", C.c_void_p), ("y_row", C.c_int64),
+                ("y_head", C.c_int64), ("gamma", C.c_void_p), ("heads", C.c_int32), ("pad", C.c_int32)]
+
+
+class hm_head_grad(C.Structure):
+    _fields_ = [("dy", C.c_void_p), ("dy_row", C.c_int64), ("dy_head", C.c_int64), ("x", C.c_void_p),
+                ("x_row", C.c_int64), ("x_head", C.c_int64), ("dx", C.c_void_p), ("dx_row", C.c_int64),
+                ("dx_head", C.c_int64), ("gamma", C.c_void_p), ("dgamma", C.c_void_p), ("heads", C.c_int32),
+                ("accumulate", C.c_int32)]
+
+
 class HmError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn} returned {status} ({status_str(status)})")
@@ -133,6 +162,17 @@ _SIGS = {
     "mxfp8_tiled_scale_bytes": (C.c_int, [C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
     "mxfp8_gemm": (C.c_int, [_P, C.c_int64, _P, _P, C.c_int64, _P, C.c_int64, C.c_int64, C.c_int64, _P, C.c_int64,
                              C.c_int, C.c_int, _P]),
+    "mxfp8_gemm_epilogue": (C.c_int, [_P, C.c_int64, _P, _P, C.c_int64, _P, C.c_int64, C.c_int64, C.c_int64, _P,
+                                      C.c_int64, C.c_int, C.POINTER(hm_epilogue), _P]),
+    "mxfp8_quantize_bias_workspace": (C.c_int, [C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
+    "mxfp8_quantize_bias": (C.c_int, [_P, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_int, _P, C.c_int64, _P, _P,
+                                      C.c_int64, _P, _P, C.c_int, _P, C.c_size_t, _P]),
+    "head_norm_rope": (C.c_int, [_P, C.c_int, C.c_int, C.c_int64, C.c_int64, C.c_float, C.POINTER(hm_rotation), _P]),
+    "head_norm_rope_backward_workspace": (C.c_int, [_P, C.c_int, C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
+    "head_norm_rope_backward": (C.c_int, [_P, C.c_int, C.c_int, C.c_int64, C.c_int64, C.c_float,
+                                          C.POINTER(hm_rotation), _P, C.c_size_t, _P]),
+    "rope_turns": (C.c_int, [C.c_int32, C.c_double, C.c_int32, C.c_double, C.c_double, C.c_double, C.c_double,
+                             C.POINTER(C.c_uint64), C.POINTER(C.c_float)]),
     "mxfp8_gemm_form": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.c_int, _I32P, _I32P, _I32P]),
     "mxfp8_quantize": (C.c_int, [_P, C.c_int, C.c_int64, C.c_int64, C.c_int64, _P, _P, C.c_int, _P, C.c_int64, _P, _P,
                                  C.c_int64, _P, _P]),
@@ -399,3 +439,64 @@ def grad_norm_clip(tensors, max_norm: float, eps: float, stats: int, workspace: 
     """Global norm of a grad_list and dst = src * min(1, max_norm / (norm + eps)); stats: norm, coefficient."""
     check("grad_norm_clip", lib().grad_norm_clip(tensors, len(tensors), max_norm, eps, stats, workspace,
                                                  workspace_bytes, stream))
+
+
+def mxfp8_gemm_epilogue(a: int, lda: int, a_scales: int, b: int, ldb: int, b_scales: int, m: int, n: int, k: int, d: int,
+                        ldd: int, d_dtype: int, epilogue: hm_epilogue, stream: int = 0) -> None:
+    """The product with bias, activation, gate, residual or their gradients in its epilogue (see include/hm.h)."""
+    check("mxfp8_gemm_epilogue", lib().mxfp8_gemm_epilogue(a, lda, a_scales, b, ldb, b_scales, m, n, k, d, ldd, d_dtype,
+                                                           C.byref(epilogue), stream))
+
+
+def mxfp8_quantize_bias_workspace(rows: int, cols: int) -> int:
+    n = C.c_size_t(0)
+    check("mxfp8_quantize_bias_workspace", lib().mxfp8_quantize_bias_workspace(rows, cols, C.byref(n)))
+    return n.value
+
+
+def mxfp8_quantize_bias(x: int, x_dtype: int, rows: int, cols: int, ldx: int, block: int, q: int, ldq: int, s: int,
+                        qt: int, ldqt: int, st: int, dbias: int, accumulate: bool, workspace: int, workspace_bytes: int,
+                        stream: int = 0) -> None:
+    """mxfp8_quantize without factors, and dbias (+)= the sum of x's rows."""
+    check("mxfp8_quantize_bias", lib().mxfp8_quantize_bias(x, x_dtype, rows, cols, ldx, block, q, ldq, s, qt, ldqt, st,
+                                                           dbias, accumulate, workspace, workspace_bytes, stream))
+
+
+def head_list(groups):
+    """(x, x_row, x_head, y, y_row, y_head, gamma, heads) of every group as the array
+    head_norm_rope takes; build it once for buffers that stay in place."""
+    return (hm_head_group * len(groups))(*[hm_head_group(*g, 0) for g in groups])
+
+
+def head_norm_rope(groups, dtype: int, rows: int, head_dim: int, eps: float, rotation: "hm_rotation | None",
+                   stream: int = 0) -> None:
+    """RMS norm of the heads of a head_list and their rotation by position (see include/hm.h)."""
+    check("head_norm_rope", lib().head_norm_rope(groups, len(groups), dtype, rows, head_dim, eps, rotation, stream))
+
+
+def head_grad_list(groups):
+    """(dy, dy_row, dy_head, x, x_row, x_head, dx, dx_row, dx_head, gamma, dgamma, heads, accumulate) of every group."""
+    return (hm_head_grad * len(groups))(*[hm_head_grad(*g) for g in groups])
+
+
+def head_norm_rope_backward_workspace(groups, rows: int, head_dim: int) -> int:
+    n = C.c_size_t(0)
+    check("head_norm_rope_backward_workspace",
+          lib().head_norm_rope_backward_workspace(groups, len(groups), rows, head_dim, C.byref(n)))
+    return n.value
+
+
+def head_norm_rope_backward(groups, dtype: int, rows: int, head_dim: int, eps: float, rotation: "hm_rotation | None",
+                            workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    check("head_norm_rope_backward",
+          lib().head_norm_rope_backward(groups, len(groups), dtype, rows, head_dim, eps, rotation, workspace,
+                                        workspace_bytes, stream))
+
+
+def rope_turns(rot_dim: int, theta: float = 10000.0, scaling: int = HM_ROPE_UNSCALED, factor: float = 1.0,
+               trained: float = 1.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(frequencies, scale) of head_norm_rope: the frequencies as the signed 64-bit patterns an int64 tensor takes."""
+    out, scale = (C.c_uint64 * min(max(1, rot_dim // 2), HM_HEAD_MAX_DIM))(), C.c_float(0)
+    check("rope_turns", lib().rope_turns(rot_dim, theta, scaling, factor, trained, beta_fast, beta_slow, out,
+                                         C.byref(scale)))
+    return [v - (1 << 64) if v >> 63 else v for v in out], scale.value

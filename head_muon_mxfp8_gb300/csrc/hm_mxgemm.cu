@@ -139,6 +139,118 @@ __device__ __forceinline__ void store_chunk(const MxGemmArgs& p, int i, int j0, 
 }
 
 // ---------------------------------------------------------------------------
+// Epilogue with activation (hm_epilogue).  Elements of D that a thread holds, N of them
+// along a column (ROWS: the pair kernel's and the undivided split kernel's chunks) or
+// along a row (the split kernel's added parts), `count` of them inside D.
+// ---------------------------------------------------------------------------
+template <int N, bool ROWS, bool F32>
+__device__ __forceinline__ void load_like_d(const void* base, int64_t ld, int row, int col, int count, float (&x)[N]) {
+    const int64_t at = static_cast<int64_t>(row) * ld + col, step = ROWS ? ld : 1;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (F32) x[j] = j < count ? static_cast<const float*>(base)[at + j * step] : 0.f;
+        else x[j] = j < count ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at + j * step]) << 16) : 0.f;
+    }
+}
+template <int N, bool ROWS, bool F32>
+__device__ __forceinline__ void store_like_d(void* base, int64_t ld, int row, int col, int count, const float (&x)[N]) {
+    const int64_t at = static_cast<int64_t>(row) * ld + col, step = ROWS ? ld : 1;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (j < count) {
+            if (F32) static_cast<float*>(base)[at + j * step] = x[j];
+            else static_cast<uint16_t*>(base)[at + j * step] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
+        }
+}
+
+// f(x) and f'(x).  SiLU and GELU's tanh form are both x s(u), s the logistic function
+// and u = x (c0 + c1 x^2): 0.5 (1 + tanh(w)) = s(2 w).  x^2 is held finite, so that
+// nothing infinite meets a vanished s or 1 - s (a NaN stays one through x).
+template <int N>
+__device__ __forceinline__ void activate(int act, const float (&x)[N], float (&f)[N], float (&slope)[N]) {
+    if (act == HM_ACT_SILU || act == HM_ACT_GELU_TANH) {
+        const float c0 = act == HM_ACT_SILU ? 1.f : 1.5957691216f;      // 2 sqrt(2 / pi)
+        const float c1 = act == HM_ACT_SILU ? 0.f : 0.0713548162726f;   // 0.044715 of it
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float x2 = fminf(x[j] * x[j], 1e30f);
+            const float s = __fdividef(1.f, 1.f + expf(-x[j] * fmaf(c1, x2, c0)));
+            f[j] = x[j] * s;
+            slope[j] = fmaf(f[j] * (1.f - s), fmaf(3.f * c1, x2, c0), s);
+        }
+    } else if (act == HM_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float phi = 0.5f * erfcf(-0.70710678118654752f * x[j]);
+            f[j] = x[j] * phi;
+            slope[j] = fmaf(x[j] * 0.39894228040143268f, expf(-0.5f * x[j] * x[j]), phi);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const bool off = act == HM_ACT_RELU && x[j] <= 0.f;
+            f[j] = off ? 0.f : x[j];
+            slope[j] = off || x[j] != x[j] ? 0.f : 1.f;
+        }
+    }
+}
+
+template <int N, bool ROWS, bool F32>
+__device__ __forceinline__ void finish_typed(const MxGemmArgs& p, int row, int col, int count, float (&z)[N]) {
+    const MxEpilogue& e = p.e;
+    float x[N], f[N], slope[N], more[N];
+    const bool has_in = e.in != nullptr;
+    if (has_in) load_like_d<N, ROWS, F32>(e.in, e.ld_in, row, col, count, x);
+    if (e.in2) load_like_d<N, ROWS, F32>(e.in2, e.ld_in2, row, col, count, more);
+    if (e.bias) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) z[j] += ROWS ? e.bias[col] : j < count ? e.bias[col + j] : 0.f;
+    }
+    if (e.form == HM_EPI_FORWARD) {
+        if (e.out2) store_like_d<N, ROWS, F32>(e.out2, e.ld_out2, row, col, count, z);
+        activate<N>(e.act, z, f, slope);
+#pragma unroll
+        for (int j = 0; j < N; ++j) z[j] = has_in ? f[j] + x[j] : f[j];
+    } else {
+        activate<N>(e.act, x, f, slope);
+        if (e.form == HM_EPI_GRADIENT) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) z[j] *= slope[j];
+        } else {
+            if (e.form == HM_EPI_GATED_GRADIENT) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) more[j] = z[j] * more[j] * slope[j];
+                store_like_d<N, ROWS, F32>(e.out2, e.ld_out2, row, col, count, more);
+            } else if (e.out2) {
+                store_like_d<N, ROWS, F32>(e.out2, e.ld_out2, row, col, count, z);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) z[j] *= f[j];
+        }
+    }
+    store_like_d<N, ROWS, F32>(p.d, p.ldd, row, col, count, z);
+}
+template <int N, bool ROWS>
+__device__ __forceinline__ void finish(const MxGemmArgs& p, int row, int col, int count, float (&z)[N]) {
+    if (p.d_f32) finish_typed<N, ROWS, true>(p, row, col, count, z);
+    else finish_typed<N, ROWS, false>(p, row, col, count, z);
+}
+// 16 rows from j0 of column i
+template <bool F32_ONLY = false>
+__device__ __forceinline__ void finish16(const MxGemmArgs& p, int i, int j0, const uint32_t (&r)[16]) {
+    if (i >= p.n) return;
+#pragma unroll
+    for (int b = 0; b < 16; b += 8) {
+        if (j0 + b >= p.m) return;
+        float z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(r[b + j]);
+        if (F32_ONLY) finish_typed<8, true, true>(p, j0 + b, i, min(8, p.m - (j0 + b)), z);
+        else finish<8, true>(p, j0 + b, i, min(8, p.m - (j0 + b)), z);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Persistent kernel on CTA pairs (cta_group::2), tiles of 256 M-side rows (B's
 // rows, D's columns) x BN N-side rows (A's, D's rows), 320 threads per CTA.  Each CTA of a pair loads its 128 M-side rows
 // and half of the N-side rows; the even one issues the MMAs, which read both
@@ -191,7 +303,7 @@ __device__ __forceinline__ void pair_tile(const MxGemmArgs& p, int t, int& tp, i
     tq = l / rows;
 }
 
-template <int BN, bool SUMS>
+template <int BN, bool SUMS, bool EPI>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUtensorMap mq,
                         const __grid_constant__ CUtensorMap msp, const __grid_constant__ CUtensorMap msq,
@@ -349,7 +461,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             pair_tile(p, t, tp, tq);
             const int i = tp * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
             float sum[SUMS ? (C::CHUNKS + 1) / 2 : 1][32];
-            if (p.accumulate) {
+            if (EPI) {
+                // what the epilogue reads, likewise (see below)
+#pragma unroll
+                for (int ch = half; ch < C::CHUNKS; ch += 2) {
+                    const int64_t row = tq * BN + ch * 32 + lane;
+                    if (i - lane >= p.n || row >= p.m) continue;
+                    const int es = p.d_f32 ? 4 : 2;
+                    if (p.e.in) prefetch_l2(static_cast<const char*>(p.e.in) + (row * p.e.ld_in + (i - lane)) * es);
+                    if (p.e.in2) prefetch_l2(static_cast<const char*>(p.e.in2) + (row * p.e.ld_in2 + (i - lane)) * es);
+                }
+            } else if (p.accumulate) {
                 // the earlier D is read when the tile is done: start it into the L2
                 // now, lane l the line of row l of each chunk
 #pragma unroll
@@ -368,6 +490,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 // first (even half); that half drains it first, the other has nothing to release
                 const bool owner = BN == 256 && half == ((u & 1) ? 0 : 1);
                 if (BN == 256 && !owner) release(freed);
+                if constexpr (EPI && !SUMS) {
+                    // one copy of the epilogue's code: 16 columns of the accumulator at a time
+#pragma unroll 1
+                    for (int k = 0; k < (C::CHUNKS + 1) / 2 * 2; ++k) {
+                        const int order = BN == 256 && !(u & 1) ? (C::CHUNKS + 1) / 2 - 1 - (k >> 1) : k >> 1;
+                        const int ch = 2 * order + half;
+                        if (ch >= C::CHUNKS) break;
+                        const int at = ch * 32 + (k & 1) * 16;
+                        uint32_t r[16];
+                        __syncwarp();
+                        tmem_ld16(acc + at, r);
+                        tmem_ld_wait();
+                        tmem_ld_pin16(r);
+                        if (owner && k == 1) release(freed);
+                        finish16(p, i, tq * BN + at, r);
+                    }
+                    if (BN != 256) release(freed);
+                    continue;
+                }
 #pragma unroll
                 for (int k = 0; k < (C::CHUNKS + 1) / 2; ++k) {
                     const int order = BN == 256 && !(u & 1) ? (C::CHUNKS + 1) / 2 - 1 - k : k;
@@ -404,6 +545,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 for (int k = 0; k < (C::CHUNKS + 1) / 2; ++k) {
                     const int ch = 2 * k + half;
                     if (ch >= C::CHUNKS) break;
+                    if constexpr (EPI) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t r[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(sum[k][16 * h + j]);
+                            finish16<true>(p, i, tq * BN + ch * 32 + h * 16, r);
+                        }
+                        continue;
+                    }
                     uint32_t r[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[k][j]);
@@ -494,8 +645,8 @@ __device__ __forceinline__ void store_four(const MxGemmArgs& p, int row, int col
 // shared memory in flight (with two rows at a time the latency of those loads
 // made a split in two slower than none: 16.4 us against 14.5 at 355 x 3149 x
 // 4704).
-template <int CK>
-__device__ __forceinline__ void add_parts(const MxGemmArgs& p, const float* part, int rank, int warp, int lane, int col0,
+template <int CK, bool EPI>
+__device__ __forceinline__ void add_parts(const MxGemmArgs& p, float* part, int rank, int warp, int lane, int col0,
                                           int row0, int rows) {
     constexpr int U = 16 / CK;
     const uint32_t mine = smem_u32(part) + static_cast<uint32_t>(lane) * 16;
@@ -518,12 +669,14 @@ __device__ __forceinline__ void add_parts(const MxGemmArgs& p, const float* part
 #pragma unroll
             for (int k = 1; k < CK; ++k)
                 v = make_float4(v.x + x[h][k].x, v.y + x[h][k].y, v.z + x[h][k].z, v.w + x[h][k].w);
-            store_four(p, row0 + c + h * step, col, v);
+            // with an epilogue the sum goes over this CTA's own part, which only this lane reads
+            if constexpr (EPI) *reinterpret_cast<float4*>(part + (c + h * step) * 128 + lane * 4) = v;
+            else store_four(p, row0 + c + h * step, col, v);
         }
     }
 }
 
-template <int BN>
+template <int BN, bool EPI>
 __global__ void __launch_bounds__(kSplitThreads, 1)
     mx_gemm_split_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
                          const __grid_constant__ MxGemmArgs p) {
@@ -629,7 +782,17 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     if (warp >= 2) {
         const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(tfull), 0, p.err, bail));
         tc_fence_after();
-        if (ok) {
+        if (EPI && ok && ck == 1) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < rows; c0 += 16) {
+                uint32_t r[16];
+                __syncwarp();
+                tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, r);
+                tmem_ld_wait();
+                tmem_ld_pin16(r);
+                finish16(p, col, row0 + c0, r);
+            }
+        } else if (ok) {
 #pragma unroll 1
             for (int c0 = 0; c0 < rows; c0 += 32) {
                 uint32_t r[32];
@@ -655,13 +818,22 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         cluster_sync_all();
         const int c0 = tp * kTileP;
         switch (ck) {
-            case 2: add_parts<2>(p, part, rank, warp, lane, c0, row0, rows); break;
-            case 3: add_parts<3>(p, part, rank, warp, lane, c0, row0, rows); break;
-            case 4: add_parts<4>(p, part, rank, warp, lane, c0, row0, rows); break;
-            case 5: add_parts<5>(p, part, rank, warp, lane, c0, row0, rows); break;
-            case 6: add_parts<6>(p, part, rank, warp, lane, c0, row0, rows); break;
-            case 7: add_parts<7>(p, part, rank, warp, lane, c0, row0, rows); break;
-            default: add_parts<8>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 2: add_parts<2, EPI>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 3: add_parts<3, EPI>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 4: add_parts<4, EPI>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 5: add_parts<5, EPI>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 6: add_parts<6, EPI>(p, part, rank, warp, lane, c0, row0, rows); break;
+            case 7: add_parts<7, EPI>(p, part, rank, warp, lane, c0, row0, rows); break;
+            default: add_parts<8, EPI>(p, part, rank, warp, lane, c0, row0, rows); break;
+        }
+        if constexpr (EPI) {
+            // the same rows and columns as above, one copy of the epilogue's code
+#pragma unroll 1
+            for (int c = rank + warp * ck; c < rows; c += ck * (kSplitThreads / 32)) {
+                const float4 v = *reinterpret_cast<const float4*>(part + c * 128 + lane * 4);
+                float z[4] = {v.x, v.y, v.z, v.w};
+                if (c0 + lane * 4 < p.n) finish<4, false>(p, row0 + c, c0 + lane * 4, min(4, p.n - (c0 + lane * 4)), z);
+            }
         }
         __syncwarp();
         cluster_arrive_relaxed();  // a CTA's part stays until its peers have read it
@@ -682,6 +854,16 @@ __global__ void __launch_bounds__(256) mx_gemm_zero_kernel(const __grid_constant
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll)
         if (p.d_f32) static_cast<float*>(p.d)[i / p.n * p.ldd + i % p.n] = 0.f;
         else static_cast<uint16_t*>(p.d)[i / p.n * p.ldd + i % p.n] = 0u;
+}
+
+// The same with an epilogue: z = 0 before the bias.
+__global__ void __launch_bounds__(256) mx_gemm_empty_kernel(const __grid_constant__ MxGemmArgs p) {
+    wait_for_earlier_kernels();
+    const int64_t total = static_cast<int64_t>(p.m) * p.n;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        float z[1] = {0.f};
+        finish<1, true>(p, static_cast<int>(i / p.n), static_cast<int>(i % p.n), 1, z);
+    }
 }
 
 // Codes [rows][ld], k of them used: boxes of box_rows x 128 bytes, zero outside.
@@ -747,7 +929,7 @@ int resident_clusters(int split) {
     cudaLaunchAttribute attr[2];
     split_config<BN>(cfg, attr, 1, 1, split, nullptr);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_split_kernel<BN>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_split_kernel<BN, false>, &cfg) != cudaSuccess || n < 1) {
         cudaGetLastError();
         n = std::max(1, device_sm_count() / (2 * split));
     }
@@ -786,7 +968,7 @@ int split_for(int tiles_p, int tiles_q, const MxGemmArgs& p, double* cost) {
 template <int BN>
 cudaError_t split_form(const MxGemmArgs& p, MxGemmForm* f, double* cost) {
     static PerDevice done;
-    const cudaError_t e = allow_smem(mx_gemm_split_kernel<BN>, SplitCfg<BN>::SMEM, done);  // before its occupancy is asked
+    const cudaError_t e = allow_smem(mx_gemm_split_kernel<BN, false>, SplitCfg<BN>::SMEM, done);  // before its occupancy is asked
     if (e != cudaSuccess) return e;
     f->tile = BN;
     f->parts = split_for<BN>((p.n + kTileP - 1) / kTileP, (p.m + BN - 1) / BN, p, cost);
@@ -801,15 +983,21 @@ cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     split_config<BN>(cfg, attr, (p.n + kTileP - 1) / kTileP, (p.m + BN - 1) / BN, p.split, st);
+    if (p.epilogue) {
+        static PerDevice done;
+        const cudaError_t e = allow_smem(mx_gemm_split_kernel<BN, true>, SplitCfg<BN>::SMEM, done);
+        if (e != cudaSuccess) return e;
+    }
     note_launch();
-    return cudaLaunchKernelEx(&cfg, mx_gemm_split_kernel<BN>, ma, mb, p);
+    return cudaLaunchKernelEx(&cfg, p.epilogue ? mx_gemm_split_kernel<BN, true> : mx_gemm_split_kernel<BN, false>, ma, mb, p);
 }
 
-template <int BN, bool SUMS>
+template <int BN, bool SUMS, bool EPI = false>
 cudaError_t launch_pair(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, MxGemmArgs p, cudaStream_t st) {
     using C = PairMx<BN>;
+    if (!EPI && p.epilogue) return launch_pair<BN, SUMS, true>(a, lda, b, ldb, p, st);
     static PerDevice done;
-    cudaError_t e = allow_smem(mx_gemm_pair_kernel<BN, SUMS>, C::SMEM, done);
+    cudaError_t e = allow_smem(mx_gemm_pair_kernel<BN, SUMS, EPI>, C::SMEM, done);
     if (e != cudaSuccess) return e;
     CUtensorMap mp, mq, msp, msq;
     if (!map_codes(&mp, b, p.k, p.n, ldb, kTileP) || !map_codes(&mq, a, p.k, p.m, lda, BN / 2) ||
@@ -827,7 +1015,7 @@ cudaError_t launch_pair(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t
     cudaLaunchAttribute attr[2];
     cluster_early(cfg, attr, 2);
     note_launch();
-    return cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<BN, SUMS>, mp, mq, msp, msq, p);
+    return cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<BN, SUMS, EPI>, mp, mq, msp, msq, p);
 }
 
 }  // namespace
@@ -886,6 +1074,10 @@ cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int6
         if (p.accumulate) return cudaSuccess;
         const int64_t blocks = (static_cast<int64_t>(p.m) * p.n + 255) / 256;
         note_launch();
+        if (p.epilogue) {
+            mx_gemm_empty_kernel<<<resident_grid(mx_gemm_empty_kernel, 256, blocks), 256, 0, st>>>(p);
+            return cudaGetLastError();
+        }
         mx_gemm_zero_kernel<<<resident_grid(mx_gemm_zero_kernel, 256, blocks), 256, 0, st>>>(p);
         return cudaGetLastError();
     }

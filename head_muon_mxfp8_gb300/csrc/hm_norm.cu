@@ -470,6 +470,405 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* partials, int
     }
 }
 
+// ---------------------------------------------------------------------------
+// Heads: norm and rotation in one pass.
+//
+// A pair's angle is positions[row] * freq[i].  In turns, as fixed point with 2^64
+// for a whole one, the product in 64-bit integers drops whole turns by wrapping, so
+// the fraction is exact to the frequency's own last bit times the position:
+// 2^-65 * 10^6 of a turn at the millionth token, where a product in fp32 would be
+// off by 0.06 radians.  The quarter turn is split off as an integer too; sin and cos
+// see at most an eighth of a turn.
+//
+// The pairs of a head lie in vectors of W elements: vector pair v is the W first and
+// the W second elements of pairs (halves), or two vectors of adjacent pairs; past
+// the rotated part, two vectors of the rest.  A group of `lanes` lanes holds a head,
+// V vector pairs each, so a pair never leaves its thread and in-place work is safe.
+// W is the widest that divides the head, its rotated part, strides and addresses.
+// ---------------------------------------------------------------------------
+constexpr int kHeadThreads = 256;
+
+template <bool F32, int W>
+struct HeadVec {
+    static constexpr int kBytes = W * (F32 ? 4 : 2);
+    static constexpr int N = kBytes < 4 ? 1 : kBytes / 4;
+    uint32_t w[N];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < N; ++k) w[k] = 0u;
+    }
+    __device__ __forceinline__ void load(const void* base, int64_t at) {
+        const char* p = static_cast<const char*>(base) + at * (F32 ? 4 : 2);
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int k = 0; k < N / 4; ++k) {
+                const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + k);
+                w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+            }
+        } else if constexpr (kBytes == 8) {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+            w[0] = v.x; w[1] = v.y;
+        } else if constexpr (kBytes == 4) {
+            w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
+        } else {
+            w[0] = __ldcs(reinterpret_cast<const uint16_t*>(p));
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[W]) const {
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            v[k] = F32 ? __uint_as_float(w[F32 ? k : 0])
+                       : __uint_as_float(k & 1 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+    }
+    static __device__ __forceinline__ void put(void* base, int64_t at, const float (&v)[W]) {
+        char* p = static_cast<char*>(base) + at * (F32 ? 4 : 2);
+        uint32_t w[N];
+        if constexpr (F32) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k] = __float_as_uint(v[k]);
+        } else if constexpr (W == 1) {
+            w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                w[k] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+        }
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int k = 0; k < N / 4; ++k)
+                reinterpret_cast<uint4*>(p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        } else if constexpr (kBytes == 8) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        } else if constexpr (kBytes == 4) {
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+        } else {
+            *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+        }
+    }
+};
+
+// Where a lane's vector pair v begins in a head, and its place in the table.
+template <int W>
+struct HeadPlace {
+    int a, b;      // first elements of its two vectors
+    int v;
+    bool live, rotated;
+    __device__ __forceinline__ HeadPlace(const HeadArgs& p, int v_) : v(v_) {
+        const int turned = p.rot / (2 * W), all = p.dim / (2 * W);
+        live = v < all;
+        rotated = v < turned;
+        if (!rotated) {
+            a = p.rot + W * (v - turned);
+            b = a + (p.dim - p.rot) / 2;
+        } else if (W == 1 && p.pairs) {
+            a = 2 * v;
+            b = a + 1;
+        } else {
+            a = W * v;
+            b = a + p.rot / 2;
+        }
+    }
+};
+
+// (cos, sin) of `tokens` rows from tok0, scaled: the table's entry (t, e, v) is the e-th
+// pair of vector pair v, so that neighbouring lanes read neighbouring words.
+template <int W>
+__device__ __forceinline__ void head_table(const HeadArgs& p, int64_t tok0, int tokens, float2* table) {
+    const int half = p.rot / 2, turned = p.rot / (2 * W);
+    for (int i = threadIdx.x; i < tokens * half; i += kHeadThreads) {
+        const int t = i / half, c = i - t * half;  // pair c of row tok0 + t
+        int v, e;
+        if (W > 1 && p.pairs) {  // a vector holds W / 2 pairs; the second vector's follow the first's
+            const int vec = c / (W / 2), in = c - vec * (W / 2);
+            v = vec < turned ? vec : vec - turned;
+            e = vec < turned ? in : W / 2 + in;
+        } else {
+            v = c / W;
+            e = c - v * W;
+        }
+        const uint64_t turn = static_cast<uint64_t>(p.positions[tok0 + t]) * p.turns[c];
+        const uint32_t hi = static_cast<uint32_t>(turn >> 32);
+        const uint32_t quarter = (hi + 0x20000000u) >> 30;
+        const int32_t rest = static_cast<int32_t>(hi - (quarter << 30));  // an eighth of a turn at most
+        float s, c0;
+        sincospif(static_cast<float>(rest) * 0x1p-31f, &s, &c0);
+        const float cq = quarter & 1 ? s : c0, sq = quarter & 1 ? c0 : s;
+        const float cs = (quarter + 1) & 2 ? -cq : cq, sn = quarter & 2 ? -sq : sq;
+        table[(t * W + e) * turned + v] = make_float2(cs * p.scale, sn * p.scale);
+    }
+}
+
+// Turns the pairs of (a, b) by the table's angles, or back.
+template <int W, bool BACK>
+__device__ __forceinline__ void head_turn(const HeadArgs& p, const HeadPlace<W>& at, const float2* row, float (&a)[W],
+                                          float (&b)[W]) {
+    if (!at.rotated) return;
+    const int turned = p.rot / (2 * W);
+    if (W > 1 && p.pairs) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            const float2 cs = row[e * turned + at.v];
+            const float s = BACK ? -cs.y : cs.y;
+            float& u = e < W / 2 ? a[(2 * e) % W] : b[(2 * e) % W];
+            float& v = e < W / 2 ? a[(2 * e + 1) % W] : b[(2 * e + 1) % W];
+            const float u1 = u * cs.x - v * s, v1 = v * cs.x + u * s;
+            u = u1;
+            v = v1;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            const float2 cs = row[e * turned + at.v];
+            const float s = BACK ? -cs.y : cs.y;
+            const float u1 = a[e] * cs.x - b[e] * s, v1 = b[e] * cs.x + a[e] * s;
+            a[e] = u1;
+            b[e] = v1;
+        }
+    }
+}
+
+// Sum over a head's lanes.
+__device__ __forceinline__ float head_sum(float v, int lanes) {
+    for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ int head_group(const HeadArgs& p) {
+    int g = 0;
+    while (g + 1 < p.n && static_cast<int>(blockIdx.x) >= p.g[g + 1].cta0) ++g;
+    return g;
+}
+
+template <bool F32, int W, int V, int U>
+__global__ void __launch_bounds__(kHeadThreads) head_kernel(const __grid_constant__ HeadArgs p) {
+    extern __shared__ float2 table[];
+    wait_for_earlier_kernels();
+    const HeadGroup& g = p.g[head_group(p)];
+    const int local = static_cast<int>(blockIdx.x) - g.cta0;
+    const int64_t tok0 = static_cast<int64_t>(local / g.parts) * g.tokens;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(g.tokens), p.rows - tok0));
+    const int lane = threadIdx.x & (p.lanes - 1), slot = threadIdx.x / p.lanes, slots = kHeadThreads / p.lanes;
+    const int items = tokens * g.heads, step = slots * g.parts;
+    const float inv_dim = static_cast<float>(p.dim);
+    float ga[V][W], gb[V][W];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const HeadPlace<W> at(p, lane + v * p.lanes);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            ga[v][e] = g.gamma && at.live ? g.gamma[at.a + e] : 1.f;
+            gb[v][e] = g.gamma && at.live ? g.gamma[at.b + e] : 1.f;
+        }
+    }
+    if (p.rot) head_table<W>(p, tok0, tokens, table);
+    __syncthreads();
+    // whole warps stay in the loop: a head's sum is over lanes
+    for (int first = (local % g.parts) * slots; first < items; first += U * step) {
+        HeadVec<F32, W> xa[U][V], xb[U][V];
+        int row[U], head[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int item = first + u * step + slot;
+            row[u] = item / g.heads;
+            head[u] = item - row[u] * g.heads;
+            const int64_t base = (tok0 + row[u]) * g.in_row + head[u] * g.in_head;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const HeadPlace<W> at(p, lane + v * p.lanes);
+                xa[u][v].clear();
+                xb[u][v].clear();
+                if (item < items && at.live) {
+                    xa[u][v].load(g.in, base + at.a);
+                    xb[u][v].load(g.in, base + at.b);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float a[V][W], b[V][W], sq = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                xa[u][v].get(a[v]);
+                xb[u][v].get(b[v]);
+#pragma unroll
+                for (int e = 0; e < W; ++e) sq = fmaf(a[v][e], a[v][e], fmaf(b[v][e], b[v][e], sq));
+            }
+            if (g.gamma) {
+                const float rstd = inv_root(head_sum(sq, p.lanes), inv_dim, p.eps);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) {
+                        a[v][e] = a[v][e] * rstd * ga[v][e];
+                        b[v][e] = b[v][e] * rstd * gb[v][e];
+                    }
+            }
+            if (first + u * step + slot >= items) continue;
+            const int64_t base = (tok0 + row[u]) * g.out_row + head[u] * g.out_head;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const HeadPlace<W> at(p, lane + v * p.lanes);
+                if (!at.live) continue;
+                head_turn<W, false>(p, at, table + row[u] * (p.rot / 2), a[v], b[v]);
+                HeadVec<F32, W>::put(g.out, base + at.a, a[v]);
+                HeadVec<F32, W>::put(g.out, base + at.b, b[v]);
+            }
+        }
+    }
+}
+
+// Gradient.  With t = dy turned back, u = t gamma, S1 = sum x^2 and S2 = sum u x, both
+// in the same round of shuffles: dx = r u - x r^3 S2 / dim.  A CTA takes steps of
+// `tokens` rows round-robin and keeps its lanes' part of dgamma in registers; the
+// lanes that hold the same elements are added at the end in a fixed order.
+template <bool F32, int W, int V>
+__global__ void __launch_bounds__(kHeadThreads) head_grad_kernel(const __grid_constant__ HeadArgs p) {
+    extern __shared__ float2 table[];
+    wait_for_earlier_kernels();
+    const HeadGroup& g = p.g[head_group(p)];
+    const int local = static_cast<int>(blockIdx.x) - g.cta0;
+    const int lane = threadIdx.x & (p.lanes - 1), slot = threadIdx.x / p.lanes, slots = kHeadThreads / p.lanes;
+    const float dim = static_cast<float>(p.dim);
+    float ga[V][W], gb[V][W], da[V][W], db[V][W];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const HeadPlace<W> at(p, lane + v * p.lanes);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            ga[v][e] = g.gamma && at.live ? g.gamma[at.a + e] : 0.f;
+            gb[v][e] = g.gamma && at.live ? g.gamma[at.b + e] : 0.f;
+            da[v][e] = db[v][e] = 0.f;
+        }
+    }
+    for (int64_t tok0 = static_cast<int64_t>(local) * g.tokens; tok0 < p.rows; tok0 += static_cast<int64_t>(g.parts) * g.tokens) {
+        const int tokens = static_cast<int>(min(static_cast<int64_t>(g.tokens), p.rows - tok0));
+        const int items = tokens * g.heads;
+        __syncthreads();  // the table before has been read
+        if (p.rot) head_table<W>(p, tok0, tokens, table);
+        __syncthreads();
+        for (int first = 0; first < items; first += slots) {
+            const int item = first + slot;
+            const int row = item / g.heads, head = item - row * g.heads;
+            const int64_t in = (tok0 + row) * g.in_row + head * g.in_head;
+            const int64_t at_x = (tok0 + row) * g.x_row + head * g.x_head;
+            HeadVec<F32, W> ya[V], yb[V], xa[V], xb[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const HeadPlace<W> at(p, lane + v * p.lanes);
+                ya[v].clear(); yb[v].clear(); xa[v].clear(); xb[v].clear();
+                if (item < items && at.live) {
+                    ya[v].load(g.in, in + at.a);
+                    yb[v].load(g.in, in + at.b);
+                    if (g.gamma) {
+                        xa[v].load(g.x, at_x + at.a);
+                        xb[v].load(g.x, at_x + at.b);
+                    }
+                }
+            }
+            float ta[V][W], tb[V][W], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const HeadPlace<W> at(p, lane + v * p.lanes);
+                ya[v].get(ta[v]);
+                yb[v].get(tb[v]);
+                if (item < items && at.live) head_turn<W, true>(p, at, table + row * (p.rot / 2), ta[v], tb[v]);
+                float x[W], z[W];
+                xa[v].get(x);
+                xb[v].get(z);
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    s1 = fmaf(x[e], x[e], fmaf(z[e], z[e], s1));
+                    s2 = fmaf(ta[v][e] * ga[v][e], x[e], fmaf(tb[v][e] * gb[v][e], z[e], s2));
+                }
+            }
+            if (g.gamma) {
+                for (int o = p.lanes >> 1; o; o >>= 1) {
+                    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+                    s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+                }
+                const float r = inv_root(s1, dim, p.eps);
+                const float back = -r * (r * s2 / dim);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float x[W], z[W];
+                    xa[v].get(x);
+                    xb[v].get(z);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) {
+                        const float hx = x[e] * r, hz = z[e] * r;
+                        if (item < items) {
+                            da[v][e] = fmaf(ta[v][e], hx, da[v][e]);
+                            db[v][e] = fmaf(tb[v][e], hz, db[v][e]);
+                        }
+                        ta[v][e] = fmaf(hx, back, ta[v][e] * ga[v][e] * r);
+                        tb[v][e] = fmaf(hz, back, tb[v][e] * gb[v][e] * r);
+                    }
+                }
+            }
+            if (item >= items) continue;
+            const int64_t out = (tok0 + row) * g.out_row + head * g.out_head;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const HeadPlace<W> at(p, lane + v * p.lanes);
+                if (!at.live) continue;
+                HeadVec<F32, W>::put(g.out, out + at.a, ta[v]);
+                HeadVec<F32, W>::put(g.out, out + at.b, tb[v]);
+            }
+        }
+    }
+    if (!g.partials) return;
+    // lanes of a warp that hold the same elements, then the warps in order
+    float* part = reinterpret_cast<float*>(table);  // [warps][dim]
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const HeadPlace<W> at(p, lane + v * p.lanes);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            float x = da[v][e], y = db[v][e];
+            for (int o = 16; o >= p.lanes; o >>= 1) {
+                x += __shfl_xor_sync(0xffffffffu, x, o);
+                y += __shfl_xor_sync(0xffffffffu, y, o);
+            }
+            if (static_cast<int>(threadIdx.x & 31) < p.lanes && at.live) {
+                part[(threadIdx.x >> 5) * p.dim + at.a + e] = x;
+                part[(threadIdx.x >> 5) * p.dim + at.b + e] = y;
+            }
+        }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.dim; c += kHeadThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kHeadThreads / 32; ++w) s += part[w * p.dim + c];
+        g.partials[static_cast<int64_t>(local) * p.dim + c] = s;
+    }
+}
+
+// dgamma of every group from its CTAs' partials, as dgamma_kernel does.
+__global__ void __launch_bounds__(1024) head_dgamma_kernel(const __grid_constant__ HeadArgs p) {
+    __shared__ float red[32][33];
+    wait_for_earlier_kernels();
+    const HeadGroup& g = p.g[blockIdx.y];
+    if (!g.dgamma) return;
+    const int c = threadIdx.x & 31, k0 = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + c;
+    float s = 0.f;
+    if (col < p.dim && g.partials)
+#pragma unroll 10
+        for (int k = k0; k < g.parts; k += 32) s += g.partials[static_cast<int64_t>(k) * p.dim + col];
+    red[k0][c] = s;
+    __syncthreads();
+    if (k0 == 0 && col < p.dim) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) t += red[k][c];
+        g.dgamma[col] = g.accumulate ? g.dgamma[col] + t : t;
+    }
+}
+
 template <bool F32>
 cudaError_t launch_fwd(const RmsArgs& a, cudaStream_t st) {
     const unsigned rows = static_cast<unsigned>((a.rows + 127) / 128 * 128);
@@ -535,7 +934,124 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
     return launch_early(dgamma_kernel, a.d / 32, 1024, 0, st, a.partials, parts, a.d, a.accumulate, a.dgamma);
 }
 
+// Lanes per head: the fewest that hold it with V vector pairs each, a power of two.
+int head_lanes(int dim, int width, int v) {
+    const int pairs = dim / (2 * width);
+    int lanes = 1;
+    while (lanes * v < pairs) lanes *= 2;
+    return lanes;
+}
+
+// Rows per step: enough heads for kHeadRounds rounds of a CTA's slots, up to as many
+// again where that wastes fewer slots in the last round, within the table's bytes.
+constexpr int kHeadRounds = 4;
+constexpr int kHeadTable = 32 * 1024;
+int head_tokens(int heads, int lanes, int rot) {
+    const int slots = kHeadThreads / lanes;
+    const int most = rot ? std::max(1, kHeadTable / (rot * 4)) : 1024;
+    const int least = std::min(most, std::max(1, kHeadRounds * slots / heads));
+    int best = least;
+    double use = 0;
+    for (int t = least; t <= std::min(most, 2 * least); ++t) {
+        const int rounds = (t * heads + slots - 1) / slots;
+        const double u = static_cast<double>(t) * heads / (static_cast<double>(rounds) * slots);
+        if (u > use + 1e-9) use = u, best = t;
+    }
+    return best;
+}
+
+template <bool F32, int W, int V, int U>
+cudaError_t run_heads(HeadArgs& a, cudaStream_t st) {
+    a.lanes = head_lanes(a.dim, W, V);
+    const int slots = kHeadThreads / a.lanes;
+    const int64_t sms = device_sm_count();
+    int64_t ctas = 0;
+    size_t smem = 0;
+    for (int i = 0; i < a.n; ++i) {
+        HeadGroup& g = a.g[i];
+        g.tokens = head_tokens(g.heads, a.lanes, a.rot);
+        // few rows: fewer per step, then a step's heads over several CTAs, until each SM has one
+        while (g.tokens > 1 && (a.rows + g.tokens - 1) / g.tokens < 2 * sms) g.tokens = (g.tokens + 1) / 2;
+        const int64_t steps = (a.rows + g.tokens - 1) / g.tokens;
+        const int rounds = (g.tokens * g.heads + slots - 1) / slots;
+        g.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rounds, 2 * sms / steps)));
+        g.cta0 = static_cast<int32_t>(ctas);
+        ctas += steps * g.parts;
+        smem = std::max(smem, static_cast<size_t>(g.tokens) * a.rot * 4);
+    }
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    note_launch();
+    return launch_early(head_kernel<F32, W, V, U>, static_cast<unsigned>(ctas), kHeadThreads, static_cast<int>(smem), st, a);
+}
+
+template <bool F32, int W, int V>
+cudaError_t run_heads_grad(HeadArgs& a, cudaStream_t st) {
+    a.lanes = head_lanes(a.dim, W, V);
+    int64_t ctas = 0;
+    size_t smem = static_cast<size_t>(kHeadThreads / 32) * a.dim * 4;
+    int wanted = 0, all = 0;
+    for (int i = 0; i < a.n; ++i) all += a.g[i].heads;
+    for (int i = 0; i < a.n; ++i) {
+        HeadGroup& g = a.g[i];
+        g.cta0 = static_cast<int32_t>(ctas);
+        wanted += g.dgamma != nullptr;
+        if (!g.heads || !a.rows) continue;  // an empty sum: parts = 0
+        g.parts = head_grad_parts(a.rows, g.heads, all);
+        g.tokens = head_tokens(g.heads, a.lanes, a.rot);
+        while (g.tokens > 1 && (a.rows + g.tokens - 1) / g.tokens < g.parts) g.tokens = (g.tokens + 1) / 2;
+        ctas += g.parts;
+        smem = std::max(smem, static_cast<size_t>(g.tokens) * a.rot * 4);
+    }
+    if (ctas) {
+        note_launch();
+        const cudaError_t e = launch_early(head_grad_kernel<F32, W, V>, static_cast<unsigned>(ctas), kHeadThreads,
+                                           static_cast<int>(smem), st, a);
+        if (e != cudaSuccess || !wanted) return e;
+    }
+    if (!wanted) return cudaSuccess;
+    note_launch();
+    return launch_early(head_dgamma_kernel, dim3((a.dim + 31) / 32, a.n), 1024, 0, st, a);
+}
+
 }  // namespace
+
+int head_width(const HeadArgs& a, int64_t es) {
+    for (int w = 8; w > 1; w /= 2) {
+        bool ok = a.dim % (2 * w) == 0 && a.rot % (2 * w) == 0;
+        const int64_t bytes = std::min<int64_t>(16, w * es);
+        const auto fits = [&](const void* p, int64_t row, int64_t head) {
+            return reinterpret_cast<uintptr_t>(p) % bytes == 0 && row * es % bytes == 0 && head * es % bytes == 0;
+        };
+        for (int i = 0; i < a.n; ++i)
+            ok = ok && fits(a.g[i].in, a.g[i].in_row, a.g[i].in_head) && fits(a.g[i].x, a.g[i].x_row, a.g[i].x_head) &&
+                 fits(a.g[i].out, a.g[i].out_row, a.g[i].out_head);
+        if (ok) return w;
+    }
+    return 1;
+}
+
+int head_grad_parts(int64_t rows, int heads, int all_heads) {
+    const int64_t ctas = 3 * static_cast<int64_t>(device_sm_count());
+    return static_cast<int>(std::min<int64_t>(rows, std::max<int64_t>(1, ctas * heads / all_heads)));
+}
+
+cudaError_t launch_heads(HeadArgs a, int f32, cudaStream_t st) {
+    switch (a.width) {
+        case 8: return f32 ? run_heads<true, 8, 1, 1>(a, st) : run_heads<false, 8, 1, 2>(a, st);
+        case 4: return f32 ? run_heads<true, 4, 2, 1>(a, st) : run_heads<false, 4, 2, 1>(a, st);
+        case 2: return f32 ? run_heads<true, 2, 4, 1>(a, st) : run_heads<false, 2, 4, 1>(a, st);
+        default: return f32 ? run_heads<true, 1, 8, 1>(a, st) : run_heads<false, 1, 8, 1>(a, st);
+    }
+}
+
+cudaError_t launch_heads_grad(HeadArgs a, int f32, cudaStream_t st) {
+    switch (a.width) {
+        case 8: return f32 ? run_heads_grad<true, 8, 1>(a, st) : run_heads_grad<false, 8, 1>(a, st);
+        case 4: return f32 ? run_heads_grad<true, 4, 2>(a, st) : run_heads_grad<false, 4, 2>(a, st);
+        case 2: return f32 ? run_heads_grad<true, 2, 4>(a, st) : run_heads_grad<false, 2, 4>(a, st);
+        default: return f32 ? run_heads_grad<true, 1, 8>(a, st) : run_heads_grad<false, 1, 8>(a, st);
+    }
+}
 
 int rmsnorm_grad_parts(int64_t rows, int64_t d) {
     const int64_t sms = device_sm_count();

@@ -45,7 +45,17 @@ inline cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int thread
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+struct MxEpilogue {
+    int32_t form, act;   // HM_EPI_*, HM_ACT_*
+    const float* bias;
+    const void* in;      // matrices of D's shape and type
+    const void* in2;
+    void* out2;
+    int64_t ld_in, ld_in2, ld_out2;
+};
 struct MxGemmArgs {
+    MxEpilogue e;        // with `epilogue`
+    int32_t epilogue, pad;
     const uint8_t* sa;   // tiled scales
     const uint8_t* sb;
     void* d;
@@ -84,12 +94,15 @@ struct QuantArgs {
     uint8_t* qt;         // [cols][ldqt] or nullptr
     int64_t ldqt;
     uint8_t* st;
+    float* sums;         // mxfp8_quantize_bias: [row tiles][cols] sums of x's rows, or dbias itself
+    int32_t sums_add;    // add to them
     int32_t block;       // 32 or 128
     int32_t vec;         // x's rows are 16-byte aligned
     int32_t col_vec;     // there are column factors, 16-byte aligned
-    int32_t pad;
 };
 cudaError_t launch_quantize(const QuantArgs& a, int f32, cudaStream_t st);
+// dbias (+)= the sums over the row tiles, in order
+cudaError_t launch_bias_sums(const float* sums, int64_t tiles, int64_t cols, int accumulate, float* dbias, cudaStream_t st);
 
 struct RmsArgs {
     const void* x;       // [rows][ldx]
@@ -123,6 +136,39 @@ struct RmsGradArgs {
 // CTAs (= partial rows of dgamma) that launch_rmsnorm_grad uses, at most
 int rmsnorm_grad_parts(int64_t rows, int64_t d);
 cudaError_t launch_rmsnorm_grad(const RmsGradArgs& a, int f32, cudaStream_t st);
+
+// Heads: norm and rotation, and their gradient.
+constexpr int kHeadGroups = 4;
+struct HeadGroup {
+    const void* in;      // x, or dy
+    const void* x;       // gradient: x
+    void* out;           // y, or dx
+    int64_t in_row, in_head, x_row, x_head, out_row, out_head;  // elements
+    const float* gamma;  // nullptr: no norm
+    float* partials;     // gradient: [CTAs of the group][dim], or nullptr
+    float* dgamma;
+    int32_t heads, accumulate;
+    int32_t cta0;        // its first CTA (from here on set by the launchers)
+    int32_t tokens;      // rows per step of a CTA
+    int32_t parts;       // forward: CTAs that share a step's heads; gradient: CTAs
+};
+struct HeadArgs {
+    HeadGroup g[kHeadGroups];
+    int64_t rows;
+    int32_t n, dim;
+    float eps, scale;
+    const uint64_t* turns;
+    const int64_t* positions;
+    int32_t rot, pairs;  // rotated elements; adjacent pairs instead of halves
+    int32_t width;       // elements per vector: 8, 4, 2 or 1
+    int32_t lanes;       // of a head (set by the launchers)
+};
+// Elements per vector for which every head can be read and written in whole vectors.
+int head_width(const HeadArgs& a, int64_t es);
+cudaError_t launch_heads(HeadArgs a, int f32, cudaStream_t st);
+cudaError_t launch_heads_grad(HeadArgs a, int f32, cudaStream_t st);
+// CTAs (= partial rows of dgamma) of group g in launch_heads_grad
+int head_grad_parts(int64_t rows, int heads, int all_heads);
 
 // A launch takes its tensors by value: up to kClipTensors, or up to kClipFew in
 // the one-launch form for little data.

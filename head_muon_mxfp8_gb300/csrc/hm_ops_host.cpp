@@ -4,6 +4,8 @@
 #include "hm_internal.h"
 #include "hm_ops.h"
 
+#include <algorithm>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 
@@ -57,42 +59,112 @@ extern "C" hm_status mxfp8_tiled_scale_bytes(int64_t rows, int64_t k, size_t* by
     return HM_OK;
 }
 
-extern "C" hm_status mxfp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_scales, const uint8_t* b, int64_t ldb,
-                                const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, void* d, int64_t ldd,
-                                hm_dtype d_dtype, int accumulate, void* stream) {
+namespace {
+
+// The matrices of D's shape that an epilogue reads and writes, in this order: in, in2, out2.
+struct EpilogueUse {
+    const void* p;
+    int64_t ld;
+    bool takes, needs;  // of the form
+};
+void epilogue_use(const hm_epilogue& e, EpilogueUse (&u)[3]) {
+    const bool gated = e.form == HM_EPI_GATED_GRADIENT;
+    u[0] = {e.in, e.ld_in, true, e.form != HM_EPI_FORWARD};
+    u[1] = {e.in2, e.ld_in2, gated, gated};
+    u[2] = {e.out2, e.ld_out2, e.form != HM_EPI_GRADIENT, gated};
+}
+
+// The checks of both products, the epilogue's too where there is one; *go: something to launch.
+hm_status gemm_args(const uint8_t* a, int64_t lda, const uint8_t* a_scales, const uint8_t* b, int64_t ldb,
+                    const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, void* d, int64_t ldd, hm_dtype d_dtype,
+                    int accumulate, const hm_epilogue* e, hm::MxGemmArgs* p, bool* go) {
+    *go = false;
     int64_t es = 0;
     if (m < 0 || n < 0 || k < 0) return HM_ERR_ARG;
     if (!elem_size(d_dtype, &es) || (accumulate && d_dtype != HM_F32)) return HM_ERR_DTYPE;
+    EpilogueUse use[3] = {};
+    if (e) {
+        if (e->form < HM_EPI_FORWARD || e->form > HM_EPI_GATED_GRADIENT || e->activation < HM_ACT_NONE ||
+            e->activation > HM_ACT_SILU)
+            return HM_ERR_ARG;
+        epilogue_use(*e, use);
+        if (e->bias && e->form > HM_EPI_GATED) return HM_ERR_ARG;
+        for (const EpilogueUse& u : use)
+            if (u.p && !u.takes) return HM_ERR_ARG;
+    }
     if (m > kMaxDim || n > kMaxDim || k > kMaxDim || lda > kMaxDim || ldb > kMaxDim || ldd > kMaxPitch ||
         too_far(m, lda, 1) || too_far(n, ldb, 1) || too_far(m, ldd, es))
         return HM_ERR_GEOMETRY;
+    for (const EpilogueUse& u : use)
+        if (u.p && (u.ld > kMaxPitch || too_far(m, u.ld, es))) return HM_ERR_GEOMETRY;
     if (m == 0 || n == 0) return HM_OK;
     if (!d || ldd < n || (k && (!a || !a_scales || !b || !b_scales || lda < k || ldb < k))) return HM_ERR_ARG;
+    for (const EpilogueUse& u : use)
+        if (u.p ? u.ld < n : u.needs) return HM_ERR_ARG;
     if (k % HM_MX_BLOCK || !aligned(d, es)) return HM_ERR_ALIGN;
     if (k && (lda % 16 || ldb % 16 || !aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 16) ||
               !aligned(b_scales, 16)))
         return HM_ERR_ALIGN;
-    if (k) {
-        const Span out = span(d, m, ldd, n, es);
-        if (overlap(out, span(a, m, lda, k, 1)) || overlap(out, span(b, n, ldb, k, 1)) ||
-            overlap(out, span(a_scales, 1, 0, tiled_bytes(m, k), 1)) ||
-            overlap(out, span(b_scales, 1, 0, tiled_bytes(n, k), 1)))
+    if (e && !aligned(e->bias, 4)) return HM_ERR_ALIGN;
+    for (const EpilogueUse& u : use)
+        if (!aligned(u.p, es)) return HM_ERR_ALIGN;
+    const Span outs[2] = {span(d, m, ldd, n, es), span(use[2].p, m, use[2].ld, n, es)};
+    for (int i = 0; i < 2; ++i) {
+        const Span& out = outs[i];
+        if (k && (overlap(out, span(a, m, lda, k, 1)) || overlap(out, span(b, n, ldb, k, 1)) ||
+                  overlap(out, span(a_scales, 1, 0, tiled_bytes(m, k), 1)) ||
+                  overlap(out, span(b_scales, 1, 0, tiled_bytes(n, k), 1))))
             return HM_ERR_OVERLAP;
+        if (e && overlap(out, span(e->bias, 1, 0, n, 4))) return HM_ERR_OVERLAP;
+        // an output may be an input of its shape exactly: a thread reads an element before it writes it
+        const void* q = i ? use[2].p : d;
+        const int64_t ldq = i ? use[2].ld : ldd;
+        for (int j = 0; j < 2; ++j)
+            if (!(q == use[j].p && ldq == use[j].ld) && overlap(out, span(use[j].p, m, use[j].ld, n, es)))
+                return HM_ERR_OVERLAP;
     }
+    if (overlap(outs[0], outs[1])) return HM_ERR_OVERLAP;
     if (up(m, 128) / 128 * (up(n, 128) / 128) > INT32_MAX) return HM_ERR_GEOMETRY;
     const hm_status st = hm::check_arch();
     if (st != HM_OK) return st;
+    std::memset(p, 0, sizeof(*p));
+    p->sa = a_scales;
+    p->sb = b_scales;
+    p->d = d;
+    p->ldd = ldd;
+    p->m = static_cast<int32_t>(m);
+    p->n = static_cast<int32_t>(n);
+    p->k = static_cast<int32_t>(k);
+    p->d_f32 = d_dtype == HM_F32;
+    p->accumulate = accumulate != 0;
+    if (e) {
+        p->epilogue = 1;
+        p->e = {e->form, e->activation, e->bias, e->in, e->in2, e->out2, e->ld_in, e->ld_in2, e->ld_out2};
+    }
+    *go = true;
+    return HM_OK;
+}
+
+}  // namespace
+
+extern "C" hm_status mxfp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_scales, const uint8_t* b, int64_t ldb,
+                                const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, void* d, int64_t ldd,
+                                hm_dtype d_dtype, int accumulate, void* stream) {
     hm::MxGemmArgs p;
-    std::memset(&p, 0, sizeof(p));
-    p.sa = a_scales;
-    p.sb = b_scales;
-    p.d = d;
-    p.ldd = ldd;
-    p.m = static_cast<int32_t>(m);
-    p.n = static_cast<int32_t>(n);
-    p.k = static_cast<int32_t>(k);
-    p.d_f32 = d_dtype == HM_F32;
-    p.accumulate = accumulate != 0;
+    bool go;
+    const hm_status st = gemm_args(a, lda, a_scales, b, ldb, b_scales, m, n, k, d, ldd, d_dtype, accumulate, nullptr, &p, &go);
+    if (st != HM_OK || !go) return st;
+    return cuda_status(hm::launch_mx_gemm(a, lda, b, ldb, p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" hm_status mxfp8_gemm_epilogue(const uint8_t* a, int64_t lda, const uint8_t* a_scales, const uint8_t* b,
+                                         int64_t ldb, const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, void* d,
+                                         int64_t ldd, hm_dtype d_dtype, const hm_epilogue* epilogue, void* stream) {
+    if (!epilogue) return HM_ERR_ARG;
+    hm::MxGemmArgs p;
+    bool go;
+    const hm_status st = gemm_args(a, lda, a_scales, b, ldb, b_scales, m, n, k, d, ldd, d_dtype, 0, epilogue, &p, &go);
+    if (st != HM_OK || !go) return st;
     return cuda_status(hm::launch_mx_gemm(a, lda, b, ldb, p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -117,9 +189,13 @@ extern "C" hm_status mxfp8_gemm_form(int64_t m, int64_t n, int64_t k, hm_dtype d
     return ok;
 }
 
-extern "C" hm_status mxfp8_quantize(const void* x, hm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx,
-                                    const float* row_mul, const float* col_mul, int block, uint8_t* q, int64_t ldq,
-                                    uint8_t* s, uint8_t* qt, int64_t ldqt, uint8_t* st, void* stream) {
+namespace {
+
+// The checks of both quantizations; *go: something to launch.
+hm_status quantize_args(const void* x, hm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx, const float* row_mul,
+                        const float* col_mul, int block, uint8_t* q, int64_t ldq, uint8_t* s, uint8_t* qt, int64_t ldqt,
+                        uint8_t* st, const Span (&more)[2], hm::QuantArgs* a, bool* go) {
+    *go = false;
     int64_t es = 0;
     if (rows < 0 || cols < 0 || (block != 32 && block != 128)) return HM_ERR_ARG;
     if (!elem_size(x_dtype, &es)) return HM_ERR_DTYPE;
@@ -143,27 +219,81 @@ extern "C" hm_status mxfp8_quantize(const void* x, hm_dtype x_dtype, int64_t row
     for (int i = 3; i < 7; ++i)
         for (int j = 0; j < i; ++j)
             if (overlap(all[i], all[j])) return HM_ERR_OVERLAP;
+    for (const Span& m : more)
+        for (const Span& x1 : all)
+            if (overlap(m, x1)) return HM_ERR_OVERLAP;
     const hm_status ok = hm::check_arch();
     if (ok != HM_OK) return ok;
+    std::memset(a, 0, sizeof(*a));
+    a->x = x;
+    a->rows = rows;
+    a->cols = cols;
+    a->ldx = ldx;
+    a->row_mul = row_mul;
+    a->col_mul = col_mul;
+    a->q = q;
+    a->ldq = ldq;
+    a->s = s;
+    a->qt = qt;
+    a->ldqt = ldqt;
+    a->st = st;
+    a->block = block;
+    a->vec = aligned(x, 16) && ldx * es % 16 == 0;
+    a->col_vec = col_mul && aligned(col_mul, 16);
+    *go = true;
+    return HM_OK;
+}
+
+}  // namespace
+
+extern "C" hm_status mxfp8_quantize(const void* x, hm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                    const float* row_mul, const float* col_mul, int block, uint8_t* q, int64_t ldq,
+                                    uint8_t* s, uint8_t* qt, int64_t ldqt, uint8_t* st, void* stream) {
     hm::QuantArgs a;
-    std::memset(&a, 0, sizeof(a));
-    a.x = x;
-    a.rows = rows;
-    a.cols = cols;
-    a.ldx = ldx;
-    a.row_mul = row_mul;
-    a.col_mul = col_mul;
-    a.q = q;
-    a.ldq = ldq;
-    a.s = s;
-    a.qt = qt;
-    a.ldqt = ldqt;
-    a.st = st;
-    a.block = block;
-    a.vec = aligned(x, 16) && ldx * es % 16 == 0;
-    a.col_vec = col_mul && aligned(col_mul, 16);
+    bool go;
+    const Span none[2] = {};
+    const hm_status ok = quantize_args(x, x_dtype, rows, cols, ldx, row_mul, col_mul, block, q, ldq, s, qt, ldqt, st, none, &a, &go);
+    if (ok != HM_OK || !go) return ok;
     return cuda_status(hm::launch_quantize(a, x_dtype == HM_F32, static_cast<cudaStream_t>(stream)));
 }
+
+extern "C" hm_status mxfp8_quantize_bias_workspace(int64_t rows, int64_t cols, size_t* bytes) {
+    if (!bytes || rows < 0 || cols < 0) return HM_ERR_ARG;
+    if (rows > (int64_t(1) << 22) || cols > (int64_t(1) << 30)) return HM_ERR_GEOMETRY;
+    *bytes = rows > 128 ? static_cast<size_t>(up(rows, 128) / 128) * static_cast<size_t>(cols) * 4 : 0;
+    return HM_OK;
+}
+
+extern "C" hm_status mxfp8_quantize_bias(const void* x, hm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx, int block,
+                                         uint8_t* q, int64_t ldq, uint8_t* s, uint8_t* qt, int64_t ldqt, uint8_t* st,
+                                         float* dbias, int accumulate, void* workspace, size_t workspace_bytes,
+                                         void* stream) {
+    if (rows < 0 || cols < 0) return HM_ERR_ARG;
+    if (rows > (int64_t(1) << 22) || cols > (int64_t(1) << 30)) return HM_ERR_GEOMETRY;
+    if (cols && !dbias) return HM_ERR_ARG;
+    if (!aligned(dbias, 4) || !aligned(workspace, 16)) return HM_ERR_ALIGN;
+    size_t need = 0;
+    mxfp8_quantize_bias_workspace(rows, cols, &need);
+    const Span sums[2] = {span(dbias, 1, 0, cols, 4), span(workspace, 1, 0, static_cast<int64_t>(need), 1)};
+    if (overlap(sums[0], sums[1])) return HM_ERR_OVERLAP;
+    if (rows && need && (!workspace || workspace_bytes < need)) return HM_ERR_WORKSPACE;
+    hm::QuantArgs a;
+    bool go;
+    hm_status ok = quantize_args(x, x_dtype, rows, cols, ldx, nullptr, nullptr, block, q, ldq, s, qt, ldqt, st, sums, &a, &go);
+    if (ok != HM_OK) return ok;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (!go) {  // no rows: the empty sum
+        if (!cols || accumulate) return HM_OK;
+        if ((ok = hm::check_arch()) != HM_OK) return ok;
+        return cuda_status(hm::launch_bias_sums(nullptr, 0, cols, 0, dbias, cs));
+    }
+    a.sums = need ? static_cast<float*>(workspace) : dbias;
+    a.sums_add = !need && accumulate;
+    ok = cuda_status(hm::launch_quantize(a, x_dtype == HM_F32, cs));
+    if (ok != HM_OK || !need) return ok;
+    return cuda_status(hm::launch_bias_sums(a.sums, up(rows, 128) / 128, cols, accumulate != 0, dbias, cs));
+}
+
 
 extern "C" hm_status rmsnorm_mxfp8(const void* x, int64_t ldx, const void* res, void* h, int64_t ldh, hm_dtype dtype,
                                    int64_t rows, int64_t d, const float* gamma, float eps, int block, float* rstd,
@@ -271,6 +401,291 @@ extern "C" hm_status rmsnorm_backward(const void* dy, int64_t lddy, const void* 
     a.dgamma = dgamma;
     a.partials = static_cast<float*>(workspace);
     return cuda_status(hm::launch_rmsnorm_grad(a, dtype == HM_F32, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// [rows][heads] of head_dim elements, in bytes: the outer of the two strides, how far
+// the rest reaches from one outer step, and the whole span.
+struct Block3 {
+    Span all;
+    int64_t pitch, width;  // pitch 0: one outer step
+};
+Block3 block3(const void* p, int64_t rows, int64_t row, int64_t heads, int64_t head, int64_t dim, int64_t es) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const bool row_outer = heads == 1 || (rows > 1 && row >= head);
+    const int64_t n_out = row_outer ? rows : heads, out = row_outer ? row : head;
+    const int64_t n_in = row_outer ? heads : rows, in = row_outer ? head : row;
+    Block3 b;
+    b.width = ((n_in - 1) * in + dim) * es;
+    b.pitch = n_out > 1 ? out * es : 0;
+    b.all = {a, p ? a + static_cast<uintptr_t>((n_out - 1) * out * es + b.width) : a};
+    return b;
+}
+// Blocks with one pitch may interleave (queries and keys of a packed projection);
+// otherwise the spans decide.
+bool overlap(const Block3& x, const Block3& y) {
+    if (!overlap(x.all, y.all)) return false;
+    const int64_t pitch = x.pitch ? x.pitch : y.pitch;
+    if (!pitch || (x.pitch && y.pitch && x.pitch != y.pitch) || x.width > pitch || y.width > pitch) return true;
+    const int64_t d = static_cast<int64_t>((y.all.lo - x.all.lo) % static_cast<uintptr_t>(pitch));
+    const int64_t at = y.all.lo >= x.all.lo ? d : (pitch - static_cast<int64_t>((x.all.lo - y.all.lo) % static_cast<uintptr_t>(pitch))) % pitch;
+    return at < x.width || at + y.width > pitch;
+}
+
+// One strided array of a group: its pointer and strides.
+struct HeadMatrix {
+    const void* p;
+    int64_t row, head;
+};
+constexpr int64_t kMaxHeads = 65536;
+
+// No address twice: heads inside a row, or rows inside a head.
+bool apart(const HeadMatrix& m, int64_t rows, int64_t heads, int64_t dim) {
+    if (rows > 1 && heads > 1)
+        return (m.head >= dim && m.row >= (heads - 1) * m.head + dim) || (m.row >= dim && m.head >= (rows - 1) * m.row + dim);
+    return (rows == 1 || m.row >= dim) && (heads == 1 || m.head >= dim);
+}
+bool same(const HeadMatrix& x, const HeadMatrix& y) { return x.p == y.p && x.row == y.row && x.head == y.head; }
+
+hm_status head_matrix(const HeadMatrix& m, int64_t rows, int64_t heads, int64_t dim, int64_t es, bool output) {
+    if (!m.p || m.row < 0 || m.head < 0) return HM_ERR_ARG;
+    if (m.row > kMaxPitch || m.head > kMaxPitch || too_far(rows, m.row, es) || too_far(heads, m.head, es)) return HM_ERR_GEOMETRY;
+    if (!aligned(m.p, es)) return HM_ERR_ALIGN;
+    return output && !apart(m, rows, heads, dim) ? HM_ERR_ARG : HM_OK;
+}
+
+// What both calls check of their common arguments, and a's part of them.
+hm_status head_common(int n_groups, hm_dtype dtype, int64_t rows, int64_t head_dim, float eps, const hm_rotation* rot,
+                      int64_t* es, hm::HeadArgs* a) {
+    if (n_groups < 0 || rows < 0 || head_dim < 0 || !(eps >= 0.f)) return HM_ERR_ARG;
+    if (!elem_size(dtype, es)) return HM_ERR_DTYPE;
+    if (n_groups > HM_HEAD_GROUPS || rows > kMaxDim || head_dim > HM_HEAD_MAX_DIM || head_dim % 2) return HM_ERR_GEOMETRY;
+    std::memset(a, 0, sizeof(*a));
+    a->rows = rows;
+    a->n = n_groups;
+    a->dim = static_cast<int32_t>(head_dim);
+    a->eps = eps;
+    if (rot && rot->rot_dim) {
+        if (rot->rot_dim < 0 || (rot->layout != HM_ROPE_HALF && rot->layout != HM_ROPE_PAIRS) || !std::isfinite(rot->scale))
+            return HM_ERR_ARG;
+        if (rot->rot_dim > head_dim || rot->rot_dim % 2) return HM_ERR_GEOMETRY;
+        if (rows && (!rot->turns || !rot->positions)) return HM_ERR_ARG;
+        if (!aligned(rot->turns, 8) || !aligned(rot->positions, 8)) return HM_ERR_ALIGN;
+        a->turns = rot->turns;
+        a->positions = rot->positions;
+        a->rot = rot->rot_dim;
+        a->pairs = rot->layout == HM_ROPE_PAIRS;
+        a->scale = rot->scale;
+    }
+    return HM_OK;
+}
+
+// What a call reads besides its matrices.
+void head_small(const hm::HeadArgs& a, Span (&s)[2]) {
+    s[0] = span(a.turns, 1, 0, a.rot / 2, 8);
+    s[1] = span(a.positions, 1, 0, a.rows, 8);
+}
+
+}  // namespace
+
+extern "C" hm_status head_norm_rope(const hm_head_group* groups, int n_groups, hm_dtype dtype, int64_t rows,
+                                    int64_t head_dim, float eps, const hm_rotation* rotation, void* stream) {
+    int64_t es = 0;
+    hm::HeadArgs a;
+    hm_status ok = head_common(n_groups, dtype, rows, head_dim, eps, rotation, &es, &a);
+    if (ok != HM_OK) return ok;
+    if (n_groups && !groups) return HM_ERR_ARG;
+    Span small[2];
+    head_small(a, small);
+    Block3 x[HM_HEAD_GROUPS], y[HM_HEAD_GROUPS];
+    a.n = 0;
+    for (int i = 0; i < n_groups; ++i) {
+        const hm_head_group& g = groups[i];
+        if (g.heads < 0) return HM_ERR_ARG;
+        if (g.heads > kMaxHeads) return HM_ERR_GEOMETRY;
+        if (!aligned(g.gamma, 4)) return HM_ERR_ALIGN;
+        if (!g.heads || !rows || !head_dim) continue;
+        const HeadMatrix in = {g.x, g.x_row, g.x_head}, out = {g.y, g.y_row, g.y_head};
+        if ((ok = head_matrix(in, rows, g.heads, head_dim, es, false)) != HM_OK) return ok;
+        if ((ok = head_matrix(out, rows, g.heads, head_dim, es, true)) != HM_OK) return ok;
+        x[a.n] = block3(g.x, rows, g.x_row, g.heads, g.x_head, head_dim, es);
+        y[a.n] = block3(g.y, rows, g.y_row, g.heads, g.y_head, head_dim, es);
+        hm::HeadGroup& to = a.g[a.n++];
+        to.in = g.x;
+        to.in_row = g.x_row;
+        to.in_head = g.x_head;
+        to.out = g.y;
+        to.out_row = g.y_row;
+        to.out_head = g.y_head;
+        to.gamma = g.gamma;
+        to.heads = g.heads;
+    }
+    for (int i = 0; i < a.n; ++i) {
+        for (int j = 0; j < a.n; ++j) {
+            const bool in_place = i == j && same({a.g[i].in, a.g[i].in_row, a.g[i].in_head}, {a.g[i].out, a.g[i].out_row, a.g[i].out_head});
+            if ((!in_place && overlap(y[i], x[j])) || (j < i && overlap(y[i], y[j])) ||
+                overlap(y[i].all, span(a.g[j].gamma, 1, 0, head_dim, 4)))
+                return HM_ERR_OVERLAP;
+        }
+        if (overlap(y[i].all, small[0]) || overlap(y[i].all, small[1])) return HM_ERR_OVERLAP;
+    }
+    if (!a.n) return HM_OK;
+    if ((ok = hm::check_arch()) != HM_OK) return ok;
+    a.width = hm::head_width(a, es);
+    return cuda_status(hm::launch_heads(a, dtype == HM_F32, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+int64_t all_heads(const hm_head_grad* groups, int n) {
+    int64_t all = 0;
+    for (int i = 0; i < n; ++i) all += groups[i].heads;
+    return all;
+}
+// Floats of dgamma's partial sums of group i.
+size_t grad_partials(const hm_head_grad* groups, int n, int i, int64_t rows, int64_t head_dim) {
+    const hm_head_grad& g = groups[i];
+    if (!g.dgamma || !g.heads || !rows) return 0;
+    return static_cast<size_t>(hm::head_grad_parts(rows, g.heads, static_cast<int>(all_heads(groups, n)))) * static_cast<size_t>(head_dim);
+}
+
+}  // namespace
+
+extern "C" hm_status head_norm_rope_backward_workspace(const hm_head_grad* groups, int n_groups, int64_t rows,
+                                                       int64_t head_dim, size_t* bytes) {
+    if (!bytes || n_groups < 0 || rows < 0 || head_dim < 0 || (n_groups && !groups)) return HM_ERR_ARG;
+    if (n_groups > HM_HEAD_GROUPS || rows > kMaxDim || head_dim > HM_HEAD_MAX_DIM || head_dim % 2) return HM_ERR_GEOMETRY;
+    for (int i = 0; i < n_groups; ++i) {
+        if (groups[i].heads < 0) return HM_ERR_ARG;
+        if (groups[i].heads > kMaxHeads) return HM_ERR_GEOMETRY;
+    }
+    size_t floats = 0;
+    for (int i = 0; i < n_groups; ++i) floats += grad_partials(groups, n_groups, i, rows, head_dim);
+    *bytes = floats * 4;
+    return HM_OK;
+}
+
+extern "C" hm_status head_norm_rope_backward(const hm_head_grad* groups, int n_groups, hm_dtype dtype, int64_t rows,
+                                             int64_t head_dim, float eps, const hm_rotation* rotation, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+    int64_t es = 0;
+    hm::HeadArgs a;
+    hm_status ok = head_common(n_groups, dtype, rows, head_dim, eps, rotation, &es, &a);
+    if (ok != HM_OK) return ok;
+    if (n_groups && !groups) return HM_ERR_ARG;
+    if (!aligned(workspace, 16)) return HM_ERR_ALIGN;
+    Span small[3];
+    Span rot[2];
+    head_small(a, rot);
+    small[0] = rot[0];
+    small[1] = rot[1];
+    small[2] = span(workspace, 1, 0, static_cast<int64_t>(workspace_bytes), 1);
+    Block3 dy[HM_HEAD_GROUPS], x[HM_HEAD_GROUPS], dx[HM_HEAD_GROUPS];
+    Span dg[HM_HEAD_GROUPS];
+    int from[HM_HEAD_GROUPS];
+    a.n = 0;
+    for (int i = 0; i < n_groups; ++i) {
+        const hm_head_grad& g = groups[i];
+        if (g.heads < 0 || (g.dgamma && !g.gamma)) return HM_ERR_ARG;
+        if (g.heads > kMaxHeads) return HM_ERR_GEOMETRY;
+        if (!aligned(g.gamma, 4) || !aligned(g.dgamma, 4)) return HM_ERR_ALIGN;
+        if (!head_dim) continue;
+        const bool live = g.heads && rows;
+        if (!live && !g.dgamma) continue;
+        const int k = a.n++;
+        from[k] = i;
+        hm::HeadGroup& to = a.g[k];
+        dg[k] = span(g.dgamma, 1, 0, head_dim, 4);
+        to.gamma = g.gamma;
+        to.dgamma = g.dgamma;
+        to.accumulate = g.accumulate != 0;
+        dy[k] = x[k] = dx[k] = Block3{{0, 0}, 0, 0};
+        if (!live) continue;
+        const HeadMatrix in = {g.dy, g.dy_row, g.dy_head}, xx = {g.x, g.x_row, g.x_head}, out = {g.dx, g.dx_row, g.dx_head};
+        if ((ok = head_matrix(in, rows, g.heads, head_dim, es, false)) != HM_OK) return ok;
+        if (g.gamma && (ok = head_matrix(xx, rows, g.heads, head_dim, es, false)) != HM_OK) return ok;
+        if ((ok = head_matrix(out, rows, g.heads, head_dim, es, true)) != HM_OK) return ok;
+        dy[k] = block3(g.dy, rows, g.dy_row, g.heads, g.dy_head, head_dim, es);
+        if (g.gamma) x[k] = block3(g.x, rows, g.x_row, g.heads, g.x_head, head_dim, es);
+        dx[k] = block3(g.dx, rows, g.dx_row, g.heads, g.dx_head, head_dim, es);
+        to.in = g.dy;
+        to.in_row = g.dy_row;
+        to.in_head = g.dy_head;
+        if (g.gamma) {
+            to.x = g.x;
+            to.x_row = g.x_row;
+            to.x_head = g.x_head;
+        }
+        to.out = g.dx;
+        to.out_row = g.dx_row;
+        to.out_head = g.dx_head;
+        to.heads = g.heads;
+    }
+    for (int i = 0; i < a.n; ++i) {
+        const HeadMatrix out = {a.g[i].out, a.g[i].out_row, a.g[i].out_head};
+        for (int j = 0; j < a.n; ++j) {
+            const Span gamma = span(a.g[j].gamma, 1, 0, head_dim, 4);
+            const bool is_dy = i == j && same(out, {a.g[i].in, a.g[i].in_row, a.g[i].in_head});
+            const bool is_x = i == j && same(out, {a.g[i].x, a.g[i].x_row, a.g[i].x_head});
+            if ((!is_dy && overlap(dx[i], dy[j])) || (!is_x && overlap(dx[i], x[j])) || (j < i && overlap(dx[i], dx[j])) ||
+                overlap(dx[i].all, gamma) || overlap(dx[i].all, dg[j]) || overlap(dg[i], dy[j].all) || overlap(dg[i], x[j].all) ||
+                overlap(dg[i], gamma) || (j < i && overlap(dg[i], dg[j])))
+                return HM_ERR_OVERLAP;
+        }
+        for (int j = 0; j < 3; ++j)
+            if (overlap(dx[i].all, small[j]) || overlap(dg[i], small[j])) return HM_ERR_OVERLAP;
+        if (overlap(small[2], dy[i].all) || overlap(small[2], x[i].all) || overlap(small[2], span(a.g[i].gamma, 1, 0, head_dim, 4)))
+            return HM_ERR_OVERLAP;
+    }
+    if (overlap(small[2], small[0]) || overlap(small[2], small[1])) return HM_ERR_OVERLAP;
+    if (!a.n) return HM_OK;
+    if ((ok = hm::check_arch()) != HM_OK) return ok;
+    size_t floats = 0;
+    for (int k = 0; k < a.n; ++k) {
+        const size_t part = grad_partials(groups, n_groups, from[k], rows, head_dim);
+        if (part) a.g[k].partials = static_cast<float*>(workspace) + floats;
+        floats += part;
+    }
+    if (floats && (!workspace || workspace_bytes < floats * 4)) return HM_ERR_WORKSPACE;
+    a.width = hm::head_width(a, es);
+    return cuda_status(hm::launch_heads_grad(a, dtype == HM_F32, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" hm_status rope_turns(int32_t rot_dim, double theta, int32_t scaling, double factor, double trained,
+                                double beta_fast, double beta_slow, uint64_t* turns, float* scale) {
+    const double turn = 6.283185307179586476925;  // radians
+    if (!turns || !scale || !(theta > 1.0) || !std::isfinite(theta) || scaling < HM_ROPE_UNSCALED || scaling > HM_ROPE_YARN)
+        return HM_ERR_ARG;
+    if (rot_dim < 2 || rot_dim > HM_HEAD_MAX_DIM || rot_dim % 2) return HM_ERR_GEOMETRY;
+    if (scaling == HM_ROPE_UNSCALED) factor = 1.0;
+    if (!(factor >= 1.0) || !std::isfinite(factor)) return HM_ERR_ARG;
+    double low = 0.0, high = 0.0;
+    if (scaling == HM_ROPE_BASE) {
+        if (rot_dim == 2) return HM_ERR_GEOMETRY;
+        theta *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+        if (!std::isfinite(theta)) return HM_ERR_ARG;
+    }
+    if (scaling == HM_ROPE_YARN) {
+        if (!(trained >= 1.0) || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !std::isfinite(trained) || !std::isfinite(beta_fast))
+            return HM_ERR_ARG;
+        // the pair that turns `beta` times over the trained positions
+        const auto pair_of = [&](double beta) { return rot_dim * std::log(trained / (beta * turn)) / (2.0 * std::log(theta)); };
+        low = std::max(0.0, std::floor(pair_of(beta_fast)));
+        high = std::min(rot_dim - 1.0, std::ceil(pair_of(beta_slow)));
+        if (!(high > low)) high = low + 0.001;  // no ramp left: a step
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(theta, -2.0 * i / rot_dim);
+        if (scaling == HM_ROPE_LINEAR) f /= factor;
+        if (scaling == HM_ROPE_YARN) {
+            const double ramp = std::min(1.0, std::max(0.0, (i - low) / (high - low)));
+            f = f * (1.0 - ramp) + f / factor * ramp;
+        }
+        turns[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(f / turn, 64)));  // f <= 1: below 2^62
+    }
+    *scale = scaling == HM_ROPE_YARN ? static_cast<float>(1.0 + 0.1 * std::log(factor)) : 1.f;
+    return HM_OK;
 }
 
 namespace {

@@ -123,6 +123,39 @@ __device__ __forceinline__ int row_scale(float amax, int block) {
     return mx_scale_byte(amax);
 }
 
+// The sums of the tile's columns over each of its four 32-row blocks.
+template <bool PACKED>
+__device__ __forceinline__ void sum_columns(const uint32_t* tile, float (*sum_col)[kQTile]) {
+    if constexpr (PACKED) {
+        const int cp = threadIdx.x & 63, b = threadIdx.x >> 6;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const uint32_t w = tile[(b * 32 + k) * (kQTile / 2) + cp];
+            s0 += lo_f32(w), s1 += hi_f32(w);
+        }
+        sum_col[b][2 * cp] = s0;
+        sum_col[b][2 * cp + 1] = s1;
+    } else {
+        const int c = threadIdx.x & 127;
+        const float* col = reinterpret_cast<const float*>(tile) + 4 * swizzled(c >> 2) + (c & 3);
+        for (int b = threadIdx.x >> 7; b < 4; b += kQThreads / 128) {
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s += col[(b * 32 + k) * kQTile];
+            sum_col[b][c] = s;
+        }
+    }
+}
+// Those, added: a row of the workspace, or dbias itself where this is the only row tile.
+__device__ __forceinline__ void store_sums(const QuantArgs& p, const float (*sum_col)[kQTile], int64_t c0, int64_t rt) {
+    const int c = threadIdx.x;
+    if (c >= kQTile || c0 + c >= p.cols) return;
+    float* to = p.sums + rt * p.cols + c0 + c;
+    const float s = (sum_col[0][c] + sum_col[1][c]) + (sum_col[2][c] + sum_col[3][c]);
+    *to = p.sums_add ? *to + s : s;
+}
+
 // Row phase: 8 lanes hold a row of the tile, 16 columns each (two lanes per
 // block of 32), a warp 16 rows in four steps whose loads are all issued before
 // the first is used.  16 columns per lane rather than 8: the work per block
@@ -133,12 +166,16 @@ __device__ __forceinline__ int row_scale(float amax, int block) {
 //     half the shared memory and half its traffic, and magnitudes are compared
 //     two at a time; a thread's column work is a pair of columns x 32 rows.
 //   else: y in fp32 (swizzled); a thread's column work is one column x 32 rows.
-template <bool F32, bool PACKED, bool COL>
+// SUM: the sums of the tile's columns too, from the tile in shared memory: a thread's
+// column work is summed row by row, then the 32-row blocks in order.
+template <bool F32, bool PACKED, bool COL, bool SUM>
 __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(const __grid_constant__ QuantArgs p) {
+    constexpr bool TILE = COL || SUM;
     extern __shared__ __align__(16) uint32_t tile[];  // [128][64] bf16 pairs or [128][128] fp32
     __shared__ __align__(16) uint8_t s_row[512];
     __shared__ __align__(16) uint8_t s_col[512];
     __shared__ float amax_col[4][kQTile];
+    __shared__ float sum_col[SUM ? 4 : 1][kQTile];
     wait_for_earlier_kernels();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t ct = blockIdx.x, rt = blockIdx.y;
@@ -163,7 +200,7 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int rl = rl0 + 4 * i;
-            if (COL) {
+            if (TILE) {
                 uint4* t4 = reinterpret_cast<uint4*>(tile + rl * (kQTile / 2) + c16 / 2);
                 t4[flip] = flip ? raw[i].w[1] : raw[i].w[0];
                 t4[flip ^ 1] = flip ? raw[i].w[0] : raw[i].w[1];
@@ -222,7 +259,7 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
 #pragma unroll
                         for (int k = 0; k < 16; ++k) v[k] = k < left ? v[k] : 0.f;
                 }
-                if (COL) {
+                if (TILE) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         *reinterpret_cast<float4*>(tile + rl * kQTile + 4 * swizzled(c16 / 4 + k)) =
@@ -251,6 +288,11 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
         const int64_t col_tiles = (cols32 + 127) / 128;
         reinterpret_cast<uint4*>(p.s + (rt * col_tiles + ct) * 512)[threadIdx.x] = reinterpret_cast<const uint4*>(s_row)[threadIdx.x];
     }
+    if constexpr (SUM && !COL) {
+        sum_columns<PACKED>(tile, sum_col);
+        __syncthreads();
+        store_sums(p, sum_col, c0, rt);
+    }
     if constexpr (COL) {
         if constexpr (PACKED) {
             const int cp = threadIdx.x & 63, b = threadIdx.x >> 6;
@@ -259,6 +301,13 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
             uint32_t m = 0u;
 #pragma unroll
             for (int k = 0; k < 32; ++k) w[k] = tile[(b * 32 + k) * (kQTile / 2) + cp];
+            if constexpr (SUM) {
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) s0 += lo_f32(w[k]), s1 += hi_f32(w[k]);
+                sum_col[b][c] = s0;
+                sum_col[b][c + 1] = s1;
+            }
 #pragma unroll
             for (int k = 0; k < 32; ++k) m = max_abs2(m, w[k]);
             float a0 = fabsf(lo_f32(m)), a1 = fabsf(hi_f32(m));
@@ -312,6 +361,12 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
 #pragma unroll
                     for (int k = 0; k < 32; ++k) amax = fmaxf(amax, fabsf(w[k]));
                 }
+                if constexpr (SUM) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) sum += w[k];
+                    sum_col[b0 + j][c] = sum;
+                }
                 const int byte = mx_scale_byte(amax);
                 const float sc = mx_inv_of_byte(byte);
                 s_col[(c & 31) * 16 + (c >> 5) * 4 + b0 + j] =
@@ -324,6 +379,7 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
             for (int j = 0; j < kBlocks; ++j) stage_codes32(reinterpret_cast<uint4*>(tile), c, b0 + j, x[j]);
         }
         __syncthreads();
+        if constexpr (SUM) store_sums(p, sum_col, c0, rt);
 #pragma unroll
         for (int k = 0; k < kQTile; k += kQThreads / 8) {
             const int c = k + (threadIdx.x >> 3), piece = threadIdx.x & 7;
@@ -338,22 +394,53 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
     }
 }
 
-template <bool F32, bool PACKED, bool COL>
+// dbias from the row tiles' sums: 32 columns per CTA, 32 threads per column each adding
+// every 32nd tile in order, then the 32 in order.
+__global__ void __launch_bounds__(1024) bias_sums_kernel(const float* sums, int tiles, int64_t cols, int accumulate, float* dbias) {
+    __shared__ float red[32][33];
+    wait_for_earlier_kernels();
+    const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + c;
+    float s = 0.f;
+    if (col < cols)
+#pragma unroll 4
+        for (int k = g; k < tiles; k += 32) s += sums[k * cols + col];
+    red[g][c] = s;
+    __syncthreads();
+    if (g == 0 && col < cols) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) t += red[k][c];
+        dbias[col] = accumulate ? dbias[col] + t : t;
+    }
+}
+
+template <bool F32, bool PACKED, bool COL, bool SUM = false>
 cudaError_t launch(const QuantArgs& a, cudaStream_t st) {
-    constexpr int smem = !COL ? 0 : kQTile * kQTile * (PACKED ? 2 : 4);
+    constexpr int smem = !(COL || SUM) ? 0 : kQTile * kQTile * (PACKED ? 2 : 4);
     if (smem) {
         static PerDevice done;
-        const cudaError_t e = allow_smem(quantize_kernel<F32, PACKED, COL>, smem, done);
+        const cudaError_t e = allow_smem(quantize_kernel<F32, PACKED, COL, SUM>, smem, done);
         if (e != cudaSuccess) return e;
     }
     const dim3 grid(static_cast<unsigned>((a.cols + 127) / 128), static_cast<unsigned>((a.rows + 127) / 128));
     note_launch();
-    return launch_early(quantize_kernel<F32, PACKED, COL>, grid, kQThreads, smem, st, a);
+    return launch_early(quantize_kernel<F32, PACKED, COL, SUM>, grid, kQThreads, smem, st, a);
 }
 
 }  // namespace
 
+cudaError_t launch_bias_sums(const float* sums, int64_t tiles, int64_t cols, int accumulate, float* dbias, cudaStream_t st) {
+    note_launch();
+    return launch_early(bias_sums_kernel, static_cast<unsigned>((cols + 31) / 32), 1024, 0, st, sums, static_cast<int>(tiles),
+                        cols, accumulate, dbias);
+}
+
 cudaError_t launch_quantize(const QuantArgs& a, int f32, cudaStream_t st) {
+    if (a.sums) {
+        if (f32) return a.qt ? launch<true, false, true, true>(a, st) : launch<true, false, false, true>(a, st);
+        return a.qt ? launch<false, true, true, true>(a, st) : launch<false, true, false, true>(a, st);
+    }
     if (f32) return a.qt ? launch<true, false, true>(a, st) : launch<true, false, false>(a, st);
     if (a.row_mul || a.col_mul) return a.qt ? launch<false, false, true>(a, st) : launch<false, false, false>(a, st);
     return a.qt ? launch<false, true, true>(a, st) : launch<false, true, false>(a, st);

@@ -447,6 +447,50 @@ hm_status mxfp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_scales, con
 hm_status mxfp8_gemm_form(int64_t m, int64_t n, int64_t k, hm_dtype d_dtype, int32_t* tile, int32_t* parts,
                           int32_t* sums);
 
+/* The same product with what a layer does next in its epilogue.  With
+ * z = sum_k A[m][k] B[n][k] (scales applied) and f the activation, per element:
+ *   HM_EPI_FORWARD         z += bias[n];  out2 = z;  D = f(z) + in
+ *   HM_EPI_GATED           z += bias[n];  out2 = z;  D = z * f(in)
+ *                          (in: the gate's product, before its activation)
+ *   HM_EPI_GRADIENT        D = z * f'(in)          (in: the forward pass's out2)
+ *   HM_EPI_GATED_GRADIENT  D = z * f(in),  out2 = z * in2 * f'(in)
+ *                          (in: the gate, in2: the forward pass's out2; D is in2's
+ *                          gradient, out2 the gate's)
+ * all in fp32 with one rounding of each output to d_dtype.  f is taken of the sum
+ * before out2's rounding.  bias [n] fp32 and out2 may be NULL in the first two
+ * forms, in (a residual) in the first; every other matrix of a form is needed, and
+ * one that the form does not have is NULL (HM_ERR_ARG).  in, in2 and out2 are
+ * [m][pitch] in d_dtype, aligned to their element, pitch >= n.  D or out2 may be
+ * in or in2 exactly (same address and pitch); any other overlap with an output is
+ * HM_ERR_OVERLAP.  Activations: none, max(z, 0), z Phi(z) (GELU), its form with
+ * tanh, 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))), and z / (1 + exp(-z))
+ * (SiLU); the slope of max(z, 0) at 0 is 0.  f(-infinity) is NaN for the last three.
+ * k = 0: z = 0 before the bias.  Everything else as mxfp8_gemm, without accumulation;
+ * the struct is read during the call. */
+#define HM_EPI_FORWARD        0
+#define HM_EPI_GATED          1
+#define HM_EPI_GRADIENT       2
+#define HM_EPI_GATED_GRADIENT 3
+#define HM_ACT_NONE      0
+#define HM_ACT_RELU      1
+#define HM_ACT_GELU      2
+#define HM_ACT_GELU_TANH 3
+#define HM_ACT_SILU      4
+typedef struct {
+    int32_t form;         /* HM_EPI_* */
+    int32_t activation;   /* HM_ACT_* */
+    const float* bias;
+    const void* in;
+    int64_t ld_in;        /* elements */
+    const void* in2;
+    int64_t ld_in2;
+    void* out2;
+    int64_t ld_out2;
+} hm_epilogue;
+hm_status mxfp8_gemm_epilogue(const uint8_t* a, int64_t lda, const uint8_t* a_scales, const uint8_t* b, int64_t ldb,
+                              const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, void* d, int64_t ldd,
+                              hm_dtype d_dtype, const hm_epilogue* epilogue, void* stream);
+
 /* Quantizes x [rows][ldx] (HM_BF16 or HM_F32) to MXFP8 along its columns
  * and / or along its rows, reading x once:
  *   y[r][c] = x[r][c] * row_mul[r] * col_mul[c]   (fp32, in this order; a NULL
@@ -466,6 +510,20 @@ hm_status mxfp8_gemm_form(int64_t m, int64_t n, int64_t k, hm_dtype d_dtype, int
 hm_status mxfp8_quantize(const void* x, hm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx,
                          const float* row_mul, const float* col_mul, int block, uint8_t* q, int64_t ldq, uint8_t* s,
                          uint8_t* qt, int64_t ldqt, uint8_t* st, void* stream);
+
+/* The same without factors, and the sum of x's rows in the same pass: for x the
+ * gradient of a linear layer's output, the operands of its two gradient products
+ * and the gradient of its bias,
+ *   dbias[c] = sum_r x[r][c]                  (added to dbias when accumulate)
+ * fp32 [cols], summed in fp32 in a fixed order.  Everything else as
+ * mxfp8_quantize; dbias overlaps nothing else.  rows = 0 writes dbias = 0 unless
+ * accumulating.  workspace: 16-byte aligned, at least
+ * mxfp8_quantize_bias_workspace(rows, cols) bytes (HM_ERR_WORKSPACE; 0 for up to
+ * 128 rows), its contents need not be kept; calls that share one must not overlap. */
+hm_status mxfp8_quantize_bias_workspace(int64_t rows, int64_t cols, size_t* bytes);
+hm_status mxfp8_quantize_bias(const void* x, hm_dtype x_dtype, int64_t rows, int64_t cols, int64_t ldx, int block,
+                              uint8_t* q, int64_t ldq, uint8_t* s, uint8_t* qt, int64_t ldqt, uint8_t* st, float* dbias,
+                              int accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /* RMS norm with the residual's addition and an MXFP8 output, per row of d:
  *   h    = round(x + res)             (stored in `dtype`; res NULL: h = x)
@@ -498,6 +556,100 @@ hm_status rmsnorm_backward_workspace(int64_t rows, int64_t d, size_t* bytes);
 hm_status rmsnorm_backward(const void* dy, int64_t lddy, const void* dres, const void* h, void* dx, int64_t ldh,
                            hm_dtype dtype, int64_t rows, int64_t d, const float* gamma, const float* rstd,
                            float* dgamma, int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Norm of each query and key head and its rotation by the row's position, in one
+ * pass over the packed projection's output.  For every row and every head x of
+ * head_dim elements of a group:
+ *   v = x * gamma / sqrt(mean(x^2) + eps)     (gamma NULL: v = x)
+ *   y = v turned: pair i of the first rot_dim elements, (a, b), becomes
+ *       scale * (a cos t - b sin t, b cos t + a sin t),  t = positions[row] * freq[i]
+ * in fp32, rounded once.  Pair i is elements (i, i + rot_dim / 2) in HM_ROPE_HALF
+ * and (2 i, 2 i + 1) in HM_ROPE_PAIRS; elements from rot_dim on stay v.
+ * A group is `heads` heads that share gamma: element e of head j of row r at
+ * x[r * x_row + j * x_head + e], and likewise in y, which may be x itself with the
+ * same strides; no other outputs may overlap an input or each other
+ * (HM_ERR_OVERLAP).  Queries and keys are two groups; a token's keys can go
+ * straight to their place in a cache, heads first or rows first.  n_groups at
+ * most HM_HEAD_GROUPS; dtype HM_BF16 or HM_F32; pointers aligned to their element,
+ * heads of a group in the same row at least head_dim elements apart, and so are
+ * the rows of a head (HM_ERR_ARG).  head_dim even, up to HM_HEAD_MAX_DIM, rot_dim even,
+ * 0 .. head_dim (HM_ERR_GEOMETRY).
+ * turns: device, rot_dim / 2 frequencies in turns per position as fixed point,
+ * freq[i] / (2 pi) * 2^64 (rope_turns makes them): the product with the position
+ * wraps at whole turns by itself, so a position of any size or sign keeps a
+ * turn's fraction to 32 bits.  positions: device, int64 [rows].  rotation NULL
+ * or rot_dim 0: the norm alone.  rows = 0 or n_groups = 0 is a no-op. */
+#define HM_HEAD_MAX_DIM 512
+#define HM_HEAD_GROUPS 4
+#define HM_ROPE_HALF  0
+#define HM_ROPE_PAIRS 1
+typedef struct {
+    const uint64_t* turns;
+    const int64_t* positions;
+    float scale;              /* finite; of cos and sin */
+    int32_t rot_dim;
+    int32_t layout;           /* HM_ROPE_HALF or HM_ROPE_PAIRS */
+    int32_t pad;
+} hm_rotation;
+typedef struct {
+    const void* x;
+    int64_t x_row, x_head;    /* elements */
+    void* y;
+    int64_t y_row, y_head;
+    const float* gamma;       /* [head_dim] or NULL */
+    int32_t heads;
+    int32_t pad;
+} hm_head_group;
+hm_status head_norm_rope(const hm_head_group* groups, int n_groups, hm_dtype dtype, int64_t rows, int64_t head_dim,
+                         float eps, const hm_rotation* rotation, void* stream);
+
+/* Its gradient.  With t = dy turned back (by -t, the same scale), r = 1 / sqrt(mean(x^2) + eps),
+ * xhat = x r and u = t gamma:
+ *   dx     = r (u - xhat mean(u xhat))        (gamma NULL: dx = t, x is not read)
+ *   dgamma = sum over rows and heads of t xhat    (added to dgamma when accumulate;
+ *            NULL: not wanted)
+ * x is what the forward pass read, so that one must not have worked in place.
+ * dx may be dy or x itself with the same strides.  dgamma's sums run in fp32 in a
+ * fixed order; two groups that share a dgamma are refused (HM_ERR_OVERLAP).
+ * workspace as rmsnorm_backward's: head_norm_rope_backward_workspace bytes (0
+ * where no group wants dgamma).  rows = 0 writes dgamma = 0 unless accumulating. */
+typedef struct {
+    const void* dy;
+    int64_t dy_row, dy_head;
+    const void* x;
+    int64_t x_row, x_head;
+    void* dx;
+    int64_t dx_row, dx_head;
+    const float* gamma;
+    float* dgamma;
+    int32_t heads;
+    int32_t accumulate;
+} hm_head_grad;
+hm_status head_norm_rope_backward_workspace(const hm_head_grad* groups, int n_groups, int64_t rows, int64_t head_dim,
+                                            size_t* bytes);
+hm_status head_norm_rope_backward(const hm_head_grad* groups, int n_groups, hm_dtype dtype, int64_t rows,
+                                  int64_t head_dim, float eps, const hm_rotation* rotation, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Host: the frequencies theta^(-2 i / rot_dim), i < rot_dim / 2, in head_norm_rope's
+ * fixed point, and its scale, for contexts longer than the trained one by `factor`:
+ *   HM_ROPE_UNSCALED  as they are, scale 1 (factor and what follows are not read)
+ *   HM_ROPE_LINEAR    all divided by factor, scale 1
+ *   HM_ROPE_BASE      theta replaced by theta factor^(rot_dim / (rot_dim - 2)), scale 1: the
+ *                     last pair is divided by factor, the first stays (rot_dim > 2)
+ *   HM_ROPE_YARN      YaRN (Peng et al., arXiv 2309.00071, section 3): pairs that turn
+ *                     more than beta_fast times over `trained` positions stay, those that
+ *                     turn less than beta_slow times are divided by factor, between the two
+ *                     a ramp over i (its ends rounded outwards to whole pairs);
+ *                     scale = 1 + 0.1 ln(factor)
+ * turns: rot_dim / 2 words in host memory.  theta > 1, factor >= 1, trained >= 1,
+ * beta_fast > beta_slow > 0, all finite; rot_dim even, 2 .. HM_HEAD_MAX_DIM (HM_ERR_GEOMETRY). */
+#define HM_ROPE_UNSCALED 0
+#define HM_ROPE_LINEAR   1
+#define HM_ROPE_BASE     2
+#define HM_ROPE_YARN     3
+hm_status rope_turns(int32_t rot_dim, double theta, int32_t scaling, double factor, double trained, double beta_fast,
+                     double beta_slow, uint64_t* turns, float* scale);
 
 /* Global gradient norm over n tensors, and clipping:
  *   norm = sqrt(sum of every element's square)
