@@ -23,6 +23,7 @@
 // Every wait is bounded as in the Newton-Schulz kernels (HM_ERR_TIMEOUT in the
 // device error word).
 #include "hm.h"
+#include "hm_epilogue.cuh"
 #include "hm_internal.h"
 #include "hm_ops.h"
 #include "hm_ptx.cuh"
@@ -139,118 +140,6 @@ __device__ __forceinline__ void store_chunk(const MxGemmArgs& p, int i, int j0, 
 }
 
 // ---------------------------------------------------------------------------
-// Epilogue with activation (hm_epilogue).  Elements of D that a thread holds, N of them
-// along a column (ROWS: the pair kernel's and the undivided split kernel's chunks) or
-// along a row (the split kernel's added parts), `count` of them inside D.
-// ---------------------------------------------------------------------------
-template <int N, bool ROWS, bool F32>
-__device__ __forceinline__ void load_like_d(const void* base, int64_t ld, int row, int col, int count, float (&x)[N]) {
-    const int64_t at = static_cast<int64_t>(row) * ld + col, step = ROWS ? ld : 1;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        if (F32) x[j] = j < count ? static_cast<const float*>(base)[at + j * step] : 0.f;
-        else x[j] = j < count ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at + j * step]) << 16) : 0.f;
-    }
-}
-template <int N, bool ROWS, bool F32>
-__device__ __forceinline__ void store_like_d(void* base, int64_t ld, int row, int col, int count, const float (&x)[N]) {
-    const int64_t at = static_cast<int64_t>(row) * ld + col, step = ROWS ? ld : 1;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (j < count) {
-            if (F32) static_cast<float*>(base)[at + j * step] = x[j];
-            else static_cast<uint16_t*>(base)[at + j * step] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
-        }
-}
-
-// f(x) and f'(x).  SiLU and GELU's tanh form are both x s(u), s the logistic function
-// and u = x (c0 + c1 x^2): 0.5 (1 + tanh(w)) = s(2 w).  x^2 is held finite, so that
-// nothing infinite meets a vanished s or 1 - s (a NaN stays one through x).
-template <int N>
-__device__ __forceinline__ void activate(int act, const float (&x)[N], float (&f)[N], float (&slope)[N]) {
-    if (act == HM_ACT_SILU || act == HM_ACT_GELU_TANH) {
-        const float c0 = act == HM_ACT_SILU ? 1.f : 1.5957691216f;      // 2 sqrt(2 / pi)
-        const float c1 = act == HM_ACT_SILU ? 0.f : 0.0713548162726f;   // 0.044715 of it
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float x2 = fminf(x[j] * x[j], 1e30f);
-            const float s = __fdividef(1.f, 1.f + expf(-x[j] * fmaf(c1, x2, c0)));
-            f[j] = x[j] * s;
-            slope[j] = fmaf(f[j] * (1.f - s), fmaf(3.f * c1, x2, c0), s);
-        }
-    } else if (act == HM_ACT_GELU) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float phi = 0.5f * erfcf(-0.70710678118654752f * x[j]);
-            f[j] = x[j] * phi;
-            slope[j] = fmaf(x[j] * 0.39894228040143268f, expf(-0.5f * x[j] * x[j]), phi);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const bool off = act == HM_ACT_RELU && x[j] <= 0.f;
-            f[j] = off ? 0.f : x[j];
-            slope[j] = off || x[j] != x[j] ? 0.f : 1.f;
-        }
-    }
-}
-
-template <int N, bool ROWS, bool F32>
-__device__ __forceinline__ void finish_typed(const MxGemmArgs& p, int row, int col, int count, float (&z)[N]) {
-    const MxEpilogue& e = p.e;
-    float x[N], f[N], slope[N], more[N];
-    const bool has_in = e.in != nullptr;
-    if (has_in) load_like_d<N, ROWS, F32>(e.in, e.ld_in, row, col, count, x);
-    if (e.in2) load_like_d<N, ROWS, F32>(e.in2, e.ld_in2, row, col, count, more);
-    if (e.bias) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) z[j] += ROWS ? e.bias[col] : j < count ? e.bias[col + j] : 0.f;
-    }
-    if (e.form == HM_EPI_FORWARD) {
-        if (e.out2) store_like_d<N, ROWS, F32>(e.out2, e.ld_out2, row, col, count, z);
-        activate<N>(e.act, z, f, slope);
-#pragma unroll
-        for (int j = 0; j < N; ++j) z[j] = has_in ? f[j] + x[j] : f[j];
-    } else {
-        activate<N>(e.act, x, f, slope);
-        if (e.form == HM_EPI_GRADIENT) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) z[j] *= slope[j];
-        } else {
-            if (e.form == HM_EPI_GATED_GRADIENT) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) more[j] = z[j] * more[j] * slope[j];
-                store_like_d<N, ROWS, F32>(e.out2, e.ld_out2, row, col, count, more);
-            } else if (e.out2) {
-                store_like_d<N, ROWS, F32>(e.out2, e.ld_out2, row, col, count, z);
-            }
-#pragma unroll
-            for (int j = 0; j < N; ++j) z[j] *= f[j];
-        }
-    }
-    store_like_d<N, ROWS, F32>(p.d, p.ldd, row, col, count, z);
-}
-template <int N, bool ROWS>
-__device__ __forceinline__ void finish(const MxGemmArgs& p, int row, int col, int count, float (&z)[N]) {
-    if (p.d_f32) finish_typed<N, ROWS, true>(p, row, col, count, z);
-    else finish_typed<N, ROWS, false>(p, row, col, count, z);
-}
-// 16 rows from j0 of column i
-template <bool F32_ONLY = false>
-__device__ __forceinline__ void finish16(const MxGemmArgs& p, int i, int j0, const uint32_t (&r)[16]) {
-    if (i >= p.n) return;
-#pragma unroll
-    for (int b = 0; b < 16; b += 8) {
-        if (j0 + b >= p.m) return;
-        float z[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(r[b + j]);
-        if (F32_ONLY) finish_typed<8, true, true>(p, j0 + b, i, min(8, p.m - (j0 + b)), z);
-        else finish<8, true>(p, j0 + b, i, min(8, p.m - (j0 + b)), z);
-    }
-}
-
-// ---------------------------------------------------------------------------
 // Persistent kernel on CTA pairs (cta_group::2), tiles of 256 M-side rows (B's
 // rows, D's columns) x BN N-side rows (A's, D's rows), 320 threads per CTA.  Each CTA of a pair loads its 128 M-side rows
 // and half of the N-side rows; the even one issues the MMAs, which read both
@@ -303,7 +192,7 @@ __device__ __forceinline__ void pair_tile(const MxGemmArgs& p, int t, int& tp, i
     tq = l / rows;
 }
 
-template <int BN, bool SUMS, bool EPI>
+template <int BN, bool SUMS, int EPI>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUtensorMap mq,
                         const __grid_constant__ CUtensorMap msp, const __grid_constant__ CUtensorMap msq,
@@ -454,6 +343,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (lane == 0) mbar_arrive_cluster_relaxed(bar);
         };
         const uint32_t free0 = mapa_shared(smem_u32(&tfree[0]), 0), free1 = mapa_shared(smem_u32(&tfree[1]), 0);
+        // with an epilogue: this warp's place for turning pieces, its pieces of a tile and
+        // where the k-th begins (the owner of BN = 256's shared columns starts with those)
+        float* stage = reinterpret_cast<float*>(smem_raw + C::SMEM) + (warp - 2) * (kPieceBytes / 4);
+        constexpr int kPieces = (C::CHUNKS + 1) / 2 * 2;
+        auto piece_at = [&](int k, int unit) {
+            const int order = BN == 256 && !(unit & 1) ? (C::CHUNKS + 1) / 2 - 1 - (k >> 1) : k >> 1;
+            return (2 * order + half) * 32 + (k & 1) * 16;
+        };
         int u = 0;
         bool ok = true;
         for (int t = pair; t < total && ok; t += npairs) {
@@ -461,6 +358,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             pair_tile(p, t, tp, tq);
             const int i = tp * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
             float sum[SUMS ? (C::CHUNKS + 1) / 2 : 1][32];
+            EpiPiece<EPI, !SUMS> piece;
+            float2 bias[4];
+            if constexpr (EPI != kEpiNone) {
+                piece.bias(p, i - lane, bias);
+                if (!SUMS) piece.load(p, tq * BN + piece_at(0, u), i - lane);
+            }
             if (EPI) {
                 // what the epilogue reads, likewise (see below)
 #pragma unroll
@@ -491,70 +394,76 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const bool owner = BN == 256 && half == ((u & 1) ? 0 : 1);
                 if (BN == 256 && !owner) release(freed);
                 if constexpr (EPI && !SUMS) {
-                    // one copy of the epilogue's code: 16 columns of the accumulator at a time
+                    // one copy of the epilogue's code: a piece of 16 columns of the accumulator at a time
 #pragma unroll 1
-                    for (int k = 0; k < (C::CHUNKS + 1) / 2 * 2; ++k) {
-                        const int order = BN == 256 && !(u & 1) ? (C::CHUNKS + 1) / 2 - 1 - (k >> 1) : k >> 1;
-                        const int ch = 2 * order + half;
-                        if (ch >= C::CHUNKS) break;
-                        const int at = ch * 32 + (k & 1) * 16;
+                    for (int k = 0; k < kPieces; ++k) {
+                        const int at = piece_at(k, u), next = piece_at(k + 1, u);
+                        if (at >= BN) break;
+                        piece.begin(p, tq * BN + at, i - lane);
                         uint32_t r[16];
                         __syncwarp();
                         tmem_ld16(acc + at, r);
                         tmem_ld_wait();
                         tmem_ld_pin16(r);
                         if (owner && k == 1) release(freed);
-                        finish16(p, i, tq * BN + at, r);
+                        EpiPiece<EPI, true> ahead;
+                        if (k + 1 < kPieces && next < BN) ahead.load(p, tq * BN + next, i - lane);
+                        piece.finish(p, stage, tq * BN + at, i - lane, bias, r);
+                        piece.take(p, ahead);
                     }
                     if (BN != 256) release(freed);
-                    continue;
-                }
+                } else {
 #pragma unroll
-                for (int k = 0; k < (C::CHUNKS + 1) / 2; ++k) {
-                    const int order = BN == 256 && !(u & 1) ? (C::CHUNKS + 1) / 2 - 1 - k : k;
-                    const int ch = 2 * order + half;
-                    if (ch >= C::CHUNKS) break;
-                    if (SUMS) {
+                    for (int k = 0; k < (C::CHUNKS + 1) / 2; ++k) {
+                        const int order = BN == 256 && !(u & 1) ? (C::CHUNKS + 1) / 2 - 1 - k : k;
+                        const int ch = 2 * order + half;
+                        if (ch >= C::CHUNKS) break;
+                        if (SUMS) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t r[16];
-                            __syncwarp();
-                            tmem_ld16(acc + ch * 32 + h * 16, r);
-                            tmem_ld_wait();
-                            tmem_ld_pin16(r);
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t r[16];
+                                __syncwarp();
+                                tmem_ld16(acc + ch * 32 + h * 16, r);
+                                tmem_ld_wait();
+                                tmem_ld_pin16(r);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float v = __uint_as_float(r[j]);
-                                sum[k][16 * h + j] = c ? sum[k][16 * h + j] + v : v;
+                                for (int j = 0; j < 16; ++j) {
+                                    const float v = __uint_as_float(r[j]);
+                                    sum[k][16 * h + j] = c ? sum[k][16 * h + j] + v : v;
+                                }
                             }
+                            continue;
                         }
-                        continue;
+                        uint32_t r[32];
+                        __syncwarp();  // lanes past the last column left the chunk before early
+                        tmem_ld32(acc + ch * 32, r);
+                        tmem_ld_wait();
+                        tmem_ld_pin(r);
+                        if (owner && k == 0) release(freed);
+                        store_chunk(p, i, tq * BN + ch * 32, r);
                     }
-                    uint32_t r[32];
-                    __syncwarp();  // lanes past the last column left the chunk before early
-                    tmem_ld32(acc + ch * 32, r);
-                    tmem_ld_wait();
-                    tmem_ld_pin(r);
-                    if (owner && k == 0) release(freed);
-                    store_chunk(p, i, tq * BN + ch * 32, r);
+                    if (BN != 256) release(freed);
                 }
-                if (BN != 256) release(freed);
             }
-            if (SUMS && ok) {
+            if (SUMS && EPI != kEpiNone && ok) {
+#pragma unroll 1
+                for (int k = 0; k < kPieces; ++k) {
+                    const int at = (2 * (k >> 1) + half) * 32 + (k & 1) * 16;
+                    if (at >= BN) break;
+                    uint32_t r[16];
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c)
+                        if (c == k)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(sum[(c >> 1) % (SUMS ? kPieces / 2 : 1)][16 * (c & 1) + j]);
+                    piece.begin(p, tq * BN + at, i - lane);
+                    piece.finish(p, stage, tq * BN + at, i - lane, bias, r);
+                }
+            } else if (SUMS && ok) {
 #pragma unroll
                 for (int k = 0; k < (C::CHUNKS + 1) / 2; ++k) {
                     const int ch = 2 * k + half;
                     if (ch >= C::CHUNKS) break;
-                    if constexpr (EPI) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t r[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(sum[k][16 * h + j]);
-                            finish16<true>(p, i, tq * BN + ch * 32 + h * 16, r);
-                        }
-                        continue;
-                    }
                     uint32_t r[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[k][j]);
@@ -645,7 +554,7 @@ __device__ __forceinline__ void store_four(const MxGemmArgs& p, int row, int col
 // shared memory in flight (with two rows at a time the latency of those loads
 // made a split in two slower than none: 16.4 us against 14.5 at 355 x 3149 x
 // 4704).
-template <int CK, bool EPI>
+template <int CK, int EPI>
 __device__ __forceinline__ void add_parts(const MxGemmArgs& p, float* part, int rank, int warp, int lane, int col0,
                                           int row0, int rows) {
     constexpr int U = 16 / CK;
@@ -670,14 +579,14 @@ __device__ __forceinline__ void add_parts(const MxGemmArgs& p, float* part, int 
             for (int k = 1; k < CK; ++k)
                 v = make_float4(v.x + x[h][k].x, v.y + x[h][k].y, v.z + x[h][k].z, v.w + x[h][k].w);
             // with an epilogue the sum goes over this CTA's own part, which only this lane reads
-            if constexpr (EPI) *reinterpret_cast<float4*>(part + (c + h * step) * 128 + lane * 4) = v;
+            if constexpr (EPI != kEpiNone) *reinterpret_cast<float4*>(part + (c + h * step) * 128 + lane * 4) = v;
             else store_four(p, row0 + c + h * step, col, v);
         }
     }
 }
 
-template <int BN, bool EPI>
-__global__ void __launch_bounds__(kSplitThreads, 1)
+template <int BN, int EPI>
+__global__ void __launch_bounds__(kSplitThreads, EPI ? 2 : 1)
     mx_gemm_split_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
                          const __grid_constant__ MxGemmArgs p) {
     using C = SplitCfg<BN>;
@@ -779,18 +688,30 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     const int col = tp * kTileP + q * 32 + lane;  // column of D
     const int row0 = tq * BN;
     const int rows = min(BN, p.m - row0);
+    EpiPiece<EPI, true> piece;
+    float2 bias[4];
+    if (EPI && ck == 1 && warp >= 2) {
+        piece.bias(p, col - lane, bias);
+        piece.load(p, row0, col - lane);
+    }
     if (warp >= 2) {
         const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(tfull), 0, p.err, bail));
         tc_fence_after();
         if (EPI && ok && ck == 1) {
+            // the ring has been read: it turns the pieces
+            float* stage = reinterpret_cast<float*>(smem) + q * (kPieceBytes / 4);
 #pragma unroll 1
-            for (int c0 = 0; c0 < rows; c0 += 16) {
+            for (int c0 = 0; c0 < rows; c0 += kPieceRows) {
+                piece.begin(p, row0 + c0, col - lane);
                 uint32_t r[16];
                 __syncwarp();
                 tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, r);
                 tmem_ld_wait();
                 tmem_ld_pin16(r);
-                finish16(p, col, row0 + c0, r);
+                EpiPiece<EPI, true> ahead;
+                if (c0 + kPieceRows < rows) ahead.load(p, row0 + c0 + kPieceRows, col - lane);
+                piece.finish(p, stage, row0 + c0, col - lane, bias, r);
+                piece.take(p, ahead);
             }
         } else if (ok) {
 #pragma unroll 1
@@ -826,13 +747,25 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
             case 7: add_parts<7, EPI>(p, part, rank, warp, lane, c0, row0, rows); break;
             default: add_parts<8, EPI>(p, part, rank, warp, lane, c0, row0, rows); break;
         }
-        if constexpr (EPI) {
+        if constexpr (EPI != kEpiNone) {
             // the same rows and columns as above, one copy of the epilogue's code
+            const int at = c0 + lane * 4, count = p.n - at;
+            float b4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) b4[k] = p.e.bias && k < count ? p.e.bias[at + k] : 0.f;
+            const int step = ck * (kSplitThreads / 32);
+            EpiRow<EpiPiece<EPI, true>::F32, EpiPiece<EPI, true>::VEC> now, ahead;
+            int c = rank + warp * ck;
+            if (c < rows) now.load(p, row0 + c, at, count);
 #pragma unroll 1
-            for (int c = rank + warp * ck; c < rows; c += ck * (kSplitThreads / 32)) {
-                const float4 v = *reinterpret_cast<const float4*>(part + c * 128 + lane * 4);
-                float z[4] = {v.x, v.y, v.z, v.w};
-                if (c0 + lane * 4 < p.n) finish<4, false>(p, row0 + c, c0 + lane * 4, min(4, p.n - (c0 + lane * 4)), z);
+            for (; c < rows; c += step) {
+                if (c + step < rows) ahead.load(p, row0 + c + step, at, count);
+                if (count > 0) {
+                    const float4 v = *reinterpret_cast<const float4*>(part + c * 128 + lane * 4);
+                    const float2 z[2] = {make_float2(v.x + b4[0], v.y + b4[1]), make_float2(v.z + b4[2], v.w + b4[3])};
+                    now.finish(p, row0 + c, at, count, z);
+                }
+                now = ahead;
             }
         }
         __syncwarp();
@@ -857,12 +790,16 @@ __global__ void __launch_bounds__(256) mx_gemm_zero_kernel(const __grid_constant
 }
 
 // The same with an epilogue: z = 0 before the bias.
+template <bool F32>
 __global__ void __launch_bounds__(256) mx_gemm_empty_kernel(const __grid_constant__ MxGemmArgs p) {
     wait_for_earlier_kernels();
     const int64_t total = static_cast<int64_t>(p.m) * p.n;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        float z[1] = {0.f};
-        finish<1, true>(p, static_cast<int>(i / p.n), static_cast<int>(i % p.n), 1, z);
+        const int row = static_cast<int>(i / p.n), col = static_cast<int>(i % p.n);
+        EpiRow<F32, false> x;
+        x.load(p, row, col, 1);
+        const float2 z[2] = {make_float2(p.e.bias ? p.e.bias[col] : 0.f, 0.f), make_float2(0.f, 0.f)};
+        x.finish(p, row, col, 1, z);
     }
 }
 
@@ -929,7 +866,7 @@ int resident_clusters(int split) {
     cudaLaunchAttribute attr[2];
     split_config<BN>(cfg, attr, 1, 1, split, nullptr);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_split_kernel<BN, false>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_split_kernel<BN, kEpiNone>, &cfg) != cudaSuccess || n < 1) {
         cudaGetLastError();
         n = std::max(1, device_sm_count() / (2 * split));
     }
@@ -968,7 +905,7 @@ int split_for(int tiles_p, int tiles_q, const MxGemmArgs& p, double* cost) {
 template <int BN>
 cudaError_t split_form(const MxGemmArgs& p, MxGemmForm* f, double* cost) {
     static PerDevice done;
-    const cudaError_t e = allow_smem(mx_gemm_split_kernel<BN, false>, SplitCfg<BN>::SMEM, done);  // before its occupancy is asked
+    const cudaError_t e = allow_smem(mx_gemm_split_kernel<BN, kEpiNone>, SplitCfg<BN>::SMEM, done);  // before its occupancy is asked
     if (e != cudaSuccess) return e;
     f->tile = BN;
     f->parts = split_for<BN>((p.n + kTileP - 1) / kTileP, (p.m + BN - 1) / BN, p, cost);
@@ -983,21 +920,35 @@ cudaError_t launch_split(const uint8_t* a, int64_t lda, const uint8_t* b, int64_
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     split_config<BN>(cfg, attr, (p.n + kTileP - 1) / kTileP, (p.m + BN - 1) / BN, p.split, st);
+    auto kernel = mx_gemm_split_kernel<BN, kEpiNone>;
     if (p.epilogue) {
-        static PerDevice done;
-        const cudaError_t e = allow_smem(mx_gemm_split_kernel<BN, true>, SplitCfg<BN>::SMEM, done);
+        static PerDevice done[5];
+        kernel = p.epilogue == kEpiBf16  ? mx_gemm_split_kernel<BN, kEpiBf16>
+                 : p.epilogue == kEpiF32 ? mx_gemm_split_kernel<BN, kEpiF32>
+                 : p.d_f32               ? mx_gemm_split_kernel<BN, kEpiF32Any>
+                                         : mx_gemm_split_kernel<BN, kEpiBf16Any>;
+        const cudaError_t e = allow_smem(kernel, SplitCfg<BN>::SMEM, done[p.epilogue]);
         if (e != cudaSuccess) return e;
     }
     note_launch();
-    return cudaLaunchKernelEx(&cfg, p.epilogue ? mx_gemm_split_kernel<BN, true> : mx_gemm_split_kernel<BN, false>, ma, mb, p);
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
 }
 
-template <int BN, bool SUMS, bool EPI = false>
+template <int BN, bool SUMS, int EPI = kEpiNone>
 cudaError_t launch_pair(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, MxGemmArgs p, cudaStream_t st) {
     using C = PairMx<BN>;
-    if (!EPI && p.epilogue) return launch_pair<BN, SUMS, true>(a, lda, b, ldb, p, st);
+    if constexpr (EPI == kEpiNone) {
+        if (p.epilogue == kEpiF32) return launch_pair<BN, SUMS, kEpiF32>(a, lda, b, ldb, p, st);
+        if (p.epilogue == kEpiF32Any) return launch_pair<BN, SUMS, kEpiF32Any>(a, lda, b, ldb, p, st);
+        if constexpr (!SUMS) {
+            if (p.epilogue == kEpiBf16) return launch_pair<BN, SUMS, kEpiBf16>(a, lda, b, ldb, p, st);
+            if (p.epilogue == kEpiBf16Any) return launch_pair<BN, SUMS, kEpiBf16Any>(a, lda, b, ldb, p, st);
+        }
+    }
+    constexpr int smem = C::SMEM + (EPI ? kPairEpiWarps * kPieceBytes : 0);
+    static_assert(smem <= 232448, "the ring and the pieces");
     static PerDevice done;
-    cudaError_t e = allow_smem(mx_gemm_pair_kernel<BN, SUMS, EPI>, C::SMEM, done);
+    cudaError_t e = allow_smem(mx_gemm_pair_kernel<BN, SUMS, EPI>, smem, done);
     if (e != cudaSuccess) return e;
     CUtensorMap mp, mq, msp, msq;
     if (!map_codes(&mp, b, p.k, p.n, ldb, kTileP) || !map_codes(&mq, a, p.k, p.m, lda, BN / 2) ||
@@ -1010,7 +961,7 @@ cudaError_t launch_pair(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs, 1, 1);
     cfg.blockDim = dim3(kPairThreads, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     cluster_early(cfg, attr, 2);
@@ -1070,12 +1021,19 @@ cudaError_t mx_gemm_form(const MxGemmArgs& args, MxGemmForm* f) {
 cudaError_t launch_mx_gemm(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, const MxGemmArgs& args,
                            cudaStream_t st) {
     MxGemmArgs p = args;
+    if (p.epilogue) {
+        const int64_t es = p.d_f32 ? 4 : 2;
+        const auto rows16 = [&](const void* q, int64_t ld) { return !q || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * es % 16 == 0); };
+        const bool vec = p.n % 8 == 0 && rows16(p.d, p.ldd) && rows16(p.e.in, p.e.ld_in) && rows16(p.e.in2, p.e.ld_in2) && rows16(p.e.out2, p.e.ld_out2);
+        p.epilogue = p.d_f32 ? (vec ? kEpiF32 : kEpiF32Any) : (vec ? kEpiBf16 : kEpiBf16Any);
+    }
     if (p.k == 0) {
         if (p.accumulate) return cudaSuccess;
         const int64_t blocks = (static_cast<int64_t>(p.m) * p.n + 255) / 256;
         note_launch();
         if (p.epilogue) {
-            mx_gemm_empty_kernel<<<resident_grid(mx_gemm_empty_kernel, 256, blocks), 256, 0, st>>>(p);
+            const auto kernel = p.d_f32 ? mx_gemm_empty_kernel<true> : mx_gemm_empty_kernel<false>;
+            kernel<<<resident_grid(kernel, 256, blocks), 256, 0, st>>>(p);
             return cudaGetLastError();
         }
         mx_gemm_zero_kernel<<<resident_grid(mx_gemm_zero_kernel, 256, blocks), 256, 0, st>>>(p);

@@ -17,6 +17,7 @@
 #include "hm_mx_device.cuh"
 #include "hm_ops.h"
 #include "hm_ptx.cuh"
+#include "hm_vec.cuh"
 
 #include <cuda_bf16.h>
 
@@ -488,67 +489,6 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* partials, int
 // ---------------------------------------------------------------------------
 constexpr int kHeadThreads = 256;
 
-template <bool F32, int W>
-struct HeadVec {
-    static constexpr int kBytes = W * (F32 ? 4 : 2);
-    static constexpr int N = kBytes < 4 ? 1 : kBytes / 4;
-    uint32_t w[N];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int k = 0; k < N; ++k) w[k] = 0u;
-    }
-    __device__ __forceinline__ void load(const void* base, int64_t at) {
-        const char* p = static_cast<const char*>(base) + at * (F32 ? 4 : 2);
-        if constexpr (kBytes >= 16) {
-#pragma unroll
-            for (int k = 0; k < N / 4; ++k) {
-                const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + k);
-                w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
-            }
-        } else if constexpr (kBytes == 8) {
-            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
-            w[0] = v.x; w[1] = v.y;
-        } else if constexpr (kBytes == 4) {
-            w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
-        } else {
-            w[0] = __ldcs(reinterpret_cast<const uint16_t*>(p));
-        }
-    }
-    __device__ __forceinline__ void get(float (&v)[W]) const {
-#pragma unroll
-        for (int k = 0; k < W; ++k)
-            v[k] = F32 ? __uint_as_float(w[F32 ? k : 0])
-                       : __uint_as_float(k & 1 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
-    }
-    static __device__ __forceinline__ void put(void* base, int64_t at, const float (&v)[W]) {
-        char* p = static_cast<char*>(base) + at * (F32 ? 4 : 2);
-        uint32_t w[N];
-        if constexpr (F32) {
-#pragma unroll
-            for (int k = 0; k < W; ++k) w[k] = __float_as_uint(v[k]);
-        } else if constexpr (W == 1) {
-            w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                w[k] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-        }
-        if constexpr (kBytes >= 16) {
-#pragma unroll
-            for (int k = 0; k < N / 4; ++k)
-                reinterpret_cast<uint4*>(p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-        } else if constexpr (kBytes == 8) {
-            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-        } else if constexpr (kBytes == 4) {
-            *reinterpret_cast<uint32_t*>(p) = w[0];
-        } else {
-            *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
-        }
-    }
-};
-
 // Where a lane's vector pair v begins in a head, and its place in the table.
 template <int W>
 struct HeadPlace {
@@ -666,7 +606,7 @@ __global__ void __launch_bounds__(kHeadThreads) head_kernel(const __grid_constan
     __syncthreads();
     // whole warps stay in the loop: a head's sum is over lanes
     for (int first = (local % g.parts) * slots; first < items; first += U * step) {
-        HeadVec<F32, W> xa[U][V], xb[U][V];
+        RowVec<F32, W> xa[U][V], xb[U][V];
         int row[U], head[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -712,8 +652,8 @@ __global__ void __launch_bounds__(kHeadThreads) head_kernel(const __grid_constan
                 const HeadPlace<W> at(p, lane + v * p.lanes);
                 if (!at.live) continue;
                 head_turn<W, false>(p, at, table + row[u] * (p.rot / 2), a[v], b[v]);
-                HeadVec<F32, W>::put(g.out, base + at.a, a[v]);
-                HeadVec<F32, W>::put(g.out, base + at.b, b[v]);
+                RowVec<F32, W>::put(g.out, base + at.a, a[v]);
+                RowVec<F32, W>::put(g.out, base + at.b, b[v]);
             }
         }
     }
@@ -753,7 +693,7 @@ __global__ void __launch_bounds__(kHeadThreads) head_grad_kernel(const __grid_co
             const int row = item / g.heads, head = item - row * g.heads;
             const int64_t in = (tok0 + row) * g.in_row + head * g.in_head;
             const int64_t at_x = (tok0 + row) * g.x_row + head * g.x_head;
-            HeadVec<F32, W> ya[V], yb[V], xa[V], xb[V];
+            RowVec<F32, W> ya[V], yb[V], xa[V], xb[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const HeadPlace<W> at(p, lane + v * p.lanes);
@@ -813,8 +753,8 @@ __global__ void __launch_bounds__(kHeadThreads) head_grad_kernel(const __grid_co
             for (int v = 0; v < V; ++v) {
                 const HeadPlace<W> at(p, lane + v * p.lanes);
                 if (!at.live) continue;
-                HeadVec<F32, W>::put(g.out, out + at.a, ta[v]);
-                HeadVec<F32, W>::put(g.out, out + at.b, tb[v]);
+                RowVec<F32, W>::put(g.out, out + at.a, ta[v]);
+                RowVec<F32, W>::put(g.out, out + at.b, tb[v]);
             }
         }
     }

@@ -55,7 +55,7 @@ struct MxEpilogue {
 };
 struct MxGemmArgs {
     MxEpilogue e;        // with `epilogue`
-    int32_t epilogue, pad;
+    int32_t epilogue, pad;  // whether (launch_mx_gemm: which form of) an epilogue
     const uint8_t* sa;   // tiled scales
     const uint8_t* sb;
     void* d;

@@ -133,7 +133,7 @@ SHAPES = [(1, 33, 32), (1, 5120, 1024), (5, 130, 96), (16, 128, 1024), (17, 257,
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_epilogue(hm, dev, i, shape, form, out):
     act = OL.ACTS[(i + FORMS.index(form)) % len(OL.ACTS)]
-    p = _Product(hm, dev, form, act, *shape, out, pad=(0, 3, 8)[i % 3], bias=i % 2 == 0, first=i % 3 != 1, keep=i % 4 != 2,
+    p = _Product(hm, dev, form, act, *shape, out, pad=(0, 3, -shape[1] % 8)[i % 3], bias=i % 2 == 0, first=i % 3 != 1, keep=i % 4 != 2,
                  block=(32, 128)[i % 2])
     p.call()
     p.check()
