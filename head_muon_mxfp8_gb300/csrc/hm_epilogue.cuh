@@ -29,28 +29,6 @@ constexpr int kPieceRows = 16;
 constexpr int kPiecePitch = 36;  // floats: rows 4 banks apart
 constexpr int kPieceBytes = kPieceRows * kPiecePitch * 4;
 
-__device__ __forceinline__ uint64_t pack2(float2 v) {
-    return static_cast<uint64_t>(__float_as_uint(v.x)) | (static_cast<uint64_t>(__float_as_uint(v.y)) << 32);
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-    return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
-    return unpack2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
-    return unpack2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
-    return unpack2(r);
-}
-__device__ __forceinline__ float2 both2(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -66,14 +44,12 @@ __device__ __forceinline__ float2 inv_fast(float2 x) { return make_float2(inv_fa
 
 // Activations of two elements: value() and both(), with the slope.
 constexpr float kLog2e = 1.4426950408889634f;
-struct ActNone {
-    __device__ __forceinline__ float2 value(float2 x) const { return x; }
-    __device__ __forceinline__ float2 both(float2 x, float2& slope) const { slope = both2(1.f); return x; }
-};
-struct ActRelu {
-    __device__ __forceinline__ float2 value(float2 x) const { return make_float2(x.x <= 0.f ? 0.f : x.x, x.y <= 0.f ? 0.f : x.y); }  // a NaN stays
+// max(x, 0), and x itself where `cut` is NaN; a NaN stays.
+struct ActCut {
+    float cut;
+    __device__ __forceinline__ float2 value(float2 x) const { return make_float2(x.x <= cut ? 0.f : x.x, x.y <= cut ? 0.f : x.y); }
     __device__ __forceinline__ float2 both(float2 x, float2& slope) const {
-        slope = make_float2(x.x > 0.f ? 1.f : 0.f, x.y > 0.f ? 1.f : 0.f);
+        slope = make_float2(x.x <= cut ? 0.f : 1.f, x.y <= cut ? 0.f : 1.f);
         return value(x);
     }
 };
@@ -136,8 +112,8 @@ struct ActGeluBf16 {
     }
 };
 
-// D and out2 of N / 2 pairs, handed to store(D, out2).  z: the product with the bias;
-// x: in; y: in2.
+// D and out2 of P pairs, handed to store(D, out2).  z: the product with the bias; x: in;
+// y: in2.
 template <int P, class Act, class Store>
 __device__ __forceinline__ void finish_as(const MxEpilogue& e, const Act act, const float2 (&z)[P], const float2 (&x)[P],
                                           const float2 (&y)[P], const Store& store) {
@@ -174,19 +150,51 @@ __device__ __forceinline__ void finish_as(const MxEpilogue& e, const Act act, co
         store(d, w);
     }
 }
+// Calls f(activation).
+template <bool F32, class F>
+__device__ __forceinline__ void with_activation(int act, const F& f) {
+    if (act <= HM_ACT_RELU) {
+        f(ActCut{act == HM_ACT_RELU ? 0.f : __int_as_float(0x7fffffff)});
+    } else if (act == HM_ACT_GELU) {
+        if constexpr (F32) f(ActGeluF32{});
+        else f(ActGeluBf16{});
+    } else if (act == HM_ACT_GELU_TANH) {
+        f(ActGeluTanh{});
+    } else {
+        f(ActSilu{});
+    }
+}
 template <bool F32, int P, class Store>
 __device__ __forceinline__ void finish_elements(const MxEpilogue& e, const float2 (&z)[P], const float2 (&x)[P],
                                                 const float2 (&y)[P], const Store& store) {
-    switch (e.act) {
-        case HM_ACT_NONE: finish_as<P>(e, ActNone{}, z, x, y, store); break;
-        case HM_ACT_RELU: finish_as<P>(e, ActRelu{}, z, x, y, store); break;
-        case HM_ACT_GELU:
-            if constexpr (F32) finish_as<P>(e, ActGeluF32{}, z, x, y, store);
-            else finish_as<P>(e, ActGeluBf16{}, z, x, y, store);
-            break;
-        case HM_ACT_GELU_TANH: finish_as<P>(e, ActGeluTanh{}, z, x, y, store); break;
-        default: finish_as<P>(e, ActSilu{}, z, x, y, store);
+    with_activation<F32>(e.act, [&](const auto act) { finish_as<P>(e, act, z, x, y, store); });
+}
+// The same in little code, for the kernels whose time is not their epilogue's: the
+// activation and its slope first, then the form.
+template <bool F32, int P, class Store>
+__device__ __forceinline__ void finish_short(const MxEpilogue& e, const float2 (&z)[P], const float2 (&x)[P],
+                                             const float2 (&y)[P], const Store& store) {
+    const bool forward = e.form == HM_EPI_FORWARD;
+    float2 f[P], slope[P], w[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) f[j] = forward ? z[j] : x[j], w[j] = z[j];
+    with_activation<F32>(e.act, [&](const auto act) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) f[j] = act.both(f[j], slope[j]);
+    });
+    if (forward) {
+        if (e.in)
+#pragma unroll
+            for (int j = 0; j < P; ++j) f[j] = add2(f[j], x[j]);
+    } else {
+        const bool plain = e.form == HM_EPI_GRADIENT;
+        if (e.form == HM_EPI_GATED_GRADIENT)
+#pragma unroll
+            for (int j = 0; j < P; ++j) w[j] = mul2(mul2(w[j], y[j]), slope[j]);
+#pragma unroll
+        for (int j = 0; j < P; ++j) f[j] = mul2(z[j], plain ? slope[j] : f[j]);
     }
+    store(f, w);
 }
 
 template <bool F32, int N, int P>
@@ -226,7 +234,7 @@ struct EpiRow {
         float2 x[2], y[2];
         to_pairs<F32, 4>(in, x, 0);
         to_pairs<F32, 4>(in2, y, 0);
-        finish_elements<F32>(p.e, z, x, y, [&](const float2(&d)[2], const float2(&w)[2]) {
+        finish_short<F32>(p.e, z, x, y, [&](const float2(&d)[2], const float2(&w)[2]) {
             if (p.e.out2) put(from_pairs<F32, 4>(w, 0), p.e.out2, row * p.e.ld_out2 + col, count);
             put(from_pairs<F32, 4>(d, 0), p.d, row * p.ldd + col, count);
         });
@@ -239,7 +247,8 @@ constexpr int kEpiNone = 0, kEpiBf16 = 1, kEpiF32 = 2, kEpiBf16Any = 3, kEpiF32A
 
 // Pieces of a warp.  AHEAD: load() one piece ahead of its finish() (aligned rows only);
 // otherwise finish() loads what it needs itself, but for a lane's column: begin() does.
-template <int EPI, bool AHEAD>
+// SHORT: finish_short.
+template <int EPI, bool AHEAD, bool SHORT>
 struct EpiPiece {
     static constexpr bool F32 = EPI == kEpiF32 || EPI == kEpiF32Any, VEC = EPI == kEpiBf16 || EPI == kEpiF32;
     static constexpr bool kAhead = AHEAD && VEC;
@@ -328,7 +337,7 @@ struct EpiPiece {
                         to_pairs<F32, 8>(second ? in2[1] : in2[k], y, 4 * k);
                     }
                 }
-                finish_elements<F32>(p.e, z, x, y, [&](const float2(&d)[4 * H], const float2(&w)[4 * H]) {
+                const auto store = [&](const float2(&d)[4 * H], const float2(&w)[4 * H]) {
 #pragma unroll
                     for (int k = 0; k < H; ++k) {
                         const int row = r0 + 8 * (h0 + k);
@@ -336,7 +345,9 @@ struct EpiPiece {
                         if (p.e.out2) from_pairs<F32, 8>(w, 4 * k).store(p.e.out2, row * p.e.ld_out2 + col);
                         from_pairs<F32, 8>(d, 4 * k).store(p.d, row * p.ldd + col);
                     }
-                });
+                };
+                if constexpr (SHORT) finish_short<F32>(p.e, z, x, y, store);
+                else finish_elements<F32>(p.e, z, x, y, store);
             }
         } else {
             const int col = col0 + lane, rows = p.m - row0;
@@ -367,7 +378,7 @@ struct EpiPiece {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 z[j] = add2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), b[0]);
-            finish_elements<F32>(p.e, z, x, y, [&](const float2(&d)[8], const float2(&w)[8]) {
+            finish_short<F32>(p.e, z, x, y, [&](const float2(&d)[8], const float2(&w)[8]) {
                 if (p.e.out2) put(w, p.e.out2, p.e.ld_out2);
                 put(d, p.d, p.ldd);
             });

@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             pair_tile(p, t, tp, tq);
             const int i = tp * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
             float sum[SUMS ? (C::CHUNKS + 1) / 2 : 1][32];
-            EpiPiece<EPI, !SUMS> piece;
+            EpiPiece<EPI, !SUMS, SUMS> piece;
             float2 bias[4];
             if constexpr (EPI != kEpiNone) {
                 piece.bias(p, i - lane, bias);
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         tmem_ld_wait();
                         tmem_ld_pin16(r);
                         if (owner && k == 1) release(freed);
-                        EpiPiece<EPI, true> ahead;
+                        EpiPiece<EPI, true, false> ahead;
                         if (k + 1 < kPieces && next < BN) ahead.load(p, tq * BN + next, i - lane);
                         piece.finish(p, stage, tq * BN + at, i - lane, bias, r);
                         piece.take(p, ahead);
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kSplitThreads, EPI ? 2 : 1)
     const int col = tp * kTileP + q * 32 + lane;  // column of D
     const int row0 = tq * BN;
     const int rows = min(BN, p.m - row0);
-    EpiPiece<EPI, true> piece;
+    EpiPiece<EPI, true, true> piece;
     float2 bias[4];
     if (EPI && ck == 1 && warp >= 2) {
         piece.bias(p, col - lane, bias);
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(kSplitThreads, EPI ? 2 : 1)
                 tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, r);
                 tmem_ld_wait();
                 tmem_ld_pin16(r);
-                EpiPiece<EPI, true> ahead;
+                EpiPiece<EPI, true, true> ahead;
                 if (c0 + kPieceRows < rows) ahead.load(p, row0 + c0 + kPieceRows, col - lane);
                 piece.finish(p, stage, row0 + c0, col - lane, bias, r);
                 piece.take(p, ahead);
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kSplitThreads, EPI ? 2 : 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) b4[k] = p.e.bias && k < count ? p.e.bias[at + k] : 0.f;
             const int step = ck * (kSplitThreads / 32);
-            EpiRow<EpiPiece<EPI, true>::F32, EpiPiece<EPI, true>::VEC> now, ahead;
+            EpiRow<EPI == kEpiF32 || EPI == kEpiF32Any, EPI == kEpiBf16 || EPI == kEpiF32> now, ahead;
             int c = rank + warp * ck;
             if (c < rows) now.load(p, row0 + c, at, count);
 #pragma unroll 1

@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace hm {
 
@@ -483,96 +484,271 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* partials, int
 //
 // The pairs of a head lie in vectors of W elements: vector pair v is the W first and
 // the W second elements of pairs (halves), or two vectors of adjacent pairs; past
-// the rotated part, two vectors of the rest.  A group of `lanes` lanes holds a head,
-// V vector pairs each, so a pair never leaves its thread and in-place work is safe.
-// W is the widest that divides the head, its rotated part, strides and addresses.
+// the rotated part, two vectors of the rest.  A thread holds 8 / W vector pairs, so a
+// pair never leaves its thread and in-place work is safe; a head takes as many
+// neighbouring lanes as that needs, a warp as many heads as fit (head_dim 96: 5 heads
+// of 6 lanes).  W is the widest that divides the head, its rotated part, strides
+// and addresses.  Arithmetic goes two pairs at a time: one by one, with a division
+// per head and a 64-bit multiplication per address, the kernel issued 31 instructions
+// per element where memory leaves time for 21 (8192 x 80 heads of 128 bf16: 100 us).
 // ---------------------------------------------------------------------------
 constexpr int kHeadThreads = 256;
 
-// Where a lane's vector pair v begins in a head, and its place in the table.
-template <int W>
+// A thread's 8 first and 8 second elements of pairs.
+struct HeadPairs {
+    float2 a[4], b[4];
+};
+
+// Where a lane's vector pairs lie in a head.
+template <int W, bool PAIRS>
 struct HeadPlace {
-    int a, b;      // first elements of its two vectors
-    int v;
-    bool live, rotated;
-    __device__ __forceinline__ HeadPlace(const HeadArgs& p, int v_) : v(v_) {
-        const int turned = p.rot / (2 * W), all = p.dim / (2 * W);
-        live = v < all;
-        rotated = v < turned;
-        if (!rotated) {
-            a = p.rot + W * (v - turned);
-            b = a + (p.dim - p.rot) / 2;
-        } else if (W == 1 && p.pairs) {
-            a = 2 * v;
-            b = a + 1;
-        } else {
-            a = W * v;
-            b = a + p.rot / 2;
+    static constexpr int V = 8 / W;
+    int a[V], b[V];   // first elements of the two vectors
+    int v[V];         // place in the planes of the tables
+    int all;          // vector pairs of a head
+    int mine;         // this lane's vector pairs (with W = 8 always one, with 4 one or two)
+    __device__ __forceinline__ HeadPlace(const HeadArgs& p, int lane) : all(p.dim / (2 * W)), mine((all - lane + p.lanes - 1) / p.lanes) {
+        const int turned = p.rot / (2 * W);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int i = min(lane + k * p.lanes, all - 1);
+            v[k] = i;
+            if (i >= turned) {
+                a[k] = p.rot + W * (i - turned);
+                b[k] = a[k] + (p.dim - p.rot) / 2;
+            } else if (W == 1 && PAIRS) {
+                a[k] = 2 * i;
+                b[k] = a[k] + 1;
+            } else {
+                a[k] = W * i;
+                b[k] = a[k] + p.rot / 2;
+            }
+        }
+    }
+    __device__ __forceinline__ bool live(int k) const { return V == 1 || (V == 2 && k == 0) || k < mine; }
+    // element of the head that is pair e's first (second: the one after it, or as far on in b)
+    __device__ __forceinline__ int first(int k, int e) const {
+        return !PAIRS || W == 1 ? a[k] + e : e < W / 2 ? a[k] + 2 * e : b[k] + 2 * e - W;
+    }
+    __device__ __forceinline__ int second(int k, int e) const { return !PAIRS || W == 1 ? b[k] + e : first(k, e) + 1; }
+};
+
+// A thread's part of a head as loaded.
+template <bool F32, int W, bool PAIRS>
+struct HeadRaw {
+    static constexpr int V = 8 / W;
+    RowVec<F32, W> a[V], b[V];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < V; ++k) a[k].clear(), b[k].clear();
+    }
+    __device__ __forceinline__ void load(const HeadPlace<W, PAIRS>& at, const char* head) {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (at.live(k)) {
+                a[k].load(head, at.a[k]);
+                b[k].load(head, at.b[k]);
+            }
+    }
+    __device__ __forceinline__ void get(HeadPairs& x) const {
+        float first[8], second[8];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            float u[W], v[W];
+            a[k].get(u);
+            b[k].get(v);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                first[k * W + e] = !PAIRS || W == 1 ? u[e] : e < W / 2 ? u[(2 * e) % W] : v[(2 * e) % W];
+                second[k * W + e] = !PAIRS || W == 1 ? v[e] : e < W / 2 ? u[(2 * e + 1) % W] : v[(2 * e + 1) % W];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x.a[j] = make_float2(first[2 * j], first[2 * j + 1]);
+            x.b[j] = make_float2(second[2 * j], second[2 * j + 1]);
+        }
+    }
+    static __device__ __forceinline__ void put(const HeadPlace<W, PAIRS>& at, char* head, const HeadPairs& x) {
+        float first[8], second[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            first[2 * j] = x.a[j].x, first[2 * j + 1] = x.a[j].y;
+            second[2 * j] = x.b[j].x, second[2 * j + 1] = x.b[j].y;
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            if (!at.live(k)) continue;
+            float u[W], v[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                if (!PAIRS || W == 1) {
+                    u[e] = first[k * W + e];
+                    v[e] = second[k * W + e];
+                } else {
+                    u[e] = e & 1 ? second[k * W + e / 2] : first[k * W + e / 2];
+                    v[e] = e & 1 ? second[k * W + W / 2 + e / 2] : first[k * W + W / 2 + e / 2];
+                }
+            }
+            RowVec<F32, W>::put(head, at.a[k], u);
+            RowVec<F32, W>::put(head, at.b[k], v);
         }
     }
 };
 
-// (cos, sin) of `tokens` rows from tok0, scaled: the table's entry (t, e, v) is the e-th
-// pair of vector pair v, so that neighbouring lanes read neighbouring words.
+// Tables in shared memory hold two values for each pair of a head, dim floats: all
+// first ones, then all second ones; each in planes of M pairs of every vector pair, so
+// that neighbouring lanes read neighbouring M floats.
 template <int W>
-__device__ __forceinline__ void head_table(const HeadArgs& p, int64_t tok0, int tokens, float2* table) {
-    const int half = p.rot / 2, turned = p.rot / (2 * W);
-    for (int i = threadIdx.x; i < tokens * half; i += kHeadThreads) {
-        const int t = i / half, c = i - t * half;  // pair c of row tok0 + t
-        int v, e;
-        if (W > 1 && p.pairs) {  // a vector holds W / 2 pairs; the second vector's follow the first's
-            const int vec = c / (W / 2), in = c - vec * (W / 2);
-            v = vec < turned ? vec : vec - turned;
-            e = vec < turned ? in : W / 2 + in;
+__device__ __forceinline__ int head_plane(int v, int e, int all) {
+    constexpr int M = W < 4 ? W : 4;
+    return ((e / M) * all + v) * M + e % M;
+}
+template <int W, bool PAIRS>
+__device__ __forceinline__ void head_planes(const HeadPlace<W, PAIRS>& at, const float* table, int dim, HeadPairs& x) {
+    constexpr int M = W < 4 ? W : 4, V = 8 / W;
+    float c[8], s[8];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+#pragma unroll
+        for (int h = 0; h < W / M; ++h) {
+            const float* from = table + (h * at.all + at.v[k]) * M;
+            float* ck = c + k * W + h * M;
+            float* sk = s + k * W + h * M;
+            if constexpr (M == 4) {
+                const float4 u = *reinterpret_cast<const float4*>(from), v = *reinterpret_cast<const float4*>(from + dim / 2);
+                ck[0] = u.x, ck[1] = u.y, ck[2] = u.z, ck[3] = u.w;
+                sk[0] = v.x, sk[1] = v.y, sk[2] = v.z, sk[3] = v.w;
+            } else if constexpr (M == 2) {
+                const float2 u = *reinterpret_cast<const float2*>(from), v = *reinterpret_cast<const float2*>(from + dim / 2);
+                ck[0] = u.x, ck[1] = u.y;
+                sk[0] = v.x, sk[1] = v.y;
+            } else {
+                ck[0] = *from;
+                sk[0] = from[dim / 2];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x.a[j] = make_float2(c[2 * j], c[2 * j + 1]);
+        x.b[j] = make_float2(s[2 * j], s[2 * j + 1]);
+    }
+}
+
+// sin and cos of pi y, |y| <= 1/4: their Taylor series, off by less than 2^-30 there;
+// pi in two parts, so that the sine keeps its last bit.
+__device__ __forceinline__ void sincos_eighth(float y, float& s, float& c) {
+    const float z = y * y;
+    float u = fmaf(z, 0.08214588661f, -0.59926452932f);
+    u = fmaf(u, z, 2.55016403988f);
+    u = fmaf(u, z, -5.16771278005f);
+    s = fmaf(y, 3.14159274101f, y * fmaf(u, z, -8.74227801e-8f));
+    float v = fmaf(z, -0.02580689139f, 0.23533063036f);
+    v = fmaf(v, z, -1.33526276885f);
+    v = fmaf(v, z, 4.05871212642f);
+    v = fmaf(v, z, -4.93480220054f);
+    c = fmaf(v, z, 1.f);
+}
+
+// cos and sin of `tokens` rows from tok0, scaled (1 and 0 past the rotated part): a
+// table of dim floats for each.
+template <int W, bool PAIRS>
+__device__ __forceinline__ void head_angles(const HeadArgs& p, int64_t tok0, int tokens, float* tables) {
+    const int half = p.dim / 2, pairs = p.rot / 2, turned = p.rot / (2 * W), all = p.dim / (2 * W);
+    int t = threadIdx.x / half, c = threadIdx.x - t * half;  // pair c of row tok0 + t
+    const int t_on = kHeadThreads / half, c_on = kHeadThreads - t_on * half;
+    while (t < tokens) {
+        float cs = 1.f, sn = 0.f;
+        int v = c / W, e = c - v * W;
+        if (c < pairs) {
+            if (W > 1 && PAIRS) {  // a vector holds W / 2 pairs; the second vector's follow the first's
+                constexpr int P = W > 1 ? W / 2 : 1;
+                const int vec = c / P, in = c - vec * P;
+                v = vec < turned ? vec : vec - turned;
+                e = vec < turned ? in : P + in;
+            }
+            const uint64_t turn = static_cast<uint64_t>(p.positions[tok0 + t]) * p.turns[c];
+            const uint32_t hi = static_cast<uint32_t>(turn >> 32);
+            const uint32_t quarter = (hi + 0x20000000u) >> 30;
+            const int32_t rest = static_cast<int32_t>(hi - (quarter << 30));  // an eighth of a turn at most
+            float s, k;
+            sincos_eighth(static_cast<float>(rest) * 0x1p-31f, s, k);
+            const float cq = quarter & 1 ? s : k, sq = quarter & 1 ? k : s;
+            cs = ((quarter + 1) & 2 ? -cq : cq) * p.scale;
+            sn = (quarter & 2 ? -sq : sq) * p.scale;
+        }
+        float* to = tables + t * p.dim + head_plane<W>(v, e, all);
+        to[0] = cs;
+        to[half] = sn;
+        t += t_on;
+        c += c_on;
+        if (c >= half) c -= half, ++t;
+    }
+}
+
+// Turns the pairs by the row's angles, or back.
+template <int W, bool PAIRS, bool BACK>
+__device__ __forceinline__ void head_turn(const HeadArgs& p, const HeadPlace<W, PAIRS>& at, const float* row, HeadPairs& x) {
+    HeadPairs w;
+    head_planes(at, row, p.dim, w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 ac = mul2(x.a[j], w.a[j]), bc = mul2(x.b[j], w.a[j]);
+        // the side that subtracts in single instructions, which negate for free
+        if (BACK) {
+            const float2 a = fma2(x.b[j], w.b[j], ac);
+            x.b[j] = make_float2(fmaf(-x.a[j].x, w.b[j].x, bc.x), fmaf(-x.a[j].y, w.b[j].y, bc.y));
+            x.a[j] = a;
         } else {
-            v = c / W;
-            e = c - v * W;
-        }
-        const uint64_t turn = static_cast<uint64_t>(p.positions[tok0 + t]) * p.turns[c];
-        const uint32_t hi = static_cast<uint32_t>(turn >> 32);
-        const uint32_t quarter = (hi + 0x20000000u) >> 30;
-        const int32_t rest = static_cast<int32_t>(hi - (quarter << 30));  // an eighth of a turn at most
-        float s, c0;
-        sincospif(static_cast<float>(rest) * 0x1p-31f, &s, &c0);
-        const float cq = quarter & 1 ? s : c0, sq = quarter & 1 ? c0 : s;
-        const float cs = (quarter + 1) & 2 ? -cq : cq, sn = quarter & 2 ? -sq : sq;
-        table[(t * W + e) * turned + v] = make_float2(cs * p.scale, sn * p.scale);
-    }
-}
-
-// Turns the pairs of (a, b) by the table's angles, or back.
-template <int W, bool BACK>
-__device__ __forceinline__ void head_turn(const HeadArgs& p, const HeadPlace<W>& at, const float2* row, float (&a)[W],
-                                          float (&b)[W]) {
-    if (!at.rotated) return;
-    const int turned = p.rot / (2 * W);
-    if (W > 1 && p.pairs) {
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-            const float2 cs = row[e * turned + at.v];
-            const float s = BACK ? -cs.y : cs.y;
-            float& u = e < W / 2 ? a[(2 * e) % W] : b[(2 * e) % W];
-            float& v = e < W / 2 ? a[(2 * e + 1) % W] : b[(2 * e + 1) % W];
-            const float u1 = u * cs.x - v * s, v1 = v * cs.x + u * s;
-            u = u1;
-            v = v1;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-            const float2 cs = row[e * turned + at.v];
-            const float s = BACK ? -cs.y : cs.y;
-            const float u1 = a[e] * cs.x - b[e] * s, v1 = b[e] * cs.x + a[e] * s;
-            a[e] = u1;
-            b[e] = v1;
+            const float2 b = fma2(x.a[j], w.b[j], bc);
+            x.a[j] = make_float2(fmaf(-x.b[j].x, w.b[j].x, ac.x), fmaf(-x.b[j].y, w.b[j].y, ac.y));
+            x.b[j] = b;
         }
     }
 }
 
-// Sum over a head's lanes.
-__device__ __forceinline__ float head_sum(float v, int lanes) {
-    for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// gamma as a table, written by the CTA's first head's lanes.  (In registers it cost 16
+// of them, and a CTA per SM.)
+template <int W, bool PAIRS>
+__device__ __forceinline__ void head_gamma(const HeadPlace<W, PAIRS>& at, const float* gamma, int dim, float* table) {
+#pragma unroll
+    for (int k = 0; k < 8 / W; ++k)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            float* to = table + head_plane<W>(at.v[k], e, at.all);
+            to[0] = gamma[at.first(k, e)];
+            to[dim / 2] = gamma[at.second(k, e)];
+        }
+}
+
+// Sum over a head's lanes, the same in each: a head's lanes are neighbours, `lane` this
+// one's place among them; whole warps come here.
+__device__ __forceinline__ float head_sum(float v, int lane, int lanes) {
+    if (lanes == 8) {
+#pragma unroll
+        for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+    if ((lanes & (lanes - 1)) == 0) {
+        for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        if (o >= lanes) continue;
+        const float t = __shfl_down_sync(0xffffffffu, v, o);
+        // a tree over any number: the upper part of what is left is folded onto its beginning
+        if (lane + o < lanes && lane < o) v += t;
+    }
+    return __shfl_sync(0xffffffffu, v, (threadIdx.x & 31) - lane);
+}
+
+// 1 / sqrt(sum / dim + eps): the hardware's approximation and a Newton step.
+__device__ __forceinline__ float head_rstd(float sum, float inv_dim, float eps) {
+    const float a = fmaf(sum, inv_dim, eps), y = rsqrtf(a);
+    const float e = fmaf(-a * y, y, 1.f);
+    return a > 1e-35f && a < 1e35f ? fmaf(0.5f * y, e, y) : y;
 }
 
 __device__ __forceinline__ int head_group(const HeadArgs& p) {
@@ -581,209 +757,193 @@ __device__ __forceinline__ int head_group(const HeadArgs& p) {
     return g;
 }
 
-template <bool F32, int W, int V, int U>
-__global__ void __launch_bounds__(kHeadThreads) head_kernel(const __grid_constant__ HeadArgs p) {
-    extern __shared__ float2 table[];
+// This thread's way through its CTA's rows: a range of them, in steps of `tokens`, in
+// each of which it takes every stride-th (row, head).  All strides are the host's.
+struct HeadWay {
+    int lane;          // of its head
+    int slot;          // which head of the CTA's round; -1: a lane that is left over
+    int row, head;     // its first item of a step
+    int part;          // of the CTAs that share a step
+    int64_t tok0, end;
+    __device__ __forceinline__ HeadWay(const HeadArgs& p, const HeadGroup& g) {
+        const int local = static_cast<int>(blockIdx.x) - g.cta0, range = local / g.split;
+        part = local - range * g.split;
+        const int per_warp = 32 / p.lanes, in_warp = (threadIdx.x & 31) / p.lanes;
+        lane = (threadIdx.x & 31) - in_warp * p.lanes;
+        slot = in_warp < per_warp ? (threadIdx.x >> 5) * per_warp + in_warp : -1;
+        const int item = part * g.slots + max(slot, 0);
+        row = item / g.heads;
+        head = item - row * g.heads;
+        tok0 = p.rows * range / g.ranges;
+        end = p.rows * (range + 1) / g.ranges;
+    }
+    // rounds that all threads of the CTA make in a step
+    __device__ __forceinline__ int rounds(const HeadGroup& g, int tokens) const {
+        return (tokens * g.heads - part * g.slots + g.stride - 1) / g.stride;
+    }
+};
+
+// Forward, persistent.  Every round a thread loads its next (row, head) before it works on this one.
+template <bool F32, int W, bool PAIRS>
+__global__ void __launch_bounds__(kHeadThreads, W < 4 ? 2 : F32 ? 3 : 4) head_kernel(const __grid_constant__ HeadArgs p) {
+    extern __shared__ __align__(16) float tables[];  // gamma, then the step's rows
+    constexpr int64_t es = F32 ? 4 : 2;
     wait_for_earlier_kernels();
     const HeadGroup& g = p.g[head_group(p)];
-    const int local = static_cast<int>(blockIdx.x) - g.cta0;
-    const int64_t tok0 = static_cast<int64_t>(local / g.parts) * g.tokens;
-    const int tokens = static_cast<int>(min(static_cast<int64_t>(g.tokens), p.rows - tok0));
-    const int lane = threadIdx.x & (p.lanes - 1), slot = threadIdx.x / p.lanes, slots = kHeadThreads / p.lanes;
-    const int items = tokens * g.heads, step = slots * g.parts;
-    const float inv_dim = static_cast<float>(p.dim);
-    float ga[V][W], gb[V][W];
+    const HeadWay way(p, g);
+    const HeadPlace<W, PAIRS> at(p, way.lane);
+    const float inv_dim = 1.f / static_cast<float>(p.dim);
+    const bool norm = g.gamma != nullptr;
+    if (norm && way.slot == 0) head_gamma(at, g.gamma, p.dim, tables);
+    HeadRaw<F32, W, PAIRS> next;
+    next.clear();
+    for (int64_t tok0 = way.tok0; tok0 < way.end; tok0 += g.tokens) {
+        const int tokens = static_cast<int>(min(static_cast<int64_t>(g.tokens), way.end - tok0));
+        const int rows = way.slot < 0 ? 0 : tokens;
+        int row = way.row, head = way.head;
+        const char* in = static_cast<const char*>(g.in) + ((tok0 + row) * g.in_row + head * g.in_head) * es;
+        char* out = static_cast<char*>(g.out) + ((tok0 + row) * g.out_row + head * g.out_head) * es;
+        if (row < rows) next.load(at, in);
+        __syncthreads();  // the tables before have been read
+        if (p.rot) head_angles<W, PAIRS>(p, tok0, tokens, tables + p.dim);
+        __syncthreads();
+        // whole warps stay in the loop: a head's sum is over lanes
+        for (int left = way.rounds(g, tokens); left > 0; --left) {
+            HeadPairs x;
+            next.get(x);
+            const bool live = row < rows;
+            const float* angles = tables + (row + 1) * p.dim;
+            char* to = out;
+            row += g.rows_on;
+            head += g.heads_on;
+            in += g.in_step;
+            out += g.out_step;
+            if (head >= g.heads) head -= g.heads, ++row, in += g.in_wrap, out += g.out_wrap;
+            if (row < rows) next.load(at, in);
+            if (norm) {
+                float2 sq = mul2(x.a[0], x.a[0]);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const HeadPlace<W> at(p, lane + v * p.lanes);
+                for (int j = 0; j < 4; ++j) {
+                    if (j) sq = fma2(x.a[j], x.a[j], sq);
+                    sq = fma2(x.b[j], x.b[j], sq);
+                }
+                const float2 r = both2(head_rstd(head_sum(sq.x + sq.y, way.lane, p.lanes), inv_dim, p.eps));
+                HeadPairs gamma;
+                head_planes(at, tables, p.dim, gamma);
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            ga[v][e] = g.gamma && at.live ? g.gamma[at.a + e] : 1.f;
-            gb[v][e] = g.gamma && at.live ? g.gamma[at.b + e] : 1.f;
-        }
-    }
-    if (p.rot) head_table<W>(p, tok0, tokens, table);
-    __syncthreads();
-    // whole warps stay in the loop: a head's sum is over lanes
-    for (int first = (local % g.parts) * slots; first < items; first += U * step) {
-        RowVec<F32, W> xa[U][V], xb[U][V];
-        int row[U], head[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int item = first + u * step + slot;
-            row[u] = item / g.heads;
-            head[u] = item - row[u] * g.heads;
-            const int64_t base = (tok0 + row[u]) * g.in_row + head[u] * g.in_head;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const HeadPlace<W> at(p, lane + v * p.lanes);
-                xa[u][v].clear();
-                xb[u][v].clear();
-                if (item < items && at.live) {
-                    xa[u][v].load(g.in, base + at.a);
-                    xb[u][v].load(g.in, base + at.b);
+                for (int j = 0; j < 4; ++j) {
+                    x.a[j] = mul2(mul2(x.a[j], r), gamma.a[j]);
+                    x.b[j] = mul2(mul2(x.b[j], r), gamma.b[j]);
                 }
             }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float a[V][W], b[V][W], sq = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                xa[u][v].get(a[v]);
-                xb[u][v].get(b[v]);
-#pragma unroll
-                for (int e = 0; e < W; ++e) sq = fmaf(a[v][e], a[v][e], fmaf(b[v][e], b[v][e], sq));
-            }
-            if (g.gamma) {
-                const float rstd = inv_root(head_sum(sq, p.lanes), inv_dim, p.eps);
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-#pragma unroll
-                    for (int e = 0; e < W; ++e) {
-                        a[v][e] = a[v][e] * rstd * ga[v][e];
-                        b[v][e] = b[v][e] * rstd * gb[v][e];
-                    }
-            }
-            if (first + u * step + slot >= items) continue;
-            const int64_t base = (tok0 + row[u]) * g.out_row + head[u] * g.out_head;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const HeadPlace<W> at(p, lane + v * p.lanes);
-                if (!at.live) continue;
-                head_turn<W, false>(p, at, table + row[u] * (p.rot / 2), a[v], b[v]);
-                RowVec<F32, W>::put(g.out, base + at.a, a[v]);
-                RowVec<F32, W>::put(g.out, base + at.b, b[v]);
-            }
+            if (!live) continue;
+            if (p.rot) head_turn<W, PAIRS, false>(p, at, angles, x);
+            HeadRaw<F32, W, PAIRS>::put(at, to, x);
         }
     }
 }
 
 // Gradient.  With t = dy turned back, u = t gamma, S1 = sum x^2 and S2 = sum u x, both
-// in the same round of shuffles: dx = r u - x r^3 S2 / dim.  A CTA takes steps of
-// `tokens` rows round-robin and keeps its lanes' part of dgamma in registers; the
-// lanes that hold the same elements are added at the end in a fixed order.
-template <bool F32, int W, int V>
-__global__ void __launch_bounds__(kHeadThreads) head_grad_kernel(const __grid_constant__ HeadArgs p) {
-    extern __shared__ float2 table[];
+// in the same round of shuffles: dx = r u - x r^3 S2 / dim.  A thread keeps its
+// elements' part of dgamma in registers; the slots' parts are added at the end in order.
+template <bool F32, int W, bool PAIRS>
+__global__ void __launch_bounds__(kHeadThreads, W == 1 ? 1 : 2) head_grad_kernel(const __grid_constant__ HeadArgs p) {
+    extern __shared__ __align__(16) float tables[];
+    constexpr int64_t es = F32 ? 4 : 2;
     wait_for_earlier_kernels();
     const HeadGroup& g = p.g[head_group(p)];
-    const int local = static_cast<int>(blockIdx.x) - g.cta0;
-    const int lane = threadIdx.x & (p.lanes - 1), slot = threadIdx.x / p.lanes, slots = kHeadThreads / p.lanes;
-    const float dim = static_cast<float>(p.dim);
-    float ga[V][W], gb[V][W], da[V][W], db[V][W];
+    const HeadWay way(p, g);
+    const HeadPlace<W, PAIRS> at(p, way.lane);
+    const float inv_dim = 1.f / static_cast<float>(p.dim);
+    const bool norm = g.gamma != nullptr;
+    if (norm && way.slot == 0) head_gamma(at, g.gamma, p.dim, tables);
+    HeadPairs dg;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const HeadPlace<W> at(p, lane + v * p.lanes);
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-            ga[v][e] = g.gamma && at.live ? g.gamma[at.a + e] : 0.f;
-            gb[v][e] = g.gamma && at.live ? g.gamma[at.b + e] : 0.f;
-            da[v][e] = db[v][e] = 0.f;
+    for (int j = 0; j < 4; ++j) dg.a[j] = dg.b[j] = both2(0.f);
+    HeadRaw<F32, W, PAIRS> dy, x;
+    dy.clear();
+    x.clear();
+    for (int64_t tok0 = way.tok0; tok0 < way.end; tok0 += g.tokens) {
+        const int tokens = static_cast<int>(min(static_cast<int64_t>(g.tokens), way.end - tok0));
+        const int rows = way.slot < 0 ? 0 : tokens;
+        int row = way.row, head = way.head;
+        const char* in = static_cast<const char*>(g.in) + ((tok0 + row) * g.in_row + head * g.in_head) * es;
+        const char* from = static_cast<const char*>(g.x) + ((tok0 + row) * g.x_row + head * g.x_head) * es;
+        char* out = static_cast<char*>(g.out) + ((tok0 + row) * g.out_row + head * g.out_head) * es;
+        if (row < rows) {
+            dy.load(at, in);
+            if (norm) x.load(at, from);
         }
-    }
-    for (int64_t tok0 = static_cast<int64_t>(local) * g.tokens; tok0 < p.rows; tok0 += static_cast<int64_t>(g.parts) * g.tokens) {
-        const int tokens = static_cast<int>(min(static_cast<int64_t>(g.tokens), p.rows - tok0));
-        const int items = tokens * g.heads;
-        __syncthreads();  // the table before has been read
-        if (p.rot) head_table<W>(p, tok0, tokens, table);
+        __syncthreads();  // the tables before have been read
+        if (p.rot) head_angles<W, PAIRS>(p, tok0, tokens, tables + p.dim);
         __syncthreads();
-        for (int first = 0; first < items; first += slots) {
-            const int item = first + slot;
-            const int row = item / g.heads, head = item - row * g.heads;
-            const int64_t in = (tok0 + row) * g.in_row + head * g.in_head;
-            const int64_t at_x = (tok0 + row) * g.x_row + head * g.x_head;
-            RowVec<F32, W> ya[V], yb[V], xa[V], xb[V];
+        for (int left = way.rounds(g, tokens); left > 0; --left) {
+            HeadPairs t, h;
+            dy.get(t);
+            x.get(h);
+            const bool live = row < rows;
+            const float* angles = tables + (row + 1) * p.dim;
+            char* to = out;
+            row += g.rows_on;
+            head += g.heads_on;
+            in += g.in_step;
+            from += g.x_step;
+            out += g.out_step;
+            if (head >= g.heads) head -= g.heads, ++row, in += g.in_wrap, from += g.x_wrap, out += g.out_wrap;
+            if (row < rows) {
+                dy.load(at, in);
+                if (norm) x.load(at, from);
+            }
+            if (p.rot && live) head_turn<W, PAIRS, true>(p, at, angles, t);
+            if (norm) {
+                float2 s1 = both2(0.f), s2 = both2(0.f);
+                HeadPairs u;
+                head_planes(at, tables, p.dim, u);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const HeadPlace<W> at(p, lane + v * p.lanes);
-                ya[v].clear(); yb[v].clear(); xa[v].clear(); xb[v].clear();
-                if (item < items && at.live) {
-                    ya[v].load(g.in, in + at.a);
-                    yb[v].load(g.in, in + at.b);
-                    if (g.gamma) {
-                        xa[v].load(g.x, at_x + at.a);
-                        xb[v].load(g.x, at_x + at.b);
+                for (int j = 0; j < 4; ++j) {
+                    u.a[j] = mul2(t.a[j], u.a[j]);
+                    u.b[j] = mul2(t.b[j], u.b[j]);
+                    s1 = fma2(h.a[j], h.a[j], fma2(h.b[j], h.b[j], s1));
+                    s2 = fma2(u.a[j], h.a[j], fma2(u.b[j], h.b[j], s2));
+                }
+                const float sq = head_sum(s1.x + s1.y, way.lane, p.lanes), dot = head_sum(s2.x + s2.y, way.lane, p.lanes);
+                const float r = head_rstd(sq, inv_dim, p.eps);
+                const float2 back = both2(-r * (r * dot * inv_dim)), r2 = both2(r);
+                if (live) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        h.a[j] = mul2(h.a[j], r2);
+                        h.b[j] = mul2(h.b[j], r2);
+                        dg.a[j] = fma2(t.a[j], h.a[j], dg.a[j]);
+                        dg.b[j] = fma2(t.b[j], h.b[j], dg.b[j]);
+                        t.a[j] = fma2(h.a[j], back, mul2(u.a[j], r2));
+                        t.b[j] = fma2(h.b[j], back, mul2(u.b[j], r2));
                     }
                 }
             }
-            float ta[V][W], tb[V][W], s1 = 0.f, s2 = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const HeadPlace<W> at(p, lane + v * p.lanes);
-                ya[v].get(ta[v]);
-                yb[v].get(tb[v]);
-                if (item < items && at.live) head_turn<W, true>(p, at, table + row * (p.rot / 2), ta[v], tb[v]);
-                float x[W], z[W];
-                xa[v].get(x);
-                xb[v].get(z);
-#pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    s1 = fmaf(x[e], x[e], fmaf(z[e], z[e], s1));
-                    s2 = fmaf(ta[v][e] * ga[v][e], x[e], fmaf(tb[v][e] * gb[v][e], z[e], s2));
-                }
-            }
-            if (g.gamma) {
-                for (int o = p.lanes >> 1; o; o >>= 1) {
-                    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-                    s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-                }
-                const float r = inv_root(s1, dim, p.eps);
-                const float back = -r * (r * s2 / dim);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float x[W], z[W];
-                    xa[v].get(x);
-                    xb[v].get(z);
-#pragma unroll
-                    for (int e = 0; e < W; ++e) {
-                        const float hx = x[e] * r, hz = z[e] * r;
-                        if (item < items) {
-                            da[v][e] = fmaf(ta[v][e], hx, da[v][e]);
-                            db[v][e] = fmaf(tb[v][e], hz, db[v][e]);
-                        }
-                        ta[v][e] = fmaf(hx, back, ta[v][e] * ga[v][e] * r);
-                        tb[v][e] = fmaf(hz, back, tb[v][e] * gb[v][e] * r);
-                    }
-                }
-            }
-            if (item >= items) continue;
-            const int64_t out = (tok0 + row) * g.out_row + head * g.out_head;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const HeadPlace<W> at(p, lane + v * p.lanes);
-                if (!at.live) continue;
-                RowVec<F32, W>::put(g.out, out + at.a, ta[v]);
-                RowVec<F32, W>::put(g.out, out + at.b, tb[v]);
-            }
+            if (live) HeadRaw<F32, W, PAIRS>::put(at, to, t);
         }
     }
     if (!g.partials) return;
-    // lanes of a warp that hold the same elements, then the warps in order
-    float* part = reinterpret_cast<float*>(table);  // [warps][dim]
+    // [slots][dim] in the tables' place, then the slots in order
     __syncthreads();
+    if (way.slot >= 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const HeadPlace<W> at(p, lane + v * p.lanes);
+        for (int k = 0; k < 8 / W; ++k)
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            float x = da[v][e], y = db[v][e];
-            for (int o = 16; o >= p.lanes; o >>= 1) {
-                x += __shfl_xor_sync(0xffffffffu, x, o);
-                y += __shfl_xor_sync(0xffffffffu, y, o);
+            for (int e = 0; e < W; ++e) {
+                const int j = (k * W + e) / 2;
+                if (!at.live(k)) continue;
+                tables[way.slot * p.dim + at.first(k, e)] = (k * W + e) & 1 ? dg.a[j].y : dg.a[j].x;
+                tables[way.slot * p.dim + at.second(k, e)] = (k * W + e) & 1 ? dg.b[j].y : dg.b[j].x;
             }
-            if (static_cast<int>(threadIdx.x & 31) < p.lanes && at.live) {
-                part[(threadIdx.x >> 5) * p.dim + at.a + e] = x;
-                part[(threadIdx.x >> 5) * p.dim + at.b + e] = y;
-            }
-        }
     }
     __syncthreads();
     for (int c = threadIdx.x; c < p.dim; c += kHeadThreads) {
         float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kHeadThreads / 32; ++w) s += part[w * p.dim + c];
-        g.partials[static_cast<int64_t>(local) * p.dim + c] = s;
+#pragma unroll 8
+        for (int w = 0; w < g.slots; ++w) s += tables[w * p.dim + c];
+        g.partials[static_cast<int64_t>(static_cast<int>(blockIdx.x) - g.cta0) * p.dim + c] = s;
     }
 }
 
@@ -798,7 +958,7 @@ __global__ void __launch_bounds__(1024) head_dgamma_kernel(const __grid_constant
     float s = 0.f;
     if (col < p.dim && g.partials)
 #pragma unroll 10
-        for (int k = k0; k < g.parts; k += 32) s += g.partials[static_cast<int64_t>(k) * p.dim + col];
+        for (int k = k0; k < g.ranges; k += 32) s += g.partials[static_cast<int64_t>(k) * p.dim + col];
     red[k0][c] = s;
     __syncthreads();
     if (k0 == 0 && col < p.dim) {
@@ -874,21 +1034,16 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
     return launch_early(dgamma_kernel, a.d / 32, 1024, 0, st, a.partials, parts, a.d, a.accumulate, a.dgamma);
 }
 
-// Lanes per head: the fewest that hold it with V vector pairs each, a power of two.
-int head_lanes(int dim, int width, int v) {
-    const int pairs = dim / (2 * width);
-    int lanes = 1;
-    while (lanes * v < pairs) lanes *= 2;
-    return lanes;
-}
+// Lanes per head, 16 elements each, and heads in a CTA's round.
+int head_lanes(int dim) { return (dim + 15) / 16; }
+int head_slots(int lanes) { return kHeadThreads / 32 * (32 / lanes); }
 
 // Rows per step: enough heads for kHeadRounds rounds of a CTA's slots, up to as many
-// again where that wastes fewer slots in the last round, within the table's bytes.
+// again where that wastes fewer slots in the last round, within the tables' bytes.
 constexpr int kHeadRounds = 4;
-constexpr int kHeadTable = 32 * 1024;
-int head_tokens(int heads, int lanes, int rot) {
-    const int slots = kHeadThreads / lanes;
-    const int most = rot ? std::max(1, kHeadTable / (rot * 4)) : 1024;
+constexpr int kHeadTables = 32 * 1024;
+int head_tokens(int heads, int slots, int dim, int rot) {
+    const int most = rot ? std::max(1, kHeadTables / (dim * 4)) : 1024;
     const int least = std::min(most, std::max(1, kHeadRounds * slots / heads));
     int best = least;
     double use = 0;
@@ -900,58 +1055,72 @@ int head_tokens(int heads, int lanes, int rot) {
     return best;
 }
 
-template <bool F32, int W, int V, int U>
-cudaError_t run_heads(HeadArgs& a, cudaStream_t st) {
-    a.lanes = head_lanes(a.dim, W, V);
-    const int slots = kHeadThreads / a.lanes;
-    const int64_t sms = device_sm_count();
-    int64_t ctas = 0;
-    size_t smem = 0;
-    for (int i = 0; i < a.n; ++i) {
-        HeadGroup& g = a.g[i];
-        g.tokens = head_tokens(g.heads, a.lanes, a.rot);
-        // few rows: fewer per step, then a step's heads over several CTAs, until each SM has one
-        while (g.tokens > 1 && (a.rows + g.tokens - 1) / g.tokens < 2 * sms) g.tokens = (g.tokens + 1) / 2;
-        const int64_t steps = (a.rows + g.tokens - 1) / g.tokens;
-        const int rounds = (g.tokens * g.heads + slots - 1) / slots;
-        g.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rounds, 2 * sms / steps)));
-        g.cta0 = static_cast<int32_t>(ctas);
-        ctas += steps * g.parts;
-        smem = std::max(smem, static_cast<size_t>(g.tokens) * a.rot * 4);
-    }
-    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-    note_launch();
-    return launch_early(head_kernel<F32, W, V, U>, static_cast<unsigned>(ctas), kHeadThreads, static_cast<int>(smem), st, a);
+// A group's CTAs and strides: `ctas` of them, fewer where there are fewer rows; with a
+// CTA per row and more CTAs than that (split), a row's heads over several.  Returns the
+// table's rows.
+int plan_group(HeadArgs& a, HeadGroup& g, int64_t ctas, int64_t es, bool split, int64_t* used) {
+    g.slots = head_slots(a.lanes);
+    g.ranges = static_cast<int32_t>(std::min<int64_t>(a.rows, ctas));
+    const int64_t rows = (a.rows + g.ranges - 1) / g.ranges;  // of a range
+    g.tokens = static_cast<int32_t>(std::min<int64_t>(rows, head_tokens(g.heads, g.slots, a.dim, a.rot)));
+    const int rounds = (g.tokens * g.heads + g.slots - 1) / g.slots;
+    g.split = split ? static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(rounds, ctas / g.ranges))) : 1;
+    g.stride = g.slots * g.split;
+    g.rows_on = g.stride / g.heads;
+    g.heads_on = g.stride - g.rows_on * g.heads;
+    const auto steps = [&](int64_t row, int64_t head, int64_t* step, int64_t* wrap) {
+        *step = (g.rows_on * row + g.heads_on * head) * es;
+        *wrap = (row - g.heads * head) * es;
+    };
+    steps(g.in_row, g.in_head, &g.in_step, &g.in_wrap);
+    steps(g.x_row, g.x_head, &g.x_step, &g.x_wrap);
+    steps(g.out_row, g.out_head, &g.out_step, &g.out_wrap);
+    g.cta0 = static_cast<int32_t>(*used);
+    *used += static_cast<int64_t>(g.ranges) * g.split;
+    return a.rot ? g.tokens : 0;
 }
 
-template <bool F32, int W, int V>
-cudaError_t run_heads_grad(HeadArgs& a, cudaStream_t st) {
-    a.lanes = head_lanes(a.dim, W, V);
+template <bool F32, int W, bool PAIRS>
+cudaError_t run_heads(HeadArgs& a, cudaStream_t st) {
+    a.lanes = head_lanes(a.dim);
     int64_t ctas = 0;
-    size_t smem = static_cast<size_t>(kHeadThreads / 32) * a.dim * 4;
-    int wanted = 0, all = 0;
+    int all = 0, table = 0;
+    for (int i = 0; i < a.n; ++i) all += a.g[i].heads;
+    // as many as are resident, by heads
+    const int64_t most = static_cast<int64_t>(W < 4 ? 2 : F32 ? 3 : 4) * device_sm_count();
+    for (int i = 0; i < a.n; ++i)
+        table = std::max(table, plan_group(a, a.g[i], std::max<int64_t>(1, most * a.g[i].heads / all), F32 ? 4 : 2, true, &ctas));
+    const int smem = (table + 1) * a.dim * 4;
+    note_launch();
+    return launch_early(head_kernel<F32, W, PAIRS>, static_cast<unsigned>(ctas), kHeadThreads, smem, st, a);
+}
+
+template <bool F32, int W, bool PAIRS>
+cudaError_t run_heads_grad(HeadArgs& a, cudaStream_t st) {
+    a.lanes = head_lanes(a.dim);
+    int64_t ctas = 0;
+    int wanted = 0, all = 0, table = 0;
     for (int i = 0; i < a.n; ++i) all += a.g[i].heads;
     for (int i = 0; i < a.n; ++i) {
         HeadGroup& g = a.g[i];
         g.cta0 = static_cast<int32_t>(ctas);
         wanted += g.dgamma != nullptr;
-        if (!g.heads || !a.rows) continue;  // an empty sum: parts = 0
-        g.parts = head_grad_parts(a.rows, g.heads, all);
-        g.tokens = head_tokens(g.heads, a.lanes, a.rot);
-        while (g.tokens > 1 && (a.rows + g.tokens - 1) / g.tokens < g.parts) g.tokens = (g.tokens + 1) / 2;
-        ctas += g.parts;
-        smem = std::max(smem, static_cast<size_t>(g.tokens) * a.rot * 4);
+        if (!g.heads || !a.rows) continue;  // an empty sum: no ranges
+        table = std::max(table, plan_group(a, g, head_grad_parts(a.rows, g.heads, all), F32 ? 4 : 2, false, &ctas));
     }
+    const int smem = std::max(table + 1, head_slots(a.lanes)) * a.dim * 4;
     if (ctas) {
         note_launch();
-        const cudaError_t e = launch_early(head_grad_kernel<F32, W, V>, static_cast<unsigned>(ctas), kHeadThreads,
-                                           static_cast<int>(smem), st, a);
+        const cudaError_t e = launch_early(head_grad_kernel<F32, W, PAIRS>, static_cast<unsigned>(ctas), kHeadThreads, smem, st, a);
         if (e != cudaSuccess || !wanted) return e;
     }
     if (!wanted) return cudaSuccess;
     note_launch();
     return launch_early(head_dgamma_kernel, dim3((a.dim + 31) / 32, a.n), 1024, 0, st, a);
 }
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 }  // namespace
 
@@ -976,21 +1145,21 @@ int head_grad_parts(int64_t rows, int heads, int all_heads) {
 }
 
 cudaError_t launch_heads(HeadArgs a, int f32, cudaStream_t st) {
-    switch (a.width) {
-        case 8: return f32 ? run_heads<true, 8, 1, 1>(a, st) : run_heads<false, 8, 1, 2>(a, st);
-        case 4: return f32 ? run_heads<true, 4, 2, 1>(a, st) : run_heads<false, 4, 2, 1>(a, st);
-        case 2: return f32 ? run_heads<true, 2, 4, 1>(a, st) : run_heads<false, 2, 4, 1>(a, st);
-        default: return f32 ? run_heads<true, 1, 8, 1>(a, st) : run_heads<false, 1, 8, 1>(a, st);
-    }
+    const auto with = [&](auto width) {
+        constexpr int W = decltype(width)::value;
+        if (a.pairs) return f32 ? run_heads<true, W, true>(a, st) : run_heads<false, W, true>(a, st);
+        return f32 ? run_heads<true, W, false>(a, st) : run_heads<false, W, false>(a, st);
+    };
+    return a.width == 8 ? with(Int<8>{}) : a.width == 4 ? with(Int<4>{}) : a.width == 2 ? with(Int<2>{}) : with(Int<1>{});
 }
 
 cudaError_t launch_heads_grad(HeadArgs a, int f32, cudaStream_t st) {
-    switch (a.width) {
-        case 8: return f32 ? run_heads_grad<true, 8, 1>(a, st) : run_heads_grad<false, 8, 1>(a, st);
-        case 4: return f32 ? run_heads_grad<true, 4, 2>(a, st) : run_heads_grad<false, 4, 2>(a, st);
-        case 2: return f32 ? run_heads_grad<true, 2, 4>(a, st) : run_heads_grad<false, 2, 4>(a, st);
-        default: return f32 ? run_heads_grad<true, 1, 8>(a, st) : run_heads_grad<false, 1, 8>(a, st);
-    }
+    const auto with = [&](auto width) {
+        constexpr int W = decltype(width)::value;
+        if (a.pairs) return f32 ? run_heads_grad<true, W, true>(a, st) : run_heads_grad<false, W, true>(a, st);
+        return f32 ? run_heads_grad<true, W, false>(a, st) : run_heads_grad<false, W, false>(a, st);
+    };
+    return a.width == 8 ? with(Int<8>{}) : a.width == 4 ? with(Int<4>{}) : a.width == 2 ? with(Int<2>{}) : with(Int<1>{});
 }
 
 int rmsnorm_grad_parts(int64_t rows, int64_t d) {

@@ -148,9 +148,14 @@ struct HeadGroup {
     float* partials;     // gradient: [CTAs of the group][dim], or nullptr
     float* dgamma;
     int32_t heads, accumulate;
-    int32_t cta0;        // its first CTA (from here on set by the launchers)
-    int32_t tokens;      // rows per step of a CTA
-    int32_t parts;       // forward: CTAs that share a step's heads; gradient: CTAs
+    // set by the launchers:
+    int32_t cta0;        // its first CTA
+    int32_t ranges;      // CTAs that the rows are dealt to (and partial rows of dgamma)
+    int32_t split;       // CTAs that share a range's steps
+    int32_t tokens;      // rows per step
+    int32_t slots, stride;       // heads in a CTA's round, and of all CTAs that share a step
+    int32_t rows_on, heads_on;   // stride heads on from a (row, head),
+    int64_t in_step, in_wrap, x_step, x_wrap, out_step, out_wrap;  // in bytes; wrap: where the head passes the row's last
 };
 struct HeadArgs {
     HeadGroup g[kHeadGroups];
@@ -162,6 +167,7 @@ struct HeadArgs {
     int32_t rot, pairs;  // rotated elements; adjacent pairs instead of halves
     int32_t width;       // elements per vector: 8, 4, 2 or 1
     int32_t lanes;       // of a head (set by the launchers)
+    int32_t pad;
 };
 // Elements per vector for which every head can be read and written in whole vectors.
 int head_width(const HeadArgs& a, int64_t es);

@@ -1,4 +1,4 @@
-// W neighbouring elements of a bf16 or fp32 row as raw 32-bit words: loaded and
+// Arithmetic on two floats at a time (f32x2), and W neighbouring elements of a bf16 or fp32 row as raw 32-bit words: loaded and
 // stored in the widest pieces, up to 16 bytes, that W elements make.
 #pragma once
 
@@ -8,6 +8,29 @@
 #include <cuda_runtime.h>
 
 namespace hm {
+
+__device__ __forceinline__ uint64_t pack2(float2 v) {
+    return static_cast<uint64_t>(__float_as_uint(v.x)) | (static_cast<uint64_t>(__float_as_uint(v.y)) << 32);
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+    return unpack2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+    return unpack2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
+    return unpack2(r);
+}
+__device__ __forceinline__ float2 both2(float v) { return make_float2(v, v); }
 
 template <bool F32, int W>
 struct RowVec {
