@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* partials, int
 // per element where memory leaves time for 21 (8192 x 80 heads of 128 bf16: 100 us).
 // ---------------------------------------------------------------------------
 constexpr int kHeadThreads = 256;
+constexpr int kHeadSmem = 113 * 1024;  // at most: two CTAs per SM
 
 // A thread's 8 first and 8 second elements of pairs.
 struct HeadPairs {
@@ -596,6 +597,91 @@ struct HeadRaw {
     }
 };
 
+// A thread's parts of the heads it is going to work on, on their way into its own place
+// in shared memory (asynchronous copies; a thread waits for its own): D of them under
+// way and one that is read.  With one in registers instead, 32 KB under way on an SM,
+// 8192 x 80 heads of 128 bf16 took 61.5 us, and the gradient 109.  Vectors
+// of 2 bytes, which such copies do not take, go through registers.
+template <bool F32, int W, bool PAIRS, int D>
+struct HeadRing {
+    static constexpr int kVec = W * (F32 ? 4 : 2), kPiece = kVec < 16 ? kVec : 16, V = 8 / W, kPieces = kVec / kPiece;
+    static constexpr bool kAsync = kVec >= 4;
+    static constexpr int kStages = kAsync ? D + 1 : 0, kAhead = kAsync ? D : 1;
+    static constexpr int kStageBytes = 2 * V * kVec * kHeadThreads;
+    static constexpr int kBytes = kStages * kStageBytes;
+    HeadRaw<F32, W, PAIRS> held;  // registers only
+    uint32_t put_at, get_at, begin, end;
+
+    __device__ __forceinline__ HeadRing(char* smem) {
+        held.clear();
+        begin = smem_u32(smem) + threadIdx.x * kPiece;
+        end = begin + kBytes;
+        put_at = get_at = begin;
+    }
+    static __device__ __forceinline__ void copy(uint32_t to, const char* from) {
+        if constexpr (kPiece == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(kPiece < 4 ? 4 : kPiece) : "memory");
+    }
+    // the next head, if it is `there`
+    __device__ __forceinline__ void put(const HeadPlace<W, PAIRS>& at, const char* head, bool there) {
+        if constexpr (!kAsync) {
+            if (there) held.load(at, head);
+        } else {
+            if (there) {
+                constexpr int es = F32 ? 4 : 2;
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    if (!at.live(k)) continue;
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        copy(put_at + ((2 * k) * kPieces + i) * kPiece * kHeadThreads, head + at.a[k] * es + i * kPiece);
+                        copy(put_at + ((2 * k + 1) * kPieces + i) * kPiece * kHeadThreads, head + at.b[k] * es + i * kPiece);
+                    }
+                }
+            }
+            put_at += kStageBytes;
+            if (put_at == end) put_at = begin;
+        }
+    }
+    __device__ __forceinline__ void get(const HeadPlace<W, PAIRS>& at, HeadRaw<F32, W, PAIRS>& x) {
+        if constexpr (!kAsync) {
+            x = held;
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                if (!at.live(k)) {  // nothing was copied there
+                    x.a[k].clear();
+                    x.b[k].clear();
+                    continue;
+                }
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    piece(get_at + ((2 * k) * kPieces + i) * kPiece * kHeadThreads, x.a[k].w + i * (kPiece / 4));
+                    piece(get_at + ((2 * k + 1) * kPieces + i) * kPiece * kHeadThreads, x.b[k].w + i * (kPiece / 4));
+                }
+            }
+            get_at += kStageBytes;
+            if (get_at == end) get_at = begin;
+        }
+    }
+    static __device__ __forceinline__ void piece(uint32_t from, uint32_t* w) {
+        if constexpr (kPiece == 16)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from) : "memory");
+        else if constexpr (kPiece == 8)
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(from) : "memory");
+        else asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(from) : "memory");
+    }
+};
+// One head of each ring is a group of copies; the oldest one's have arrived once no more
+// than the ones ahead of it are under way.
+__device__ __forceinline__ void head_copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void head_copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+template <bool F32>
+constexpr int kHeadAhead = F32 ? 2 : 3;
+template <bool F32>
+constexpr int kHeadGradAhead = F32 ? 1 : 3;  // of each of its two rings
+
 // Tables in shared memory hold two values for each pair of a head, dim floats: all
 // first ones, then all second ones; each in planes of M pairs of every vector pair, so
 // that neighbouring lanes read neighbouring M floats.
@@ -651,12 +737,12 @@ __device__ __forceinline__ void sincos_eighth(float y, float& s, float& c) {
     c = fmaf(v, z, 1.f);
 }
 
-// cos and sin of `tokens` rows from tok0, scaled (1 and 0 past the rotated part): a
-// table of dim floats for each.
+// cos and sin of `tokens` rows' positions, scaled (1 and 0 past the rotated part): a
+// table of dim floats for each, the first one's at `place` of `places` in a circle.
 template <int W, bool PAIRS>
-__device__ __forceinline__ void head_angles(const HeadArgs& p, int64_t tok0, int tokens, float* tables) {
+__device__ __forceinline__ void head_angles(const HeadArgs& p, const int64_t* positions, int tokens, float* tables, int place, int places) {
     const int half = p.dim / 2, pairs = p.rot / 2, turned = p.rot / (2 * W), all = p.dim / (2 * W);
-    int t = threadIdx.x / half, c = threadIdx.x - t * half;  // pair c of row tok0 + t
+    int t = threadIdx.x / half, c = threadIdx.x - t * half;  // pair c of row t
     const int t_on = kHeadThreads / half, c_on = kHeadThreads - t_on * half;
     while (t < tokens) {
         float cs = 1.f, sn = 0.f;
@@ -668,7 +754,7 @@ __device__ __forceinline__ void head_angles(const HeadArgs& p, int64_t tok0, int
                 v = vec < turned ? vec : vec - turned;
                 e = vec < turned ? in : P + in;
             }
-            const uint64_t turn = static_cast<uint64_t>(p.positions[tok0 + t]) * p.turns[c];
+            const uint64_t turn = static_cast<uint64_t>(positions[t]) * p.turns[c];
             const uint32_t hi = static_cast<uint32_t>(turn >> 32);
             const uint32_t quarter = (hi + 0x20000000u) >> 30;
             const int32_t rest = static_cast<int32_t>(hi - (quarter << 30));  // an eighth of a turn at most
@@ -678,7 +764,8 @@ __device__ __forceinline__ void head_angles(const HeadArgs& p, int64_t tok0, int
             cs = ((quarter + 1) & 2 ? -cq : cq) * p.scale;
             sn = (quarter & 2 ? -sq : sq) * p.scale;
         }
-        float* to = tables + t * p.dim + head_plane<W>(v, e, all);
+        const int at = place + t;
+        float* to = tables + (at < places ? at : at - places) * p.dim + head_plane<W>(v, e, all);
         to[0] = cs;
         to[half] = sn;
         t += t_on;
@@ -708,7 +795,8 @@ __device__ __forceinline__ void head_turn(const HeadArgs& p, const HeadPlace<W, 
     }
 }
 
-// gamma as a table, written by the CTA's first head's lanes.  (In registers it cost 16
+// gamma as a table, copied by the CTA's first head's lanes (asynchronously: in the group
+// of the first head's copies).  (In registers it cost 16
 // of them, and a CTA per SM.)
 template <int W, bool PAIRS>
 __device__ __forceinline__ void head_gamma(const HeadPlace<W, PAIRS>& at, const float* gamma, int dim, float* table) {
@@ -716,9 +804,9 @@ __device__ __forceinline__ void head_gamma(const HeadPlace<W, PAIRS>& at, const 
     for (int k = 0; k < 8 / W; ++k)
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-            float* to = table + head_plane<W>(at.v[k], e, at.all);
-            to[0] = gamma[at.first(k, e)];
-            to[dim / 2] = gamma[at.second(k, e)];
+            const uint32_t to = smem_u32(table + head_plane<W>(at.v[k], e, at.all));
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(gamma + at.first(k, e)) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + dim * 2), "l"(gamma + at.second(k, e)) : "memory");
         }
 }
 
@@ -751,23 +839,17 @@ __device__ __forceinline__ float head_rstd(float sum, float inv_dim, float eps) 
     return a > 1e-35f && a < 1e35f ? fmaf(0.5f * y, e, y) : y;
 }
 
-__device__ __forceinline__ int head_group(const HeadArgs& p) {
-    int g = 0;
-    while (g + 1 < p.n && static_cast<int>(blockIdx.x) >= p.g[g + 1].cta0) ++g;
-    return g;
-}
-
-// This thread's way through its CTA's rows: a range of them, in steps of `tokens`, in
-// each of which it takes every stride-th (row, head).  All strides are the host's.
+// This thread's way through its CTA's rows: a range of them, of whose (row, head) items
+// it takes every stride-th.  All strides are the host's.
 struct HeadWay {
     int lane;          // of its head
     int slot;          // which head of the CTA's round; -1: a lane that is left over
-    int row, head;     // its first item of a step
-    int part;          // of the CTAs that share a step
-    int64_t tok0, end;
+    int row, head;     // its first item, the row counted from tok0
+    int rows;          // of the range
+    int64_t tok0;
+    int64_t rounds;    // that all threads of the CTA make
     __device__ __forceinline__ HeadWay(const HeadArgs& p, const HeadGroup& g) {
-        const int local = static_cast<int>(blockIdx.x) - g.cta0, range = local / g.split;
-        part = local - range * g.split;
+        const int local = static_cast<int>(blockIdx.x) - g.cta0, range = local / g.split, part = local - range * g.split;
         const int per_warp = 32 / p.lanes, in_warp = (threadIdx.x & 31) / p.lanes;
         lane = (threadIdx.x & 31) - in_warp * p.lanes;
         slot = in_warp < per_warp ? (threadIdx.x >> 5) * per_warp + in_warp : -1;
@@ -775,51 +857,96 @@ struct HeadWay {
         row = item / g.heads;
         head = item - row * g.heads;
         tok0 = p.rows * range / g.ranges;
-        end = p.rows * (range + 1) / g.ranges;
+        rows = static_cast<int>(p.rows * (range + 1) / g.ranges - tok0);
+        rounds = max(static_cast<int64_t>(0), (static_cast<int64_t>(rows) * g.heads - part * g.slots + g.stride - 1) / g.stride);
     }
-    // rounds that all threads of the CTA make in a step
-    __device__ __forceinline__ int rounds(const HeadGroup& g, int tokens) const {
-        return (tokens * g.heads - part * g.slots + g.stride - 1) / g.stride;
+};
+// The range's positions, in shared memory where they are few enough (copied with the
+// first head): read from memory at every step, they held up a CTA of 8 heads, whose
+// steps are short (16384 rows of 32 + 8 heads bf16: gradient 114 us).
+constexpr int kHeadPositions = 1024;
+__device__ __forceinline__ const int64_t* head_positions(const HeadArgs& p, const HeadWay& way, float* smem) {
+    const int64_t* from = p.positions + way.tok0;
+    if (!p.rot || way.rows > kHeadPositions) return from;
+    for (int i = threadIdx.x; i < way.rows; i += kHeadThreads)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem) + 8 * i), "l"(from + i) : "memory");
+    return reinterpret_cast<const int64_t*>(smem);
+}
+
+// Rows that the rounds up to a step's end reach: the angles of those of the next step are
+// made while this one's are read, in a circle of g.places tables.
+struct HeadReach {
+    int rows, rest, place;  // whole rows and heads of one more; where the next row's table goes
+    __device__ __forceinline__ HeadReach() : rows(0), rest(0), place(0) {}
+    template <int W, bool PAIRS>
+    __device__ __forceinline__ void step(const HeadArgs& p, const HeadGroup& g, const HeadWay& way, const int64_t* positions, float* tables) {
+        const int before = min(way.rows, rows + (rest > 0));
+        rows += g.step_rows;
+        rest += g.step_heads;
+        if (rest >= g.heads) rest -= g.heads, ++rows;
+        rows = min(rows, way.rows);  // (stays there: no overflow)
+        const int more = min(way.rows, rows + (rest > 0)) - before;
+        head_angles<W, PAIRS>(p, positions + before, more, tables, place, g.places);
+        place += more;
+        if (place >= g.places) place -= g.places;
     }
 };
 
-// Forward, persistent.  Every round a thread loads its next (row, head) before it works on this one.
-template <bool F32, int W, bool PAIRS>
-__global__ void __launch_bounds__(kHeadThreads, W < 4 ? 2 : F32 ? 3 : 4) head_kernel(const __grid_constant__ HeadArgs p) {
-    extern __shared__ __align__(16) float tables[];  // gamma, then the step's rows
+// Forward, persistent.  The group is known when it is compiled: its strides are then
+// constants of the launch, where an index into the groups loaded 16 words for each head
+// and round.
+template <bool F32, int W, bool PAIRS, int G>
+__device__ __forceinline__ void head_body(const HeadArgs& p) {
+    using Ring = HeadRing<F32, W, PAIRS, kHeadAhead<F32>>;
+    extern __shared__ __align__(16) float smem[];  // the ring, gamma, angles
     constexpr int64_t es = F32 ? 4 : 2;
-    wait_for_earlier_kernels();
-    const HeadGroup& g = p.g[head_group(p)];
+    const HeadGroup& g = p.g[G];
     const HeadWay way(p, g);
     const HeadPlace<W, PAIRS> at(p, way.lane);
+    const int rows = way.slot < 0 ? 0 : way.rows;
+    int row = way.row, head = way.head, row1 = way.row, head1 = way.head;  // 1: of the copies
+    const char* in = static_cast<const char*>(g.in) + ((way.tok0 + row) * g.in_row + head * g.in_head) * es;
+    char* out = static_cast<char*>(g.out) + ((way.tok0 + row) * g.out_row + head * g.out_head) * es;
+    Ring ring(reinterpret_cast<char*>(smem));
+    const auto ahead = [&] {
+        ring.put(at, in, row1 < rows);
+        head_copies_commit();
+        row1 += g.rows_on;
+        head1 += g.heads_on;
+        in += g.in_step;
+        if (head1 >= g.heads) head1 -= g.heads, ++row1, in += g.in_wrap;
+    };
+    float* gammas = smem + Ring::kBytes / 4;
+    float* tables = gammas + (p.dim + 3) / 4 * 4;
+    float* after = tables + (g.places * p.dim + 3) / 4 * 4;
+    const int64_t* positions = head_positions(p, way, after);
     const float inv_dim = 1.f / static_cast<float>(p.dim);
     const bool norm = g.gamma != nullptr;
-    if (norm && way.slot == 0) head_gamma(at, g.gamma, p.dim, tables);
-    HeadRaw<F32, W, PAIRS> next;
-    next.clear();
-    for (int64_t tok0 = way.tok0; tok0 < way.end; tok0 += g.tokens) {
-        const int tokens = static_cast<int>(min(static_cast<int64_t>(g.tokens), way.end - tok0));
-        const int rows = way.slot < 0 ? 0 : tokens;
-        int row = way.row, head = way.head;
-        const char* in = static_cast<const char*>(g.in) + ((tok0 + row) * g.in_row + head * g.in_head) * es;
-        char* out = static_cast<char*>(g.out) + ((tok0 + row) * g.out_row + head * g.out_head) * es;
-        if (row < rows) next.load(at, in);
-        __syncthreads();  // the tables before have been read
-        if (p.rot) head_angles<W, PAIRS>(p, tok0, tokens, tables + p.dim);
-        __syncthreads();
-        // whole warps stay in the loop: a head's sum is over lanes
-        for (int left = way.rounds(g, tokens); left > 0; --left) {
+    if (norm && way.slot == 0) head_gamma(at, g.gamma, p.dim, gammas);
+#pragma unroll
+    for (int d = 0; d < Ring::kAhead; ++d) ahead();
+    head_copies_wait<Ring::kAhead - 1>();  // gamma and the positions
+    __syncthreads();
+    HeadReach reach;
+    if (p.rot) reach.step<W, PAIRS>(p, g, way, positions, tables);
+    int place = row;  // of its row's angles (a first item's row is among the first step's)
+    // whole warps stay in the loops: a head's sum is over lanes
+    for (int64_t left = way.rounds; left > 0; left -= g.rounds) {
+        __syncthreads();  // this step's angles are there, the one's before have been read
+        if (p.rot && left > g.rounds) reach.step<W, PAIRS>(p, g, way, positions, tables);
+        for (int r = static_cast<int>(min(static_cast<int64_t>(g.rounds), left)); r > 0; --r) {
+            HeadRaw<F32, W, PAIRS> raw;
             HeadPairs x;
-            next.get(x);
+            if constexpr (Ring::kAsync) {
+                head_copies_wait<Ring::kAhead - 1>();
+                ahead();
+                ring.get(at, raw);
+            } else {
+                ring.get(at, raw);
+                ahead();
+            }
+            raw.get(x);
             const bool live = row < rows;
-            const float* angles = tables + (row + 1) * p.dim;
-            char* to = out;
-            row += g.rows_on;
-            head += g.heads_on;
-            in += g.in_step;
-            out += g.out_step;
-            if (head >= g.heads) head -= g.heads, ++row, in += g.in_wrap, out += g.out_wrap;
-            if (row < rows) next.load(at, in);
             if (norm) {
                 float2 sq = mul2(x.a[0], x.a[0]);
 #pragma unroll
@@ -827,78 +954,106 @@ __global__ void __launch_bounds__(kHeadThreads, W < 4 ? 2 : F32 ? 3 : 4) head_ke
                     if (j) sq = fma2(x.a[j], x.a[j], sq);
                     sq = fma2(x.b[j], x.b[j], sq);
                 }
-                const float2 r = both2(head_rstd(head_sum(sq.x + sq.y, way.lane, p.lanes), inv_dim, p.eps));
+                const float2 rstd = both2(head_rstd(head_sum(sq.x + sq.y, way.lane, p.lanes), inv_dim, p.eps));
                 HeadPairs gamma;
-                head_planes(at, tables, p.dim, gamma);
+                head_planes(at, gammas, p.dim, gamma);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x.a[j] = mul2(mul2(x.a[j], r), gamma.a[j]);
-                    x.b[j] = mul2(mul2(x.b[j], r), gamma.b[j]);
+                    x.a[j] = mul2(mul2(x.a[j], rstd), gamma.a[j]);
+                    x.b[j] = mul2(mul2(x.b[j], rstd), gamma.b[j]);
                 }
             }
-            if (!live) continue;
-            if (p.rot) head_turn<W, PAIRS, false>(p, at, angles, x);
-            HeadRaw<F32, W, PAIRS>::put(at, to, x);
+            if (live) {
+                if (p.rot) head_turn<W, PAIRS, false>(p, at, tables + place * p.dim, x);
+                HeadRaw<F32, W, PAIRS>::put(at, out, x);
+            }
+            row += g.rows_on;
+            place += g.rows_on;
+            head += g.heads_on;
+            out += g.out_step;
+            if (head >= g.heads) head -= g.heads, ++row, ++place, out += g.out_wrap;
+            if (place >= g.places) place -= g.places;
         }
     }
+}
+
+template <bool F32, int W, bool PAIRS>
+__global__ void __launch_bounds__(kHeadThreads, W < 4 ? 2 : F32 ? 3 : 4) head_kernel(const __grid_constant__ HeadArgs p) {
+    wait_for_earlier_kernels();
+    if (static_cast<int>(blockIdx.x) < p.g[1].cta0) head_body<F32, W, PAIRS, 0>(p);
+    else head_body<F32, W, PAIRS, 1>(p);
 }
 
 // Gradient.  With t = dy turned back, u = t gamma, S1 = sum x^2 and S2 = sum u x, both
 // in the same round of shuffles: dx = r u - x r^3 S2 / dim.  A thread keeps its
 // elements' part of dgamma in registers; the slots' parts are added at the end in order.
-template <bool F32, int W, bool PAIRS>
-__global__ void __launch_bounds__(kHeadThreads, W == 1 ? 1 : 2) head_grad_kernel(const __grid_constant__ HeadArgs p) {
-    extern __shared__ __align__(16) float tables[];
+template <bool F32, int W, bool PAIRS, int G>
+__device__ __forceinline__ void head_grad_body(const HeadArgs& p) {
+    using Ring = HeadRing<F32, W, PAIRS, kHeadGradAhead<F32>>;
+    extern __shared__ __align__(16) float smem[];  // the rings of dy and x, gamma, angles
     constexpr int64_t es = F32 ? 4 : 2;
-    wait_for_earlier_kernels();
-    const HeadGroup& g = p.g[head_group(p)];
+    const HeadGroup& g = p.g[G];
     const HeadWay way(p, g);
     const HeadPlace<W, PAIRS> at(p, way.lane);
-    const float inv_dim = 1.f / static_cast<float>(p.dim);
     const bool norm = g.gamma != nullptr;
-    if (norm && way.slot == 0) head_gamma(at, g.gamma, p.dim, tables);
+    const int rows = way.slot < 0 ? 0 : way.rows;
+    int row = way.row, head = way.head, row1 = way.row, head1 = way.head;  // 1: of the copies
+    const char* in = static_cast<const char*>(g.in) + ((way.tok0 + row) * g.in_row + head * g.in_head) * es;
+    const char* from = static_cast<const char*>(g.x) + ((way.tok0 + row) * g.x_row + head * g.x_head) * es;
+    char* out = static_cast<char*>(g.out) + ((way.tok0 + row) * g.out_row + head * g.out_head) * es;
+    Ring dys(reinterpret_cast<char*>(smem)), xs(reinterpret_cast<char*>(smem) + Ring::kBytes);
+    const auto ahead = [&] {
+        dys.put(at, in, row1 < rows);
+        xs.put(at, from, norm && row1 < rows);
+        head_copies_commit();
+        row1 += g.rows_on;
+        head1 += g.heads_on;
+        in += g.in_step;
+        from += g.x_step;
+        if (head1 >= g.heads) head1 -= g.heads, ++row1, in += g.in_wrap, from += g.x_wrap;
+    };
+    float* gammas = smem + 2 * Ring::kBytes / 4;
+    float* tables = gammas + (p.dim + 3) / 4 * 4;
+    float* after = tables + (g.places * p.dim + 3) / 4 * 4;
+    const int64_t* positions = head_positions(p, way, after);
+    const float inv_dim = 1.f / static_cast<float>(p.dim);
+    if (norm && way.slot == 0) head_gamma(at, g.gamma, p.dim, gammas);
+#pragma unroll
+    for (int d = 0; d < Ring::kAhead; ++d) ahead();
+    head_copies_wait<Ring::kAhead - 1>();  // gamma and the positions
+    __syncthreads();
+    HeadReach reach;
+    if (p.rot) reach.step<W, PAIRS>(p, g, way, positions, tables);
+    int place = row;
     HeadPairs dg;
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg.a[j] = dg.b[j] = both2(0.f);
-    HeadRaw<F32, W, PAIRS> dy, x;
-    dy.clear();
-    x.clear();
-    for (int64_t tok0 = way.tok0; tok0 < way.end; tok0 += g.tokens) {
-        const int tokens = static_cast<int>(min(static_cast<int64_t>(g.tokens), way.end - tok0));
-        const int rows = way.slot < 0 ? 0 : tokens;
-        int row = way.row, head = way.head;
-        const char* in = static_cast<const char*>(g.in) + ((tok0 + row) * g.in_row + head * g.in_head) * es;
-        const char* from = static_cast<const char*>(g.x) + ((tok0 + row) * g.x_row + head * g.x_head) * es;
-        char* out = static_cast<char*>(g.out) + ((tok0 + row) * g.out_row + head * g.out_head) * es;
-        if (row < rows) {
-            dy.load(at, in);
-            if (norm) x.load(at, from);
-        }
-        __syncthreads();  // the tables before have been read
-        if (p.rot) head_angles<W, PAIRS>(p, tok0, tokens, tables + p.dim);
-        __syncthreads();
-        for (int left = way.rounds(g, tokens); left > 0; --left) {
+    for (int64_t left = way.rounds; left > 0; left -= g.rounds) {
+        __syncthreads();  // this step's angles are there, the one's before have been read
+        if (p.rot && left > g.rounds) reach.step<W, PAIRS>(p, g, way, positions, tables);
+        for (int n = static_cast<int>(min(static_cast<int64_t>(g.rounds), left)); n > 0; --n) {
             HeadPairs t, h;
-            dy.get(t);
-            x.get(h);
-            const bool live = row < rows;
-            const float* angles = tables + (row + 1) * p.dim;
-            char* to = out;
-            row += g.rows_on;
-            head += g.heads_on;
-            in += g.in_step;
-            from += g.x_step;
-            out += g.out_step;
-            if (head >= g.heads) head -= g.heads, ++row, in += g.in_wrap, from += g.x_wrap, out += g.out_wrap;
-            if (row < rows) {
-                dy.load(at, in);
-                if (norm) x.load(at, from);
+            {
+                HeadRaw<F32, W, PAIRS> dy, x;
+                if constexpr (Ring::kAsync) {
+                    head_copies_wait<Ring::kAhead - 1>();
+                    ahead();
+                    dys.get(at, dy);
+                    xs.get(at, x);
+                } else {
+                    dys.get(at, dy);
+                    xs.get(at, x);
+                    ahead();
+                }
+                dy.get(t);
+                x.get(h);
             }
-            if (p.rot && live) head_turn<W, PAIRS, true>(p, at, angles, t);
+            const bool live = row < rows;
+            if (p.rot && live) head_turn<W, PAIRS, true>(p, at, tables + place * p.dim, t);
             if (norm) {
                 float2 s1 = both2(0.f), s2 = both2(0.f);
                 HeadPairs u;
-                head_planes(at, tables, p.dim, u);
+                head_planes(at, gammas, p.dim, u);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     u.a[j] = mul2(t.a[j], u.a[j]);
@@ -921,11 +1076,18 @@ __global__ void __launch_bounds__(kHeadThreads, W == 1 ? 1 : 2) head_grad_kernel
                     }
                 }
             }
-            if (live) HeadRaw<F32, W, PAIRS>::put(at, to, t);
+            if (live) HeadRaw<F32, W, PAIRS>::put(at, out, t);
+            row += g.rows_on;
+            place += g.rows_on;
+            head += g.heads_on;
+            out += g.out_step;
+            if (head >= g.heads) head -= g.heads, ++row, ++place, out += g.out_wrap;
+            if (place >= g.places) place -= g.places;
         }
     }
     if (!g.partials) return;
-    // [slots][dim] in the tables' place, then the slots in order
+    // [slots][dim] over all of it, then the slots in order
+    head_copies_wait<0>();
     __syncthreads();
     if (way.slot >= 0) {
 #pragma unroll
@@ -934,17 +1096,24 @@ __global__ void __launch_bounds__(kHeadThreads, W == 1 ? 1 : 2) head_grad_kernel
             for (int e = 0; e < W; ++e) {
                 const int j = (k * W + e) / 2;
                 if (!at.live(k)) continue;
-                tables[way.slot * p.dim + at.first(k, e)] = (k * W + e) & 1 ? dg.a[j].y : dg.a[j].x;
-                tables[way.slot * p.dim + at.second(k, e)] = (k * W + e) & 1 ? dg.b[j].y : dg.b[j].x;
+                smem[way.slot * p.dim + at.first(k, e)] = (k * W + e) & 1 ? dg.a[j].y : dg.a[j].x;
+                smem[way.slot * p.dim + at.second(k, e)] = (k * W + e) & 1 ? dg.b[j].y : dg.b[j].x;
             }
     }
     __syncthreads();
     for (int c = threadIdx.x; c < p.dim; c += kHeadThreads) {
         float s = 0.f;
 #pragma unroll 8
-        for (int w = 0; w < g.slots; ++w) s += tables[w * p.dim + c];
+        for (int w = 0; w < g.slots; ++w) s += smem[w * p.dim + c];
         g.partials[static_cast<int64_t>(static_cast<int>(blockIdx.x) - g.cta0) * p.dim + c] = s;
     }
+}
+
+template <bool F32, int W, bool PAIRS>
+__global__ void __launch_bounds__(kHeadThreads, W == 1 ? 1 : 2) head_grad_kernel(const __grid_constant__ HeadArgs p) {
+    wait_for_earlier_kernels();
+    if (static_cast<int>(blockIdx.x) < p.g[1].cta0) head_grad_body<F32, W, PAIRS, 0>(p);
+    else head_grad_body<F32, W, PAIRS, 1>(p);
 }
 
 // dgamma of every group from its CTAs' partials, as dgamma_kernel does.
@@ -1038,36 +1207,26 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
 int head_lanes(int dim) { return (dim + 15) / 16; }
 int head_slots(int lanes) { return kHeadThreads / 32 * (32 / lanes); }
 
-// Rows per step: enough heads for kHeadRounds rounds of a CTA's slots, up to as many
-// again where that wastes fewer slots in the last round, within the tables' bytes.
-constexpr int kHeadRounds = 4;
-constexpr int kHeadTables = 32 * 1024;
-int head_tokens(int heads, int slots, int dim, int rot) {
-    const int most = rot ? std::max(1, kHeadTables / (dim * 4)) : 1024;
-    const int least = std::min(most, std::max(1, kHeadRounds * slots / heads));
-    int best = least;
-    double use = 0;
-    for (int t = least; t <= std::min(most, 2 * least); ++t) {
-        const int rounds = (t * heads + slots - 1) / slots;
-        const double u = static_cast<double>(t) * heads / (static_cast<double>(rounds) * slots);
-        if (u > use + 1e-9) use = u, best = t;
-    }
-    return best;
-}
-
 // A group's CTAs and strides: `ctas` of them, fewer where there are fewer rows; with a
-// CTA per row and more CTAs than that (split), a row's heads over several.  Returns the
-// table's rows.
+// CTA per row and more CTAs than that (split), a row's heads over several.  A step is
+// kHeadRounds rounds, fewer where the angles of two steps' rows would take more than
+// kHeadTables.  Returns the bytes of gamma, the angles and the positions.
+constexpr int kHeadRounds = 8;
+constexpr int kHeadTables = 18 * 1024;
 int plan_group(HeadArgs& a, HeadGroup& g, int64_t ctas, int64_t es, bool split, int64_t* used) {
     g.slots = head_slots(a.lanes);
     g.ranges = static_cast<int32_t>(std::min<int64_t>(a.rows, ctas));
-    const int64_t rows = (a.rows + g.ranges - 1) / g.ranges;  // of a range
-    g.tokens = static_cast<int32_t>(std::min<int64_t>(rows, head_tokens(g.heads, g.slots, a.dim, a.rot)));
-    const int rounds = (g.tokens * g.heads + g.slots - 1) / g.slots;
+    const int rounds = (g.heads + g.slots - 1) / g.slots;  // of one row
     g.split = split ? static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(rounds, ctas / g.ranges))) : 1;
     g.stride = g.slots * g.split;
     g.rows_on = g.stride / g.heads;
     g.heads_on = g.stride - g.rows_on * g.heads;
+    g.rounds = kHeadRounds;
+    const auto places = [&] { return 2 * ((g.rounds * g.stride + g.heads - 1) / g.heads + 1); };
+    while (g.rounds > 1 && a.rot && places() * a.dim * 4 > kHeadTables) g.rounds /= 2;
+    g.places = places();
+    g.step_rows = g.rounds * g.stride / g.heads;
+    g.step_heads = g.rounds * g.stride - g.step_rows * g.heads;
     const auto steps = [&](int64_t row, int64_t head, int64_t* step, int64_t* wrap) {
         *step = (g.rows_on * row + g.heads_on * head) * es;
         *wrap = (row - g.heads * head) * es;
@@ -1077,20 +1236,24 @@ int plan_group(HeadArgs& a, HeadGroup& g, int64_t ctas, int64_t es, bool split, 
     steps(g.out_row, g.out_head, &g.out_step, &g.out_wrap);
     g.cta0 = static_cast<int32_t>(*used);
     *used += static_cast<int64_t>(g.ranges) * g.split;
-    return a.rot ? g.tokens : 0;
+    const int64_t rows = (a.rows + g.ranges - 1) / g.ranges;
+    return 4 * ((a.dim + 3) / 4 * 4 + (a.rot ? (g.places * a.dim + 3) / 4 * 4 : 0)) + (a.rot && rows <= kHeadPositions ? static_cast<int>(rows) * 8 : 0);
 }
 
 template <bool F32, int W, bool PAIRS>
 cudaError_t run_heads(HeadArgs& a, cudaStream_t st) {
     a.lanes = head_lanes(a.dim);
     int64_t ctas = 0;
-    int all = 0, table = 0;
-    for (int i = 0; i < a.n; ++i) all += a.g[i].heads;
+    int smem = 0;
     // as many as are resident, by heads
     const int64_t most = static_cast<int64_t>(W < 4 ? 2 : F32 ? 3 : 4) * device_sm_count();
     for (int i = 0; i < a.n; ++i)
-        table = std::max(table, plan_group(a, a.g[i], std::max<int64_t>(1, most * a.g[i].heads / all), F32 ? 4 : 2, true, &ctas));
-    const int smem = (table + 1) * a.dim * 4;
+        smem = std::max(smem, plan_group(a, a.g[i], std::max<int64_t>(1, most * a.g[i].heads / a.all_heads), F32 ? 4 : 2, true, &ctas));
+    if (a.n == 1) a.g[1].cta0 = INT32_MAX;
+    smem += HeadRing<F32, W, PAIRS, kHeadAhead<F32>>::kBytes;
+    static PerDevice done;
+    const cudaError_t e = allow_smem(head_kernel<F32, W, PAIRS>, kHeadSmem, done);
+    if (e != cudaSuccess) return e;
     note_launch();
     return launch_early(head_kernel<F32, W, PAIRS>, static_cast<unsigned>(ctas), kHeadThreads, smem, st, a);
 }
@@ -1099,19 +1262,22 @@ template <bool F32, int W, bool PAIRS>
 cudaError_t run_heads_grad(HeadArgs& a, cudaStream_t st) {
     a.lanes = head_lanes(a.dim);
     int64_t ctas = 0;
-    int wanted = 0, all = 0, table = 0;
-    for (int i = 0; i < a.n; ++i) all += a.g[i].heads;
+    int wanted = 0, smem = 0;
     for (int i = 0; i < a.n; ++i) {
         HeadGroup& g = a.g[i];
         g.cta0 = static_cast<int32_t>(ctas);
         wanted += g.dgamma != nullptr;
         if (!g.heads || !a.rows) continue;  // an empty sum: no ranges
-        table = std::max(table, plan_group(a, g, head_grad_parts(a.rows, g.heads, all), F32 ? 4 : 2, false, &ctas));
+        smem = std::max(smem, plan_group(a, g, head_grad_parts(a.rows, g.heads, a.all_heads), F32 ? 4 : 2, false, &ctas));
     }
-    const int smem = std::max(table + 1, head_slots(a.lanes)) * a.dim * 4;
+    if (a.n == 1) a.g[1].cta0 = INT32_MAX;
+    smem = std::max(smem + 2 * HeadRing<F32, W, PAIRS, kHeadGradAhead<F32>>::kBytes, head_slots(a.lanes) * a.dim * 4);
     if (ctas) {
+        static PerDevice done;
+        cudaError_t e = allow_smem(head_grad_kernel<F32, W, PAIRS>, kHeadSmem, done);
+        if (e != cudaSuccess) return e;
         note_launch();
-        const cudaError_t e = launch_early(head_grad_kernel<F32, W, PAIRS>, static_cast<unsigned>(ctas), kHeadThreads, smem, st, a);
+        e = launch_early(head_grad_kernel<F32, W, PAIRS>, static_cast<unsigned>(ctas), kHeadThreads, smem, st, a);
         if (e != cudaSuccess || !wanted) return e;
     }
     if (!wanted) return cudaSuccess;
@@ -1125,9 +1291,9 @@ using Int = std::integral_constant<int, N>;
 }  // namespace
 
 int head_width(const HeadArgs& a, int64_t es) {
-    for (int w = 8; w > 1; w /= 2) {
+    for (int w = static_cast<int>(16 / es); w > 1; w /= 2) {
         bool ok = a.dim % (2 * w) == 0 && a.rot % (2 * w) == 0;
-        const int64_t bytes = std::min<int64_t>(16, w * es);
+        const int64_t bytes = w * es;
         const auto fits = [&](const void* p, int64_t row, int64_t head) {
             return reinterpret_cast<uintptr_t>(p) % bytes == 0 && row * es % bytes == 0 && head * es % bytes == 0;
         };
@@ -1140,26 +1306,35 @@ int head_width(const HeadArgs& a, int64_t es) {
 }
 
 int head_grad_parts(int64_t rows, int heads, int all_heads) {
-    const int64_t ctas = 3 * static_cast<int64_t>(device_sm_count());
+    const int64_t ctas = 2 * static_cast<int64_t>(device_sm_count());  // all resident
     return static_cast<int>(std::min<int64_t>(rows, std::max<int64_t>(1, ctas * heads / all_heads)));
 }
 
+namespace {
+
+// run(width, f32, pairs) as types
+template <class Run>
+cudaError_t with_head_kind(const HeadArgs& a, int f32, const Run& run) {
+    const auto layout = [&](auto width, auto is_f32) { return a.pairs ? run(width, is_f32, Int<1>{}) : run(width, is_f32, Int<0>{}); };
+    if (f32) return a.width == 4 ? layout(Int<4>{}, Int<1>{}) : a.width == 2 ? layout(Int<2>{}, Int<1>{}) : layout(Int<1>{}, Int<1>{});
+    return a.width == 8   ? layout(Int<8>{}, Int<0>{})
+           : a.width == 4 ? layout(Int<4>{}, Int<0>{})
+           : a.width == 2 ? layout(Int<2>{}, Int<0>{})
+                          : layout(Int<1>{}, Int<0>{});
+}
+
+}  // namespace
+
 cudaError_t launch_heads(HeadArgs a, int f32, cudaStream_t st) {
-    const auto with = [&](auto width) {
-        constexpr int W = decltype(width)::value;
-        if (a.pairs) return f32 ? run_heads<true, W, true>(a, st) : run_heads<false, W, true>(a, st);
-        return f32 ? run_heads<true, W, false>(a, st) : run_heads<false, W, false>(a, st);
-    };
-    return a.width == 8 ? with(Int<8>{}) : a.width == 4 ? with(Int<4>{}) : a.width == 2 ? with(Int<2>{}) : with(Int<1>{});
+    return with_head_kind(a, f32, [&](auto w, auto f, auto pairs) {
+        return run_heads<decltype(f)::value != 0, decltype(w)::value, decltype(pairs)::value != 0>(a, st);
+    });
 }
 
 cudaError_t launch_heads_grad(HeadArgs a, int f32, cudaStream_t st) {
-    const auto with = [&](auto width) {
-        constexpr int W = decltype(width)::value;
-        if (a.pairs) return f32 ? run_heads_grad<true, W, true>(a, st) : run_heads_grad<false, W, true>(a, st);
-        return f32 ? run_heads_grad<true, W, false>(a, st) : run_heads_grad<false, W, false>(a, st);
-    };
-    return a.width == 8 ? with(Int<8>{}) : a.width == 4 ? with(Int<4>{}) : a.width == 2 ? with(Int<2>{}) : with(Int<1>{});
+    return with_head_kind(a, f32, [&](auto w, auto f, auto pairs) {
+        return run_heads_grad<decltype(f)::value != 0, decltype(w)::value, decltype(pairs)::value != 0>(a, st);
+    });
 }
 
 int rmsnorm_grad_parts(int64_t rows, int64_t d) {

@@ -138,7 +138,7 @@ int rmsnorm_grad_parts(int64_t rows, int64_t d);
 cudaError_t launch_rmsnorm_grad(const RmsGradArgs& a, int f32, cudaStream_t st);
 
 // Heads: norm and rotation, and their gradient.
-constexpr int kHeadGroups = 4;
+constexpr int kHeadGroups = 2;  // of a launch; a call with more makes several
 struct HeadGroup {
     const void* in;      // x, or dy
     const void* x;       // gradient: x
@@ -151,9 +151,11 @@ struct HeadGroup {
     // set by the launchers:
     int32_t cta0;        // its first CTA
     int32_t ranges;      // CTAs that the rows are dealt to (and partial rows of dgamma)
-    int32_t split;       // CTAs that share a range's steps
-    int32_t tokens;      // rows per step
-    int32_t slots, stride;       // heads in a CTA's round, and of all CTAs that share a step
+    int32_t split;       // CTAs that share a range
+    int32_t rounds;      // of a step, which takes step_rows rows and step_heads heads more
+    int32_t step_rows, step_heads;
+    int32_t places;      // rows whose angles are held
+    int32_t slots, stride;       // heads in a CTA's round, and of all CTAs that share a range
     int32_t rows_on, heads_on;   // stride heads on from a (row, head),
     int64_t in_step, in_wrap, x_step, x_wrap, out_step, out_wrap;  // in bytes; wrap: where the head passes the row's last
 };
@@ -167,11 +169,11 @@ struct HeadArgs {
     int32_t rot, pairs;  // rotated elements; adjacent pairs instead of halves
     int32_t width;       // elements per vector: 8, 4, 2 or 1
     int32_t lanes;       // of a head (set by the launchers)
-    int32_t pad;
+    int32_t all_heads;   // of the whole call
 };
 // Elements per vector for which every head can be read and written in whole vectors.
 int head_width(const HeadArgs& a, int64_t es);
-cudaError_t launch_heads(HeadArgs a, int f32, cudaStream_t st);
+cudaError_t launch_heads(HeadArgs a, int f32, cudaStream_t st);  // of a group at least
 cudaError_t launch_heads_grad(HeadArgs a, int f32, cudaStream_t st);
 // CTAs (= partial rows of dgamma) of group g in launch_heads_grad
 int head_grad_parts(int64_t rows, int heads, int all_heads);

@@ -455,6 +455,27 @@ hm_status head_matrix(const HeadMatrix& m, int64_t rows, int64_t heads, int64_t 
     return output && !apart(m, rows, heads, dim) ? HM_ERR_ARG : HM_OK;
 }
 
+// A call's groups, all of them.
+struct HeadCall {
+    hm::HeadGroup g[HM_HEAD_GROUPS];
+    int n;
+};
+// Launches them by pairs.
+template <class Launch>
+hm_status by_pairs(hm::HeadArgs& a, const HeadCall& call, const Launch& launch) {
+    static_assert(hm::kHeadGroups == 2, "pairs");
+    a.all_heads = 0;
+    for (int i = 0; i < call.n; ++i) a.all_heads += call.g[i].heads;
+    for (int i = 0; i < call.n; i += 2) {
+        a.n = std::min(2, call.n - i);
+        std::memset(a.g, 0, sizeof(a.g));
+        for (int k = 0; k < a.n; ++k) a.g[k] = call.g[i + k];
+        const hm_status ok = cuda_status(launch(a));
+        if (ok != HM_OK) return ok;
+    }
+    return HM_OK;
+}
+
 // What both calls check of their common arguments, and a's part of them.
 hm_status head_common(int n_groups, hm_dtype dtype, int64_t rows, int64_t head_dim, float eps, const hm_rotation* rot,
                       int64_t* es, hm::HeadArgs* a) {
@@ -463,7 +484,6 @@ hm_status head_common(int n_groups, hm_dtype dtype, int64_t rows, int64_t head_d
     if (n_groups > HM_HEAD_GROUPS || rows > kMaxDim || head_dim > HM_HEAD_MAX_DIM || head_dim % 2) return HM_ERR_GEOMETRY;
     std::memset(a, 0, sizeof(*a));
     a->rows = rows;
-    a->n = n_groups;
     a->dim = static_cast<int32_t>(head_dim);
     a->eps = eps;
     if (rot && rot->rot_dim) {
@@ -493,13 +513,14 @@ extern "C" hm_status head_norm_rope(const hm_head_group* groups, int n_groups, h
                                     int64_t head_dim, float eps, const hm_rotation* rotation, void* stream) {
     int64_t es = 0;
     hm::HeadArgs a;
+    HeadCall call = {};
     hm_status ok = head_common(n_groups, dtype, rows, head_dim, eps, rotation, &es, &a);
     if (ok != HM_OK) return ok;
     if (n_groups && !groups) return HM_ERR_ARG;
     Span small[2];
     head_small(a, small);
     Block3 x[HM_HEAD_GROUPS], y[HM_HEAD_GROUPS];
-    a.n = 0;
+    call.n = 0;
     for (int i = 0; i < n_groups; ++i) {
         const hm_head_group& g = groups[i];
         if (g.heads < 0) return HM_ERR_ARG;
@@ -509,9 +530,9 @@ extern "C" hm_status head_norm_rope(const hm_head_group* groups, int n_groups, h
         const HeadMatrix in = {g.x, g.x_row, g.x_head}, out = {g.y, g.y_row, g.y_head};
         if ((ok = head_matrix(in, rows, g.heads, head_dim, es, false)) != HM_OK) return ok;
         if ((ok = head_matrix(out, rows, g.heads, head_dim, es, true)) != HM_OK) return ok;
-        x[a.n] = block3(g.x, rows, g.x_row, g.heads, g.x_head, head_dim, es);
-        y[a.n] = block3(g.y, rows, g.y_row, g.heads, g.y_head, head_dim, es);
-        hm::HeadGroup& to = a.g[a.n++];
+        x[call.n] = block3(g.x, rows, g.x_row, g.heads, g.x_head, head_dim, es);
+        y[call.n] = block3(g.y, rows, g.y_row, g.heads, g.y_head, head_dim, es);
+        hm::HeadGroup& to = call.g[call.n++];
         to.in = g.x;
         to.in_row = g.x_row;
         to.in_head = g.x_head;
@@ -521,19 +542,21 @@ extern "C" hm_status head_norm_rope(const hm_head_group* groups, int n_groups, h
         to.gamma = g.gamma;
         to.heads = g.heads;
     }
-    for (int i = 0; i < a.n; ++i) {
-        for (int j = 0; j < a.n; ++j) {
-            const bool in_place = i == j && same({a.g[i].in, a.g[i].in_row, a.g[i].in_head}, {a.g[i].out, a.g[i].out_row, a.g[i].out_head});
+    for (int i = 0; i < call.n; ++i) {
+        for (int j = 0; j < call.n; ++j) {
+            const bool in_place = i == j && same({call.g[i].in, call.g[i].in_row, call.g[i].in_head}, {call.g[i].out, call.g[i].out_row, call.g[i].out_head});
             if ((!in_place && overlap(y[i], x[j])) || (j < i && overlap(y[i], y[j])) ||
-                overlap(y[i].all, span(a.g[j].gamma, 1, 0, head_dim, 4)))
+                overlap(y[i].all, span(call.g[j].gamma, 1, 0, head_dim, 4)))
                 return HM_ERR_OVERLAP;
         }
         if (overlap(y[i].all, small[0]) || overlap(y[i].all, small[1])) return HM_ERR_OVERLAP;
     }
-    if (!a.n) return HM_OK;
+    if (!call.n) return HM_OK;
     if ((ok = hm::check_arch()) != HM_OK) return ok;
-    a.width = hm::head_width(a, es);
-    return cuda_status(hm::launch_heads(a, dtype == HM_F32, static_cast<cudaStream_t>(stream)));
+    return by_pairs(a, call, [&](hm::HeadArgs& pair) {
+        pair.width = hm::head_width(pair, es);
+        return hm::launch_heads(pair, dtype == HM_F32, static_cast<cudaStream_t>(stream));
+    });
 }
 
 namespace {
@@ -571,6 +594,7 @@ extern "C" hm_status head_norm_rope_backward(const hm_head_grad* groups, int n_g
                                              size_t workspace_bytes, void* stream) {
     int64_t es = 0;
     hm::HeadArgs a;
+    HeadCall call = {};
     hm_status ok = head_common(n_groups, dtype, rows, head_dim, eps, rotation, &es, &a);
     if (ok != HM_OK) return ok;
     if (n_groups && !groups) return HM_ERR_ARG;
@@ -584,7 +608,7 @@ extern "C" hm_status head_norm_rope_backward(const hm_head_grad* groups, int n_g
     Block3 dy[HM_HEAD_GROUPS], x[HM_HEAD_GROUPS], dx[HM_HEAD_GROUPS];
     Span dg[HM_HEAD_GROUPS];
     int from[HM_HEAD_GROUPS];
-    a.n = 0;
+    call.n = 0;
     for (int i = 0; i < n_groups; ++i) {
         const hm_head_grad& g = groups[i];
         if (g.heads < 0 || (g.dgamma && !g.gamma)) return HM_ERR_ARG;
@@ -593,9 +617,9 @@ extern "C" hm_status head_norm_rope_backward(const hm_head_grad* groups, int n_g
         if (!head_dim) continue;
         const bool live = g.heads && rows;
         if (!live && !g.dgamma) continue;
-        const int k = a.n++;
+        const int k = call.n++;
         from[k] = i;
-        hm::HeadGroup& to = a.g[k];
+        hm::HeadGroup& to = call.g[k];
         dg[k] = span(g.dgamma, 1, 0, head_dim, 4);
         to.gamma = g.gamma;
         to.dgamma = g.dgamma;
@@ -622,12 +646,12 @@ extern "C" hm_status head_norm_rope_backward(const hm_head_grad* groups, int n_g
         to.out_head = g.dx_head;
         to.heads = g.heads;
     }
-    for (int i = 0; i < a.n; ++i) {
-        const HeadMatrix out = {a.g[i].out, a.g[i].out_row, a.g[i].out_head};
-        for (int j = 0; j < a.n; ++j) {
-            const Span gamma = span(a.g[j].gamma, 1, 0, head_dim, 4);
-            const bool is_dy = i == j && same(out, {a.g[i].in, a.g[i].in_row, a.g[i].in_head});
-            const bool is_x = i == j && same(out, {a.g[i].x, a.g[i].x_row, a.g[i].x_head});
+    for (int i = 0; i < call.n; ++i) {
+        const HeadMatrix out = {call.g[i].out, call.g[i].out_row, call.g[i].out_head};
+        for (int j = 0; j < call.n; ++j) {
+            const Span gamma = span(call.g[j].gamma, 1, 0, head_dim, 4);
+            const bool is_dy = i == j && same(out, {call.g[i].in, call.g[i].in_row, call.g[i].in_head});
+            const bool is_x = i == j && same(out, {call.g[i].x, call.g[i].x_row, call.g[i].x_head});
             if ((!is_dy && overlap(dx[i], dy[j])) || (!is_x && overlap(dx[i], x[j])) || (j < i && overlap(dx[i], dx[j])) ||
                 overlap(dx[i].all, gamma) || overlap(dx[i].all, dg[j]) || overlap(dg[i], dy[j].all) || overlap(dg[i], x[j].all) ||
                 overlap(dg[i], gamma) || (j < i && overlap(dg[i], dg[j])))
@@ -635,21 +659,23 @@ extern "C" hm_status head_norm_rope_backward(const hm_head_grad* groups, int n_g
         }
         for (int j = 0; j < 3; ++j)
             if (overlap(dx[i].all, small[j]) || overlap(dg[i], small[j])) return HM_ERR_OVERLAP;
-        if (overlap(small[2], dy[i].all) || overlap(small[2], x[i].all) || overlap(small[2], span(a.g[i].gamma, 1, 0, head_dim, 4)))
+        if (overlap(small[2], dy[i].all) || overlap(small[2], x[i].all) || overlap(small[2], span(call.g[i].gamma, 1, 0, head_dim, 4)))
             return HM_ERR_OVERLAP;
     }
     if (overlap(small[2], small[0]) || overlap(small[2], small[1])) return HM_ERR_OVERLAP;
-    if (!a.n) return HM_OK;
+    if (!call.n) return HM_OK;
     if ((ok = hm::check_arch()) != HM_OK) return ok;
     size_t floats = 0;
-    for (int k = 0; k < a.n; ++k) {
+    for (int k = 0; k < call.n; ++k) {
         const size_t part = grad_partials(groups, n_groups, from[k], rows, head_dim);
-        if (part) a.g[k].partials = static_cast<float*>(workspace) + floats;
+        if (part) call.g[k].partials = static_cast<float*>(workspace) + floats;
         floats += part;
     }
     if (floats && (!workspace || workspace_bytes < floats * 4)) return HM_ERR_WORKSPACE;
-    a.width = hm::head_width(a, es);
-    return cuda_status(hm::launch_heads_grad(a, dtype == HM_F32, static_cast<cudaStream_t>(stream)));
+    return by_pairs(a, call, [&](hm::HeadArgs& pair) {
+        pair.width = hm::head_width(pair, es);
+        return hm::launch_heads_grad(pair, dtype == HM_F32, static_cast<cudaStream_t>(stream));
+    });
 }
 
 extern "C" hm_status rope_turns(int32_t rot_dim, double theta, int32_t scaling, double factor, double trained,
