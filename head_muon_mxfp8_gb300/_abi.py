@@ -164,6 +164,7 @@ _SIGS = {
                              C.c_int, C.c_int, _P]),
     "mxfp8_gemm_epilogue": (C.c_int, [_P, C.c_int64, _P, _P, C.c_int64, _P, C.c_int64, C.c_int64, C.c_int64, _P,
                                       C.c_int64, C.c_int, C.POINTER(hm_epilogue), _P]),
+    "mxfp8_gemm_epilogue_form": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.c_int, _I32P, _I32P, _I32P]),
     "mxfp8_quantize_bias_workspace": (C.c_int, [C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
     "mxfp8_quantize_bias": (C.c_int, [_P, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_int, _P, C.c_int64, _P, _P,
                                       C.c_int64, _P, _P, C.c_int, _P, C.c_size_t, _P]),
@@ -446,6 +447,13 @@ def mxfp8_gemm_epilogue(a: int, lda: int, a_scales: int, b: int, ldb: int, b_sca
     """The product with bias, activation, gate, residual or their gradients in its epilogue (see include/hm.h)."""
     check("mxfp8_gemm_epilogue", lib().mxfp8_gemm_epilogue(a, lda, a_scales, b, ldb, b_scales, m, n, k, d, ldd, d_dtype,
                                                            C.byref(epilogue), stream))
+
+
+def mxfp8_gemm_epilogue_form(m: int, n: int, k: int, d_dtype: int):
+    """(tile, parts, sums): the kernel that a product with an epilogue takes."""
+    v = [C.c_int32(0) for _ in range(3)]
+    check("mxfp8_gemm_epilogue_form", lib().mxfp8_gemm_epilogue_form(m, n, k, d_dtype, *[C.byref(x) for x in v]))
+    return tuple(x.value for x in v)
 
 
 def mxfp8_quantize_bias_workspace(rows: int, cols: int) -> int:

@@ -880,7 +880,10 @@ int resident_clusters(int split) {
 // Measured: a stage takes 0.3 us in a CTA that has its SM to itself (128 x 128 tiles,
 // 37 stages in 11.4 us; 128 x 16, 40 in 11.1), 0.45 us where two share an SM, or
 // what the CTAs get of B from HBM together; adding 128 rows of parts takes 4.5 us, one
-// row 0.7; a round starts and ends in 3.
+// row 0.7; a round starts and ends in 3.  With an epilogue 2 more, and 0.5 for each 16 rows of
+// an undivided tile, which four warps finish (divided ones are finished by six warps of
+// each CTA): 301 x 1408 x 2048 bf16 with GELU 13.2 us in whole tiles of 128, 9.7 in tiles of 64
+// with K in four parts.
 template <int BN>
 int split_for(int tiles_p, int tiles_q, const MxGemmArgs& p, double* cost) {
     const int rows = p.m, num_kb = p.num_kb;
@@ -895,7 +898,8 @@ int split_for(int tiles_p, int tiles_q, const MxGemmArgs& p, double* cost) {
         const double stage = std::max({kStageUs, bytes * std::ceil(ctas / device_sm_count()) / 0.15e6,
                                        (kPBytes + kSfBytes) * ctas / tiles_q / 6.5e6});
         const double rounds = static_cast<double>((tiles + cap - 1) / cap);
-        const double c = rounds * (((num_kb + s - 1) / s) * stage + 3.0 + (s > 1 ? 0.7 + 0.03 * std::min(rows, BN) : 0.0));
+        const double c = rounds * (((num_kb + s - 1) / s) * stage + 3.0 + (s > 1 ? 0.7 + 0.03 * std::min(rows, BN) : 0.0) +
+                                   (p.epilogue ? 2.0 + (s > 1 ? 0.0 : 0.5 * ((std::min(rows, BN) + kPieceRows - 1) / kPieceRows)) : 0.0));
         if (!best || c < *cost) *cost = c, best = s;
     }
     return best;
@@ -911,6 +915,19 @@ cudaError_t split_form(const MxGemmArgs& p, MxGemmForm* f, double* cost) {
     f->parts = split_for<BN>((p.n + kTileP - 1) / kTileP, (p.m + BN - 1) / BN, p, cost);
     f->sums = 0;
     return cudaSuccess;
+}
+
+// Tiles of 128 rows, or with an epilogue of 64 where those are estimated to take less: there
+// are then twice as many warps to finish them.  (Tiles start at multiples of 64 rows:
+// a tile's scales begin at an even column of TMEM.)
+cudaError_t split_few_rows(const MxGemmArgs& p, MxGemmForm* f, double* cost) {
+    const cudaError_t e = split_form<128>(p, f, cost);
+    if (e != cudaSuccess || !p.epilogue || (p.m + 63) / 64 > 65535) return e;
+    MxGemmForm g;
+    double c;
+    const cudaError_t e64 = split_form<64>(p, &g, &c);
+    if (e64 == cudaSuccess && c < *cost) *f = g, *cost = c;
+    return e64;
 }
 
 template <int BN>
@@ -984,7 +1001,7 @@ cudaError_t mx_gemm_form(const MxGemmArgs& args, MxGemmForm* f) {
         if (p.m <= 16) return split_form<16>(p, f, &cost);
         if (p.m <= 32) return split_form<32>(p, f, &cost);
         if (p.m <= 64) return split_form<64>(p, f, &cost);
-        if (p.m <= 128) return split_form<128>(p, f, &cost);
+        if (p.m <= 128) return split_few_rows(p, f, &cost);
     }
     // The tile width that leaves the least time to the pair with the most tiles.  A
     // stage's time goes with the rows it loads (256 + BN): 128-wide tiles took 0.79 of
@@ -999,7 +1016,9 @@ cudaError_t mx_gemm_form(const MxGemmArgs& args, MxGemmForm* f) {
     for (const int bn : {256, 192, 128}) {
         if (bn > 192 && sums) continue;
         const int64_t tiles = static_cast<int64_t>((p.n + 255) / 256) * ((p.m + bn - 1) / bn);
-        const double c = static_cast<double>((tiles + pairs - 1) / pairs) * std::max(p.num_kb * (256 + bn) * (0.37 / 512), 2.2) + 4.0;
+        // an epilogue (hm_epilogue) takes 1.1 us per 32 rows, and the last tile's overlaps nothing
+        const double sum = p.num_kb * (256 + bn) * (0.37 / 512), last = p.epilogue ? bn / 32 * 1.1 : 2.2;
+        const double c = static_cast<double>((tiles + pairs - 1) / pairs) * std::max(sum, last) + 4.0 + (p.epilogue ? std::min(sum, last) : 0.0);
         if (!best || c < least) best = bn, least = c;
     }
     // Too few tiles for the pairs: 128 x 128 tiles with K split over clusters.  Both
@@ -1009,7 +1028,7 @@ cudaError_t mx_gemm_form(const MxGemmArgs& args, MxGemmForm* f) {
     // and 15.5), but for 300 and 384 x 20480 x 5120 bf16, where two rounds of
     // undivided tiles take 48 us that the estimate puts at 42, and pairs 38.
     if ((static_cast<int64_t>(p.m) + 127) / 128 <= 65535 && !long_sum) {
-        const cudaError_t e = split_form<128>(p, f, &cost);
+        const cudaError_t e = split_few_rows(p, f, &cost);
         if (e != cudaSuccess || cost < least) return e;
     }
     f->tile = best;

@@ -168,8 +168,10 @@ extern "C" hm_status mxfp8_gemm_epilogue(const uint8_t* a, int64_t lda, const ui
     return cuda_status(hm::launch_mx_gemm(a, lda, b, ldb, p, static_cast<cudaStream_t>(stream)));
 }
 
-extern "C" hm_status mxfp8_gemm_form(int64_t m, int64_t n, int64_t k, hm_dtype d_dtype, int32_t* tile, int32_t* parts,
-                                     int32_t* sums) {
+namespace {
+
+hm_status gemm_form(int64_t m, int64_t n, int64_t k, hm_dtype d_dtype, bool epilogue, int32_t* tile, int32_t* parts,
+                    int32_t* sums) {
     int64_t es = 0;
     if (!tile || !parts || !sums || m <= 0 || n <= 0 || k <= 0) return HM_ERR_ARG;
     if (!elem_size(d_dtype, &es)) return HM_ERR_DTYPE;
@@ -183,10 +185,23 @@ extern "C" hm_status mxfp8_gemm_form(int64_t m, int64_t n, int64_t k, hm_dtype d
     p.n = static_cast<int32_t>(n);
     p.k = static_cast<int32_t>(k);
     p.d_f32 = d_dtype == HM_F32;
+    p.epilogue = epilogue;
     hm::MxGemmForm f;
     const hm_status ok = cuda_status(hm::mx_gemm_form(p, &f));
     if (ok == HM_OK) *tile = f.tile, *parts = f.parts, *sums = f.sums;
     return ok;
+}
+
+}  // namespace
+
+extern "C" hm_status mxfp8_gemm_form(int64_t m, int64_t n, int64_t k, hm_dtype d_dtype, int32_t* tile, int32_t* parts,
+                                     int32_t* sums) {
+    return gemm_form(m, n, k, d_dtype, false, tile, parts, sums);
+}
+
+extern "C" hm_status mxfp8_gemm_epilogue_form(int64_t m, int64_t n, int64_t k, hm_dtype d_dtype, int32_t* tile,
+                                              int32_t* parts, int32_t* sums) {
+    return gemm_form(m, n, k, d_dtype, true, tile, parts, sums);
 }
 
 namespace {

@@ -490,6 +490,8 @@ typedef struct {
 hm_status mxfp8_gemm_epilogue(const uint8_t* a, int64_t lda, const uint8_t* a_scales, const uint8_t* b, int64_t ldb,
                               const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, void* d, int64_t ldd,
                               hm_dtype d_dtype, const hm_epilogue* epilogue, void* stream);
+hm_status mxfp8_gemm_epilogue_form(int64_t m, int64_t n, int64_t k, hm_dtype d_dtype, int32_t* tile, int32_t* parts,
+                                   int32_t* sums);  /* as mxfp8_gemm_form */
 
 /* Quantizes x [rows][ldx] (HM_BF16 or HM_F32) to MXFP8 along its columns
  * and / or along its rows, reading x once:
