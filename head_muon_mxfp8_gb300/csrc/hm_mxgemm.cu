@@ -955,8 +955,10 @@ template <int BN, bool SUMS, int EPI = kEpiNone>
 cudaError_t launch_pair(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, MxGemmArgs p, cudaStream_t st) {
     using C = PairMx<BN>;
     if constexpr (EPI == kEpiNone) {
-        if (p.epilogue == kEpiF32) return launch_pair<BN, SUMS, kEpiF32>(a, lda, b, ldb, p, st);
-        if (p.epilogue == kEpiF32Any) return launch_pair<BN, SUMS, kEpiF32Any>(a, lda, b, ldb, p, st);
+        if constexpr (BN < 256) {
+            if (p.epilogue == kEpiF32) return launch_pair<BN, SUMS, kEpiF32>(a, lda, b, ldb, p, st);
+            if (p.epilogue == kEpiF32Any) return launch_pair<BN, SUMS, kEpiF32Any>(a, lda, b, ldb, p, st);
+        }
         if constexpr (!SUMS) {
             if (p.epilogue == kEpiBf16) return launch_pair<BN, SUMS, kEpiBf16>(a, lda, b, ldb, p, st);
             if (p.epilogue == kEpiBf16Any) return launch_pair<BN, SUMS, kEpiBf16Any>(a, lda, b, ldb, p, st);
@@ -1010,11 +1012,14 @@ cudaError_t mx_gemm_form(const MxGemmArgs& args, MxGemmForm* f) {
     // With sums at most 192: a thread of the eight epilogue warps would hold 128 of
     // them at 256, and ten warps leave it 168 registers (192 takes all, 28 bytes spilled).
     const bool sums = p.d_f32 && p.num_kb > kChunkK / kTileK;
+    // With an epilogue and fp32 D the products of K <= kChunkK take less than their epilogue,
+    // and 128 rows finish as fast as half of 256.
+    const bool wide_never = p.d_f32 && p.epilogue;
     const int64_t pairs = device_sm_count() / 2;
     int best = 0;
     double least = 0;
     for (const int bn : {256, 192, 128}) {
-        if (bn > 192 && sums) continue;
+        if (bn > 192 && (sums || wide_never)) continue;
         const int64_t tiles = static_cast<int64_t>((p.n + 255) / 256) * ((p.m + bn - 1) / bn);
         // an epilogue (hm_epilogue) takes 1.1 us per 32 rows, and the last tile's overlaps nothing
         const double sum = p.num_kb * (256 + bn) * (0.37 / 512), last = p.epilogue ? bn / 32 * 1.1 : 2.2;
