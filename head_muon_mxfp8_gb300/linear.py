@@ -75,9 +75,13 @@ class NormLinear:
         self.gamma = torch.ones(d_in, dtype=torch.float32, device=dev)
         self._allocate(tokens, d_in, d_out, dev)
 
+    def _units(self, d_out: int, d_in: int):
+        """The weight's update units, (offset, rows, columns) each."""
+        return [(0, d_out, d_in)]
+
     @_on_its_device
     def _allocate(self, tokens: int, d_in: int, d_out: int, dev) -> None:
-        self.session = MuonSession(d_out * d_in, [(0, d_out, d_in)], so=1, sw=1, sg=1, device=dev)
+        self.session = MuonSession(d_out * d_in, self._units(d_out, d_in), so=1, sw=1, sg=1, device=dev)
         base, n = self.session.bases[0], d_out * d_in
         self.w = self.session.w[base:base + n].view(d_out, d_in)   # fp32 main weight
         self.g = self.session.g[base:base + n].view(d_out, d_in)   # fp32 main gradient
