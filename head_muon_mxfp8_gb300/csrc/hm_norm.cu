@@ -493,6 +493,9 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* partials, int
 // per element where memory leaves time for 21 (8192 x 80 heads of 128 bf16: 100 us).
 // ---------------------------------------------------------------------------
 constexpr int kHeadThreads = 256;
+// A row's angles take a CTA as long as this many heads (16384 rows of 32 + 8 heads of 128 bf16,
+// gradient: 92.6 us counting none, 88.6 one, 84.9 two, 87.3 five).
+constexpr int kAngles = 2;
 constexpr int kHeadSmem = 113 * 1024;  // at most: two CTAs per SM
 
 // A thread's 8 first and 8 second elements of pairs.
@@ -737,10 +740,10 @@ __device__ __forceinline__ void sincos_eighth(float y, float& s, float& c) {
     c = fmaf(v, z, 1.f);
 }
 
-// cos and sin of `tokens` rows' positions, scaled (1 and 0 past the rotated part): a
+// cos and sin of `tokens` positions, every apart-th, scaled (1 and 0 past the rotated part): a
 // table of dim floats for each, the first one's at `place` of `places` in a circle.
 template <int W, bool PAIRS>
-__device__ __forceinline__ void head_angles(const HeadArgs& p, const int64_t* positions, int tokens, float* tables, int place, int places) {
+__device__ __forceinline__ void head_angles(const HeadArgs& p, const int64_t* positions, int64_t apart, int tokens, float* tables, int place, int places) {
     const int half = p.dim / 2, pairs = p.rot / 2, turned = p.rot / (2 * W), all = p.dim / (2 * W);
     int t = threadIdx.x / half, c = threadIdx.x - t * half;  // pair c of row t
     const int t_on = kHeadThreads / half, c_on = kHeadThreads - t_on * half;
@@ -754,7 +757,7 @@ __device__ __forceinline__ void head_angles(const HeadArgs& p, const int64_t* po
                 v = vec < turned ? vec : vec - turned;
                 e = vec < turned ? in : P + in;
             }
-            const uint64_t turn = static_cast<uint64_t>(positions[t]) * p.turns[c];
+            const uint64_t turn = static_cast<uint64_t>(positions[t * apart]) * p.turns[c];
             const uint32_t hi = static_cast<uint32_t>(turn >> 32);
             const uint32_t quarter = (hi + 0x20000000u) >> 30;
             const int32_t rest = static_cast<int32_t>(hi - (quarter << 30));  // an eighth of a turn at most
@@ -839,13 +842,14 @@ __device__ __forceinline__ float head_rstd(float sum, float inv_dim, float eps) 
     return a > 1e-35f && a < 1e35f ? fmaf(0.5f * y, e, y) : y;
 }
 
-// This thread's way through its CTA's rows: a range of them, of whose (row, head) items
-// it takes every stride-th.  All strides are the host's.
+// This thread's way through its CTA's rows: every ranges-th of them, so that all CTAs
+// read and write in the same part of memory; of their (row, head) items it takes every
+// stride-th.  All strides are the host's.
 struct HeadWay {
     int lane;          // of its head
     int slot;          // which head of the CTA's round; -1: a lane that is left over
-    int row, head;     // its first item, the row counted from tok0
-    int rows;          // of the range
+    int row, head;     // its first item, among the CTA's rows
+    int rows;          // of the CTA
     int64_t tok0;
     int64_t rounds;    // that all threads of the CTA make
     __device__ __forceinline__ HeadWay(const HeadArgs& p, const HeadGroup& g) {
@@ -856,20 +860,20 @@ struct HeadWay {
         const int item = part * g.slots + max(slot, 0);
         row = item / g.heads;
         head = item - row * g.heads;
-        tok0 = p.rows * range / g.ranges;
-        rows = static_cast<int>(p.rows * (range + 1) / g.ranges - tok0);
+        tok0 = range;
+        rows = static_cast<int>((p.rows - range + g.ranges - 1) / g.ranges);
         rounds = max(static_cast<int64_t>(0), (static_cast<int64_t>(rows) * g.heads - part * g.slots + g.stride - 1) / g.stride);
     }
 };
-// The range's positions, in shared memory where they are few enough (copied with the
-// first head): read from memory at every step, they held up a CTA of 8 heads, whose
+// The CTA's positions, in shared memory where they are few enough (copied with the
+// first head; else nullptr): read from memory at every step, they held up a CTA of 8 heads, whose
 // steps are short (16384 rows of 32 + 8 heads bf16: gradient 114 us).
 constexpr int kHeadPositions = 1024;
-__device__ __forceinline__ const int64_t* head_positions(const HeadArgs& p, const HeadWay& way, float* smem) {
+__device__ __forceinline__ const int64_t* head_positions(const HeadArgs& p, const HeadWay& way, int ranges, float* smem) {
     const int64_t* from = p.positions + way.tok0;
-    if (!p.rot || way.rows > kHeadPositions) return from;
+    if (!p.rot || way.rows > kHeadPositions) return nullptr;
     for (int i = threadIdx.x; i < way.rows; i += kHeadThreads)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem) + 8 * i), "l"(from + i) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem) + 8 * i), "l"(from + static_cast<int64_t>(i) * ranges) : "memory");
     return reinterpret_cast<const int64_t*>(smem);
 }
 
@@ -886,7 +890,8 @@ struct HeadReach {
         if (rest >= g.heads) rest -= g.heads, ++rows;
         rows = min(rows, way.rows);  // (stays there: no overflow)
         const int more = min(way.rows, rows + (rest > 0)) - before;
-        head_angles<W, PAIRS>(p, positions + before, more, tables, place, g.places);
+        if (positions) head_angles<W, PAIRS>(p, positions + before, 1, more, tables, place, g.places);
+        else head_angles<W, PAIRS>(p, p.positions + way.tok0 + static_cast<int64_t>(before) * g.ranges, g.ranges, more, tables, place, g.places);
         place += more;
         if (place >= g.places) place -= g.places;
     }
@@ -905,8 +910,8 @@ __device__ __forceinline__ void head_body(const HeadArgs& p) {
     const HeadPlace<W, PAIRS> at(p, way.lane);
     const int rows = way.slot < 0 ? 0 : way.rows;
     int row = way.row, head = way.head, row1 = way.row, head1 = way.head;  // 1: of the copies
-    const char* in = static_cast<const char*>(g.in) + ((way.tok0 + row) * g.in_row + head * g.in_head) * es;
-    char* out = static_cast<char*>(g.out) + ((way.tok0 + row) * g.out_row + head * g.out_head) * es;
+    const char* in = static_cast<const char*>(g.in) + ((way.tok0 + static_cast<int64_t>(row) * g.ranges) * g.in_row + head * g.in_head) * es;
+    char* out = static_cast<char*>(g.out) + ((way.tok0 + static_cast<int64_t>(row) * g.ranges) * g.out_row + head * g.out_head) * es;
     Ring ring(reinterpret_cast<char*>(smem));
     const auto ahead = [&] {
         ring.put(at, in, row1 < rows);
@@ -919,7 +924,7 @@ __device__ __forceinline__ void head_body(const HeadArgs& p) {
     float* gammas = smem + Ring::kBytes / 4;
     float* tables = gammas + (p.dim + 3) / 4 * 4;
     float* after = tables + (g.places * p.dim + 3) / 4 * 4;
-    const int64_t* positions = head_positions(p, way, after);
+    const int64_t* positions = head_positions(p, way, g.ranges, after);
     const float inv_dim = 1.f / static_cast<float>(p.dim);
     const bool norm = g.gamma != nullptr;
     if (norm && way.slot == 0) head_gamma(at, g.gamma, p.dim, gammas);
@@ -998,9 +1003,9 @@ __device__ __forceinline__ void head_grad_body(const HeadArgs& p) {
     const bool norm = g.gamma != nullptr;
     const int rows = way.slot < 0 ? 0 : way.rows;
     int row = way.row, head = way.head, row1 = way.row, head1 = way.head;  // 1: of the copies
-    const char* in = static_cast<const char*>(g.in) + ((way.tok0 + row) * g.in_row + head * g.in_head) * es;
-    const char* from = static_cast<const char*>(g.x) + ((way.tok0 + row) * g.x_row + head * g.x_head) * es;
-    char* out = static_cast<char*>(g.out) + ((way.tok0 + row) * g.out_row + head * g.out_head) * es;
+    const char* in = static_cast<const char*>(g.in) + ((way.tok0 + static_cast<int64_t>(row) * g.ranges) * g.in_row + head * g.in_head) * es;
+    const char* from = static_cast<const char*>(g.x) + ((way.tok0 + static_cast<int64_t>(row) * g.ranges) * g.x_row + head * g.x_head) * es;
+    char* out = static_cast<char*>(g.out) + ((way.tok0 + static_cast<int64_t>(row) * g.ranges) * g.out_row + head * g.out_head) * es;
     Ring dys(reinterpret_cast<char*>(smem)), xs(reinterpret_cast<char*>(smem) + Ring::kBytes);
     const auto ahead = [&] {
         dys.put(at, in, row1 < rows);
@@ -1015,7 +1020,7 @@ __device__ __forceinline__ void head_grad_body(const HeadArgs& p) {
     float* gammas = smem + 2 * Ring::kBytes / 4;
     float* tables = gammas + (p.dim + 3) / 4 * 4;
     float* after = tables + (g.places * p.dim + 3) / 4 * 4;
-    const int64_t* positions = head_positions(p, way, after);
+    const int64_t* positions = head_positions(p, way, g.ranges, after);
     const float inv_dim = 1.f / static_cast<float>(p.dim);
     if (norm && way.slot == 0) head_gamma(at, g.gamma, p.dim, gammas);
 #pragma unroll
@@ -1203,6 +1208,11 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
     return launch_early(dgamma_kernel, a.d / 32, 1024, 0, st, a.partials, parts, a.d, a.accumulate, a.dgamma);
 }
 
+// A group's share of a call's CTAs: by heads and the angles of its rows.
+int64_t head_share(int64_t ctas, int heads, int all_heads, int groups) {
+    return std::max<int64_t>(1, ctas * (heads + kAngles) / (all_heads + kAngles * groups));
+}
+
 // Lanes per head, 16 elements each, and heads in a CTA's round.
 int head_lanes(int dim) { return (dim + 15) / 16; }
 int head_slots(int lanes) { return kHeadThreads / 32 * (32 / lanes); }
@@ -1211,7 +1221,7 @@ int head_slots(int lanes) { return kHeadThreads / 32 * (32 / lanes); }
 // CTA per row and more CTAs than that (split), a row's heads over several.  A step is
 // kHeadRounds rounds, fewer where the angles of two steps' rows would take more than
 // kHeadTables.  Returns the bytes of gamma, the angles and the positions.
-constexpr int kHeadRounds = 8;
+constexpr int kHeadRounds = 4;
 constexpr int kHeadTables = 18 * 1024;
 int plan_group(HeadArgs& a, HeadGroup& g, int64_t ctas, int64_t es, bool split, int64_t* used) {
     g.slots = head_slots(a.lanes);
@@ -1228,8 +1238,8 @@ int plan_group(HeadArgs& a, HeadGroup& g, int64_t ctas, int64_t es, bool split, 
     g.step_rows = g.rounds * g.stride / g.heads;
     g.step_heads = g.rounds * g.stride - g.step_rows * g.heads;
     const auto steps = [&](int64_t row, int64_t head, int64_t* step, int64_t* wrap) {
-        *step = (g.rows_on * row + g.heads_on * head) * es;
-        *wrap = (row - g.heads * head) * es;
+        *step = (g.rows_on * g.ranges * row + g.heads_on * head) * es;
+        *wrap = (g.ranges * row - g.heads * head) * es;
     };
     steps(g.in_row, g.in_head, &g.in_step, &g.in_wrap);
     steps(g.x_row, g.x_head, &g.x_step, &g.x_wrap);
@@ -1245,10 +1255,13 @@ cudaError_t run_heads(HeadArgs& a, cudaStream_t st) {
     a.lanes = head_lanes(a.dim);
     int64_t ctas = 0;
     int smem = 0;
-    // as many as are resident, by heads
-    const int64_t most = static_cast<int64_t>(W < 4 ? 2 : F32 ? 3 : 4) * device_sm_count();
+    // As many CTAs as are resident, or several times as many where each still makes 16 rounds:
+    // memory serves waves of them faster than one of longer ones (32768 x 80 heads of 128 bf16: 240
+    // us with one, 220 with two, 202 with six; 8192 of 64 29.7, 31.4 and 41.7).
+    const int64_t resident = static_cast<int64_t>(W < 4 ? 2 : F32 ? 3 : 4) * device_sm_count();
+    const int64_t most = resident * std::max<int64_t>(1, a.rows * a.all_heads / head_slots(a.lanes) / 16 / resident);
     for (int i = 0; i < a.n; ++i)
-        smem = std::max(smem, plan_group(a, a.g[i], std::max<int64_t>(1, most * a.g[i].heads / a.all_heads), F32 ? 4 : 2, true, &ctas));
+        smem = std::max(smem, plan_group(a, a.g[i], head_share(most, a.g[i].heads, a.all_heads, a.all_groups), F32 ? 4 : 2, true, &ctas));
     if (a.n == 1) a.g[1].cta0 = INT32_MAX;
     smem += HeadRing<F32, W, PAIRS, kHeadAhead<F32>>::kBytes;
     static PerDevice done;
@@ -1268,7 +1281,7 @@ cudaError_t run_heads_grad(HeadArgs& a, cudaStream_t st) {
         g.cta0 = static_cast<int32_t>(ctas);
         wanted += g.dgamma != nullptr;
         if (!g.heads || !a.rows) continue;  // an empty sum: no ranges
-        smem = std::max(smem, plan_group(a, g, head_grad_parts(a.rows, g.heads, a.all_heads), F32 ? 4 : 2, false, &ctas));
+        smem = std::max(smem, plan_group(a, g, head_grad_parts(a.rows, g.heads, a.all_heads, a.all_groups), F32 ? 4 : 2, false, &ctas));
     }
     if (a.n == 1) a.g[1].cta0 = INT32_MAX;
     smem = std::max(smem + 2 * HeadRing<F32, W, PAIRS, kHeadGradAhead<F32>>::kBytes, head_slots(a.lanes) * a.dim * 4);
@@ -1305,9 +1318,9 @@ int head_width(const HeadArgs& a, int64_t es) {
     return 1;
 }
 
-int head_grad_parts(int64_t rows, int heads, int all_heads) {
-    const int64_t ctas = 2 * static_cast<int64_t>(device_sm_count());  // all resident
-    return static_cast<int>(std::min<int64_t>(rows, std::max<int64_t>(1, ctas * heads / all_heads)));
+int head_grad_parts(int64_t rows, int heads, int all_heads, int groups) {
+    // all resident: 8192 x 80 heads of 128 bf16 84 us, with twice as many 90
+    return static_cast<int>(std::min(rows, head_share(2 * static_cast<int64_t>(device_sm_count()), heads, all_heads, groups)));
 }
 
 namespace {

@@ -169,14 +169,14 @@ struct HeadArgs {
     int32_t rot, pairs;  // rotated elements; adjacent pairs instead of halves
     int32_t width;       // elements per vector: 8, 4, 2 or 1
     int32_t lanes;       // of a head (set by the launchers)
-    int32_t all_heads;   // of the whole call
+    int32_t all_heads, all_groups;  // of the whole call
 };
 // Elements per vector for which every head can be read and written in whole vectors.
 int head_width(const HeadArgs& a, int64_t es);
 cudaError_t launch_heads(HeadArgs a, int f32, cudaStream_t st);  // of a group at least
 cudaError_t launch_heads_grad(HeadArgs a, int f32, cudaStream_t st);
 // CTAs (= partial rows of dgamma) of group g in launch_heads_grad
-int head_grad_parts(int64_t rows, int heads, int all_heads);
+int head_grad_parts(int64_t rows, int heads, int all_heads, int groups);
 
 // A launch takes its tensors by value: up to kClipTensors, or up to kClipFew in
 // the one-launch form for little data.

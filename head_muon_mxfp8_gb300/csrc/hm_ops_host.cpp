@@ -479,8 +479,11 @@ struct HeadCall {
 template <class Launch>
 hm_status by_pairs(hm::HeadArgs& a, const HeadCall& call, const Launch& launch) {
     static_assert(hm::kHeadGroups == 2, "pairs");
-    a.all_heads = 0;
-    for (int i = 0; i < call.n; ++i) a.all_heads += call.g[i].heads;
+    a.all_heads = a.all_groups = 0;
+    for (int i = 0; i < call.n; ++i) {
+        a.all_heads += call.g[i].heads;
+        a.all_groups += call.g[i].heads > 0;
+    }
     for (int i = 0; i < call.n; i += 2) {
         a.n = std::min(2, call.n - i);
         std::memset(a.g, 0, sizeof(a.g));
@@ -576,16 +579,16 @@ extern "C" hm_status head_norm_rope(const hm_head_group* groups, int n_groups, h
 
 namespace {
 
-int64_t all_heads(const hm_head_grad* groups, int n) {
-    int64_t all = 0;
-    for (int i = 0; i < n; ++i) all += groups[i].heads;
-    return all;
-}
 // Floats of dgamma's partial sums of group i.
 size_t grad_partials(const hm_head_grad* groups, int n, int i, int64_t rows, int64_t head_dim) {
     const hm_head_grad& g = groups[i];
     if (!g.dgamma || !g.heads || !rows) return 0;
-    return static_cast<size_t>(hm::head_grad_parts(rows, g.heads, static_cast<int>(all_heads(groups, n)))) * static_cast<size_t>(head_dim);
+    int heads = 0, live = 0;
+    for (int k = 0; k < n; ++k) {
+        heads += groups[k].heads;
+        live += groups[k].heads > 0;
+    }
+    return static_cast<size_t>(hm::head_grad_parts(rows, g.heads, heads, live)) * static_cast<size_t>(head_dim);
 }
 
 }  // namespace
