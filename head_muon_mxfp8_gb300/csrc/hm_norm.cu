@@ -1255,11 +1255,11 @@ cudaError_t run_heads(HeadArgs& a, cudaStream_t st) {
     a.lanes = head_lanes(a.dim);
     int64_t ctas = 0;
     int smem = 0;
-    // As many CTAs as are resident, or several times as many where each still makes 16 rounds:
+    // As many CTAs as are resident, or several times as many where each still makes 16 rounds (of fp32 8):
     // memory serves waves of them faster than one of longer ones (32768 x 80 heads of 128 bf16: 240
     // us with one, 220 with two, 202 with six; 8192 of 64 29.7, 31.4 and 41.7).
     const int64_t resident = static_cast<int64_t>(W < 4 ? 2 : F32 ? 3 : 4) * device_sm_count();
-    const int64_t most = resident * std::max<int64_t>(1, a.rows * a.all_heads / head_slots(a.lanes) / 16 / resident);
+    const int64_t most = resident * std::max<int64_t>(1, a.rows * a.all_heads / head_slots(a.lanes) / (F32 ? 8 : 16) / resident);
     for (int i = 0; i < a.n; ++i)
         smem = std::max(smem, plan_group(a, a.g[i], head_share(most, a.g[i].heads, a.all_heads, a.all_groups), F32 ? 4 : 2, true, &ctas));
     if (a.n == 1) a.g[1].cta0 = INT32_MAX;

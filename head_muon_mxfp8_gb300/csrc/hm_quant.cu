@@ -18,6 +18,7 @@
 #include "hm_mx_device.cuh"
 #include "hm_ops.h"
 #include "hm_ptx.cuh"
+#include "hm_vec.cuh"
 
 namespace hm {
 
@@ -128,14 +129,14 @@ template <bool PACKED>
 __device__ __forceinline__ void sum_columns(const uint32_t* tile, float (*sum_col)[kQTile]) {
     if constexpr (PACKED) {
         const int cp = threadIdx.x & 63, b = threadIdx.x >> 6;
-        float s0 = 0.f, s1 = 0.f;
+        float2 sum = both2(0.f);
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
             const uint32_t w = tile[(b * 32 + k) * (kQTile / 2) + cp];
-            s0 += lo_f32(w), s1 += hi_f32(w);
+            sum = add2(sum, make_float2(lo_f32(w), hi_f32(w)));
         }
-        sum_col[b][2 * cp] = s0;
-        sum_col[b][2 * cp + 1] = s1;
+        sum_col[b][2 * cp] = sum.x;
+        sum_col[b][2 * cp + 1] = sum.y;
     } else {
         const int c = threadIdx.x & 127;
         const float* col = reinterpret_cast<const float*>(tile) + 4 * swizzled(c >> 2) + (c & 3);
@@ -302,11 +303,11 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
 #pragma unroll
             for (int k = 0; k < 32; ++k) w[k] = tile[(b * 32 + k) * (kQTile / 2) + cp];
             if constexpr (SUM) {
-                float s0 = 0.f, s1 = 0.f;
+                float2 sum = both2(0.f);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) s0 += lo_f32(w[k]), s1 += hi_f32(w[k]);
-                sum_col[b][c] = s0;
-                sum_col[b][c + 1] = s1;
+                for (int k = 0; k < 32; ++k) sum = add2(sum, make_float2(lo_f32(w[k]), hi_f32(w[k])));
+                sum_col[b][c] = sum.x;
+                sum_col[b][c + 1] = sum.y;
             }
 #pragma unroll
             for (int k = 0; k < 32; ++k) m = max_abs2(m, w[k]);
@@ -394,23 +395,24 @@ __global__ void __launch_bounds__(kQThreads, PACKED ? 4 : 2) quantize_kernel(con
     }
 }
 
-// dbias from the row tiles' sums: 32 columns per CTA, 32 threads per column each adding
-// every 32nd tile in order, then the 32 in order.
-__global__ void __launch_bounds__(1024) bias_sums_kernel(const float* sums, int tiles, int64_t cols, int accumulate, float* dbias) {
-    __shared__ float red[32][33];
+// dbias from the row tiles' sums: 32 columns per CTA, G threads per column each adding
+// every G-th tile in order, then the G in order.
+template <int G>
+__global__ void __launch_bounds__(32 * G) bias_sums_kernel(const float* sums, int tiles, int64_t cols, int accumulate, float* dbias) {
+    __shared__ float red[G][33];
     wait_for_earlier_kernels();
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + c;
     float s = 0.f;
     if (col < cols)
-#pragma unroll 4
-        for (int k = g; k < tiles; k += 32) s += sums[k * cols + col];
+#pragma unroll 8
+        for (int k = g; k < tiles; k += G) s += sums[k * cols + col];
     red[g][c] = s;
     __syncthreads();
     if (g == 0 && col < cols) {
         float t = 0.f;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) t += red[k][c];
+        for (int k = 0; k < G; ++k) t += red[k][c];
         dbias[col] = accumulate ? dbias[col] + t : t;
     }
 }
@@ -432,8 +434,11 @@ cudaError_t launch(const QuantArgs& a, cudaStream_t st) {
 
 cudaError_t launch_bias_sums(const float* sums, int64_t tiles, int64_t cols, int accumulate, float* dbias, cudaStream_t st) {
     note_launch();
-    return launch_early(bias_sums_kernel, static_cast<unsigned>((cols + 31) / 32), 1024, 0, st, sums, static_cast<int>(tiles),
-                        cols, accumulate, dbias);
+    const unsigned ctas = static_cast<unsigned>((cols + 31) / 32);
+    // eight loads per thread: 64 tiles of 20480 columns in eight threads per column rather than 32
+    const int n = static_cast<int>(tiles);
+    if (n <= 64) return launch_early(bias_sums_kernel<8>, ctas, 256, 0, st, sums, n, cols, accumulate, dbias);
+    return launch_early(bias_sums_kernel<32>, ctas, 1024, 0, st, sums, n, cols, accumulate, dbias);
 }
 
 cudaError_t launch_quantize(const QuantArgs& a, int f32, cudaStream_t st) {
