@@ -869,11 +869,11 @@ struct HeadWay {
 // first head; else nullptr): read from memory at every step, they held up a CTA of 8 heads, whose
 // steps are short (16384 rows of 32 + 8 heads bf16: gradient 114 us).
 constexpr int kHeadPositions = 1024;
-__device__ __forceinline__ const int64_t* head_positions(const HeadArgs& p, const HeadWay& way, int ranges, float* smem) {
+__device__ __forceinline__ const int64_t* head_positions(const HeadArgs& p, const HeadGroup& g, const HeadWay& way, float* smem) {
     const int64_t* from = p.positions + way.tok0;
-    if (!p.rot || way.rows > kHeadPositions) return nullptr;
+    if (!p.rot || !g.held) return nullptr;
     for (int i = threadIdx.x; i < way.rows; i += kHeadThreads)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem) + 8 * i), "l"(from + static_cast<int64_t>(i) * ranges) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem) + 8 * i), "l"(from + static_cast<int64_t>(i) * g.ranges) : "memory");
     return reinterpret_cast<const int64_t*>(smem);
 }
 
@@ -924,7 +924,7 @@ __device__ __forceinline__ void head_body(const HeadArgs& p) {
     float* gammas = smem + Ring::kBytes / 4;
     float* tables = gammas + (p.dim + 3) / 4 * 4;
     float* after = tables + (g.places * p.dim + 3) / 4 * 4;
-    const int64_t* positions = head_positions(p, way, g.ranges, after);
+    const int64_t* positions = head_positions(p, g, way, after);
     const float inv_dim = 1.f / static_cast<float>(p.dim);
     const bool norm = g.gamma != nullptr;
     if (norm && way.slot == 0) head_gamma(at, g.gamma, p.dim, gammas);
@@ -1020,7 +1020,7 @@ __device__ __forceinline__ void head_grad_body(const HeadArgs& p) {
     float* gammas = smem + 2 * Ring::kBytes / 4;
     float* tables = gammas + (p.dim + 3) / 4 * 4;
     float* after = tables + (g.places * p.dim + 3) / 4 * 4;
-    const int64_t* positions = head_positions(p, way, g.ranges, after);
+    const int64_t* positions = head_positions(p, g, way, after);
     const float inv_dim = 1.f / static_cast<float>(p.dim);
     if (norm && way.slot == 0) head_gamma(at, g.gamma, p.dim, gammas);
 #pragma unroll
@@ -1246,8 +1246,9 @@ int plan_group(HeadArgs& a, HeadGroup& g, int64_t ctas, int64_t es, bool split, 
     steps(g.out_row, g.out_head, &g.out_step, &g.out_wrap);
     g.cta0 = static_cast<int32_t>(*used);
     *used += static_cast<int64_t>(g.ranges) * g.split;
-    const int64_t rows = (a.rows + g.ranges - 1) / g.ranges;
-    return 4 * ((a.dim + 3) / 4 * 4 + (a.rot ? (g.places * a.dim + 3) / 4 * 4 : 0)) + (a.rot && rows <= kHeadPositions ? static_cast<int>(rows) * 8 : 0);
+    const int64_t rows = (a.rows + g.ranges - 1) / g.ranges;  // of a CTA, at most
+    g.held = rows <= kHeadPositions;
+    return 4 * ((a.dim + 3) / 4 * 4 + (a.rot ? (g.places * a.dim + 3) / 4 * 4 : 0)) + (a.rot && g.held ? static_cast<int>(rows) * 8 : 0);
 }
 
 template <bool F32, int W, bool PAIRS>

@@ -155,6 +155,7 @@ struct HeadGroup {
     int32_t rounds;      // of a step, which takes step_rows rows and step_heads heads more
     int32_t step_rows, step_heads;
     int32_t places;      // rows whose angles are held
+    int32_t held;        // every CTA's positions are, too
     int32_t slots, stride;       // heads in a CTA's round, and of all CTAs that share a range
     int32_t rows_on, heads_on;   // stride heads on from a (row, head),
     int64_t in_step, in_wrap, x_step, x_wrap, out_step, out_wrap;  // in bytes; wrap: where the head passes the row's last

@@ -555,3 +555,91 @@ def test_replay_and_two_streams(hm, dev):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs + outs2, want + want2))
     assert hm.hm_device_error() == 0
+
+
+@pytest.mark.parametrize("extra", [0, 1])
+def test_many_rows_per_cta(hm, dev, extra):
+    """Rows that leave some CTAs 1024 each, which fit beside the angles, and others one more, which
+    do not: forward and gradient, one narrow head of each kind, every row compared."""
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    g = torch.Generator(device=dev)
+    g.manual_seed(extra)
+    for ctas, back in ((4 * sms // 2, False), (2 * sms // 2, True)):
+        rows, dim = 1024 * ctas + extra, 32
+        x = torch.randn(rows, 2, dim, generator=g, device=dev).bfloat16()
+        dy = torch.randn(rows, 2, dim, generator=g, device=dev).bfloat16()
+        pos = torch.randint(0, 100000, (rows,), generator=g, device=dev)
+        f, turns = _turns(dev, dim)
+        gamma = torch.rand(dim, generator=g, device=dev) + 0.5
+        out = torch.full((rows + 1, 2, dim), 7.0, device=dev, dtype=torch.bfloat16)
+        dg = torch.zeros(2, dim, device=dev)
+        rot = hm.hm_rotation(turns.data_ptr(), pos.data_ptr(), 1.0, dim, hm.HM_ROPE_HALF)
+        at = lambda t, h: (t.data_ptr() + 2 * h * dim, 2 * dim, dim)  # noqa: E731
+        a = pos.double()[:, None, None] * torch.from_numpy(f).to(dev)
+        x64 = x.double().requires_grad_()
+        v = x64 * torch.rsqrt(x64.square().mean(-1, keepdim=True) + 1e-5) * gamma.double()
+        u, w = v[..., :dim // 2], v[..., dim // 2:]
+        y = torch.cat([u * a.cos() - w * a.sin(), w * a.cos() + u * a.sin()], -1)
+        if back:
+            lst = hm.head_grad_list([(*at(dy, h), *at(x, h), *at(out, h), gamma.data_ptr(), dg[h].data_ptr(), 1, False) for h in range(2)])
+            ws = torch.empty(hm.head_norm_rope_backward_workspace(lst, rows, dim), dtype=torch.uint8, device=dev)
+            hm.head_norm_rope_backward(lst, hm.HM_BF16, rows, dim, 1e-5, rot, ws.data_ptr(), ws.numel())
+            want, = torch.autograd.grad((y * dy.double()).sum(), x64)
+        else:
+            hm.head_norm_rope(hm.head_list([(*at(x, h), *at(out, h), gamma.data_ptr(), 1) for h in range(2)]), hm.HM_BF16, rows, dim, 1e-5, rot)
+            want = y.detach()
+        assert (out[rows] == 7).all()
+        # half a bf16 step and the bounds of heads and gradient with each term at its head's largest
+        r = torch.rsqrt(x.double().square().mean(-1, keepdim=True) + 1e-5)
+        most = (96 * r * 3 * (1 + dim ** 0.5) * dy.double().abs().amax(-1, keepdim=True) if back
+                else 48 * v.detach().abs().amax(-1, keepdim=True))
+        err = (out[:rows].double() - want).abs()
+        assert bool((err <= (1 + 2.0 ** -8) * U * most + 2.0 ** -8 * want.abs()).all())
+
+
+def test_more_than_two_groups(hm, dev):
+    """Four groups of one call: the bits of four calls; their gammas' gradients to their sums' order."""
+    rows, dim = 150, 64
+    g = torch.Generator(device=dev)
+    g.manual_seed(4)
+    heads = (5, 2, 1, 3)
+    rand = lambda *s: torch.randn(*s, generator=g, device=dev)  # noqa: E731
+    x, dy = [rand(rows, h, dim) for h in heads], [rand(rows, h, dim) for h in heads]
+    gamma = [rand(dim), None, rand(dim), rand(dim)]
+    pos = torch.randint(0, 9000, (rows,), generator=g, device=dev)
+    _, turns = _turns(dev, dim)
+    rot = hm.hm_rotation(turns.data_ptr(), pos.data_ptr(), 1.0, dim, hm.HM_ROPE_PAIRS)
+    p = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    at = lambda t: (t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
+
+    def run(parts):
+        y, dx = [torch.zeros_like(t) for t in x], [torch.zeros_like(t) for t in x]
+        dg = [torch.zeros(dim, device=dev) for _ in x]
+        for part in parts:
+            hm.head_norm_rope(hm.head_list([(*at(x[i]), *at(y[i]), p(gamma[i]), heads[i]) for i in part]), hm.HM_F32, rows, dim, 1e-6, rot)
+            lst = hm.head_grad_list([(*at(dy[i]), *at(x[i]), *at(dx[i]), p(gamma[i]), p(dg[i]) if gamma[i] is not None else 0, heads[i], False)
+                                     for i in part])
+            ws = torch.empty(max(16, hm.head_norm_rope_backward_workspace(lst, rows, dim)), dtype=torch.uint8, device=dev)
+            hm.head_norm_rope_backward(lst, hm.HM_F32, rows, dim, 1e-6, rot, ws.data_ptr(), ws.numel())
+        return y, dx, dg
+
+    y, dx, dg = run([range(4)])
+    y1, dx1, dg1 = run([[0], [1], [2], [3]])
+    assert all(torch.equal(a, b) for a, b in zip(y + dx, y1 + dx1))
+    assert all(float((a - b).abs().max()) <= 2 * (rows * 5 + 88) * U * float(t.abs().sum()) for a, b, t in zip(dg, dg1, dy))
+
+
+def test_a_wait_that_gives_up_in_an_epilogue_kernel(hm, dev, monkeypatch):
+    """The accumulator is never signalled (a switch of the launch): the bounded waits run out, the error is
+    reported once, and the next product is right."""
+    monkeypatch.setenv("HM_INJECT_MX_WAIT_TIMEOUT", "1")
+    for shape in ((9, 130, 96), (700, 3000, 256)):
+        p = _Product(hm, dev, "gated_gradient", "silu", *shape, "bf16")
+        monkeypatch.setenv("HM_INJECT_MX_WAIT_TIMEOUT", "1")
+        p.call()
+        torch.cuda.synchronize()
+        assert hm.hm_device_error() == hm.HM_ERR_TIMEOUT
+        monkeypatch.setenv("HM_INJECT_MX_WAIT_TIMEOUT", "0")
+        p.call()
+        p.check()
+        assert hm.hm_device_error() == 0

@@ -140,6 +140,44 @@ def test_layouts_that_pass_every_check(hm, kw):
     assert _heads(hm, **kw) in (hm.HM_ERR_ARCH, hm.HM_ERR_CUDA)
 
 
+def _elements(base, rows, row, heads, head, dim):
+    """Element numbers of a matrix [rows][heads][dim], as a set."""
+    return {base + r * row + h * head + e for r in range(rows) for h in range(heads) for e in range(dim)}
+
+
+def test_no_overlap_is_missed(hm):
+    """Small matrices at random places and strides: whenever an output shares an element with an input
+    or another output, the call is refused; whenever a head's elements repeat, too."""
+    if not _no_gpu():
+        pytest.skip("would launch on addresses that do not exist")
+    rng = np.random.default_rng(5)
+    refused = passed = 0
+    for _ in range(4000):
+        rows, dim = int(rng.integers(1, 5)), 2 * int(rng.integers(1, 3))
+        groups, sets = [], []
+        for _ in range(int(rng.integers(1, 3))):
+            heads = int(rng.integers(1, 4))
+            m = [(int(rng.integers(0, 90)), int(rng.choice([0, dim, dim + 1, heads * dim, 3 * dim, 24, 40])),
+                  int(rng.choice([0, dim, dim + 3, rows * dim, 12]))) for _ in range(2)]
+            if rng.random() < 0.3:
+                m[1] = m[0]  # in place
+            groups.append((A + 2 * m[0][0], m[0][1], m[0][2], A + 2 * m[1][0], m[1][1], m[1][2], 0, heads))
+            sets.append([_elements(b, rows, r, heads, h, dim) for b, r, h in m] + [rows * heads * dim, m[0] == m[1]])
+        bad = False
+        for i, (_, y, n, _) in enumerate(sets):
+            bad |= len(y) < n
+            for j, (x, z, _, in_place) in enumerate(sets):
+                bad |= bool(y & x) and not (i == j and in_place)
+                bad |= i != j and bool(y & z)
+        got = _status(hm.head_norm_rope, hm.head_list(groups), hm.HM_BF16, rows, dim, 1e-6, None, 0)
+        assert got != 0
+        if bad:
+            assert got in (hm.HM_ERR_OVERLAP, hm.HM_ERR_ARG), groups
+        refused += bad
+        passed += got not in (hm.HM_ERR_OVERLAP, hm.HM_ERR_ARG)
+    assert refused > 500 and passed > 300
+
+
 def test_number_of_groups(hm):
     g = hm.head_list([(A, 96, 16, B, 64, 16, 0, 0)] * 5)
     assert _status(hm.head_norm_rope, g, hm.HM_BF16, 3, 16, 1e-6, None, 0) == hm.HM_ERR_GEOMETRY
