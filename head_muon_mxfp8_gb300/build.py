@@ -22,8 +22,8 @@ LIB = os.path.join(PKG, "libhm.so")
 SOURCES = ["hm_host.cpp", "hm_elementwise.cu", "hm_ns.cu", "hm_noalloc.cu", "hm_mx32.cu", "hm_ops_host.cpp",
            "hm_mxgemm.cu", "hm_quant.cu", "hm_norm.cu", "hm_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-# kernels of one file compiled in parallel: hm_mxgemm.cu 73 -> 40 s on 8 cores
-COMMON = ["-O3", "-split-compile", "0", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
+# (No -split-compile: with it the MXFP8 product ran 20 % slower, 8192 x 20480 x 5120 in 567 us, not 474.)
+COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "-I" + INCLUDE, "-I" + CSRC]
 
 
