@@ -1021,8 +1021,13 @@ cudaError_t mx_gemm_form(const MxGemmArgs& args, MxGemmForm* f) {
     for (const int bn : {256, 192, 128}) {
         if (bn > 192 && (sums || wide_never)) continue;
         const int64_t tiles = static_cast<int64_t>((p.n + 255) / 256) * ((p.m + bn - 1) / bn);
-        // an epilogue (hm_epilogue) takes 1.1 us per 32 rows, and the last tile's overlaps nothing
-        const double sum = p.num_kb * (256 + bn) * (0.37 / 512), last = p.epilogue ? bn / 32 * 1.1 : 2.2;
+        // An epilogue (hm_epilogue) takes 1 us per 32 rows, and the last tile's overlaps nothing; a
+        // stage of 512 rows 0.30 us where no power cap holds it down.  With these every form of
+        // 300 x 5120 x 5120, 512 x 20480 x 5120, 777 x 2048 x 1408, 1024 x 4096 x 4096, 2048 x 2048 x
+        // 1024 and 4096 x 4096 x 1024 bf16 is the fastest one measured or within 3 % of it
+        // (1024 x 4096 x 4096 with GELU: 19.6 us on 256-row pairs, 21.5 in whole 128-row tiles).
+        const double stage = p.epilogue ? 0.30 / 512 : 0.37 / 512;
+        const double sum = p.num_kb * (256 + bn) * stage, last = p.epilogue ? bn / 32 * 1.0 : 2.2;
         const double c = static_cast<double>((tiles + pairs - 1) / pairs) * std::max(sum, last) + 4.0 + (p.epilogue ? std::min(sum, last) : 0.0);
         if (!best || c < least) best = bn, least = c;
     }

@@ -41,16 +41,17 @@ def _operand(g, dev, rows, k):
 FORMS = [
     # m, n, k, D, (tile, parts, sums)
     (2311, 1400, 6432, "bf16", (256, 0, 0)),
-    (1030, 6403, 2208, "bf16", (256, 0, 0)),
-    (2311, 6403, 2208, "bf16", (192, 0, 0)),   # several tiles per pair, tails in m, n and k
+    (1030, 6403, 3104, "bf16", (256, 0, 0)),   # several tiles per pair, here and below
+    (2311, 4099, 96, "bf16", (192, 0, 0)),
     (4000, 6400, 1056, "f32", (192, 0, 0)),
     (2311, 6403, 1056, "bf16", (128, 0, 0)),
     (2048, 9728, 1920, "f32", (128, 0, 0)),
-    (2311, 6403, 2208, "f32", (192, 0, 1)),    # two chunks
+    (1030, 4099, 3104, "f32", (192, 0, 1)),    # two chunks
+    (2311, 1400, 2080, "f32", (128, 0, 1)),
     (617, 9731, 2080, "f32", (128, 0, 1)),
     (5, 300, 24576, "f32", (128, 0, 1)),       # twelve chunks
     (1900, 2560, 160, "bf16", (128, 1, 0)),
-    (1000, 2299, 6432, "bf16", (128, 2, 0)),
+    (1541, 1400, 3104, "bf16", (128, 2, 0)),
     (65, 2600, 544, "f32", (128, 5, 0)),
     (600, 700, 96, "bf16", (64, 1, 0)),
     (515, 1030, 4128, "f32", (64, 3, 0)),
