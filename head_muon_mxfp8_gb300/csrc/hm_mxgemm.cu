@@ -20,6 +20,10 @@
 // 3.07 PFLOP/s at about 1.4 GHz); 6144 x 4096 x 4096 added to fp32, 92 us, by the
 // loads into the SMs and by D; a token's row by latency (1 x 5120 x 5120: 6.4 us,
 // 4.0 at the copy rate).
+// With an epilogue (hm_epilogue.cuh) 8192 x 20480 x 5120 to bf16 takes 530 to 574 us with bias,
+// GELU and the kept sum and 620 to 631 as its gradient, where the plain product took 474 to
+// 482 on those boxes: every instruction per element of D costs 3 us, and 335 MB more to
+// write or read, under the power cap.
 // Every wait is bounded as in the Newton-Schulz kernels (HM_ERR_TIMEOUT in the
 // device error word).
 #include "hm.h"
@@ -882,7 +886,7 @@ int resident_clusters(int split) {
 // what the CTAs get of B from HBM together; adding 128 rows of parts takes 4.5 us, one
 // row 0.7; a round starts and ends in 3.  With an epilogue 2 more, and 0.5 for each 16 rows of
 // an undivided tile, which four warps finish (divided ones are finished by six warps of
-// each CTA): 301 x 1408 x 2048 bf16 with GELU 13.2 us in whole tiles of 128, 9.7 in tiles of 64
+// each CTA): 301 x 1408 x 2048 bf16 with GELU 11.6 us in whole tiles of 128, 8.8 in tiles of 64
 // with K in four parts.
 template <int BN>
 int split_for(int tiles_p, int tiles_q, const MxGemmArgs& p, double* cost) {

@@ -10,6 +10,7 @@
 // so every tensor is read and written once.  8192 x 5120 bf16 with residual: norm
 // 46.1 us (6.4 TB/s, 0.94 of the measured copy rate), gradient 54.6 us (6.1 TB/s,
 // dgamma's second launch included); in fp32 81.7 and 100.3 us (6.7 TB/s both).
+// The norm and rotation of heads has its own notes below.
 // Far from it are the gradient's fp32 forms whose registers spill: 8192 rows of 6656
 // columns without a residual's gradient 183 us (3.6 TB/s), of 16384 558 us with it and
 // 439 without (3.8 and 3.7 TB/s).
@@ -491,6 +492,12 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* partials, int
 // and addresses.  Arithmetic goes two pairs at a time: one by one, with a division
 // per head and a 64-bit multiplication per address, the kernel issued 31 instructions
 // per element where memory leaves time for 21 (8192 x 80 heads of 128 bf16: 100 us).
+//
+// Memory-bound.  8192 x 80 heads of 128 bf16: 55.8 us (6.0 TB/s, 0.89 of the measured copy
+// rate; 32768 rows 0.98), gradient with both gammas' 83.5 us (0.89; 0.96); fp32 56.6 and
+// 79.6 us at 4096 rows.  Heads whose vectors are 8 bytes are bound by the instructions of their many
+// small pieces (72 elements: 49.6 and 76.6 us, floors 27.8 and 41.7); one token's 40 heads by
+// latency (2.7 us).
 // ---------------------------------------------------------------------------
 constexpr int kHeadThreads = 256;
 // A row's angles take a CTA as long as this many heads (16384 rows of 32 + 8 heads of 128 bf16,
@@ -602,9 +609,9 @@ struct HeadRaw {
 
 // A thread's parts of the heads it is going to work on, on their way into its own place
 // in shared memory (asynchronous copies; a thread waits for its own): D of them under
-// way and one that is read.  With one in registers instead, 32 KB under way on an SM,
-// 8192 x 80 heads of 128 bf16 took 61.5 us, and the gradient 109.  Vectors
-// of 2 bytes, which such copies do not take, go through registers.
+// way and one that is read.  With one in registers instead, 32 KB under way on an SM, the
+// gradient of 8192 x 80 heads of 128 bf16 took 109 us, not 84.  Vectors of 2 bytes, which such
+// copies do not take, go through registers.
 template <bool F32, int W, bool PAIRS, int D>
 struct HeadRing {
     static constexpr int kVec = W * (F32 ? 4 : 2), kPiece = kVec < 16 ? kVec : 16, V = 8 / W, kPieces = kVec / kPiece;
