@@ -557,15 +557,16 @@ def test_replay_and_two_streams(hm, dev):
     assert hm.hm_device_error() == 0
 
 
-@pytest.mark.parametrize("extra", [0, 1])
-def test_many_rows_per_cta(hm, dev, extra):
+@pytest.mark.parametrize("extra,dim", [(0, 32), (1, 32), (0, 16), (0, 512)])
+def test_many_rows_per_cta(hm, dev, extra, dim):
     """Rows that leave some CTAs 1024 each, which fit beside the angles, and others one more, which
-    do not: forward and gradient, one narrow head of each kind, every row compared."""
+    do not: forward and gradient, one head of each kind, every row compared.  Angles of one head's
+    rows, 1024 positions and the rings together are the most that a CTA asks for."""
     sms = torch.cuda.get_device_properties(dev).multi_processor_count
     g = torch.Generator(device=dev)
     g.manual_seed(extra)
     for ctas, back in ((4 * sms // 2, False), (2 * sms // 2, True)):
-        rows, dim = 1024 * ctas + extra, 32
+        rows = 1024 * ctas + extra
         x = torch.randn(rows, 2, dim, generator=g, device=dev).bfloat16()
         dy = torch.randn(rows, 2, dim, generator=g, device=dev).bfloat16()
         pos = torch.randint(0, 100000, (rows,), generator=g, device=dev)
