@@ -20,10 +20,9 @@
 // 3.07 PFLOP/s at about 1.4 GHz); 6144 x 4096 x 4096 added to fp32, 92 us, by the
 // loads into the SMs and by D; a token's row by latency (1 x 5120 x 5120: 6.4 us,
 // 4.0 at the copy rate).
-// With an epilogue (hm_epilogue.cuh) 8192 x 20480 x 5120 to bf16 takes 530 to 574 us with bias,
-// GELU and the kept sum and 620 to 631 as its gradient, where the plain product took 474 to
-// 482 on those boxes: every instruction per element of D costs 3 us, and 335 MB more to
-// write or read, under the power cap.
+// With an epilogue (hm_epilogue.cuh), calls of all kinds in turn under the power cap: 8192 x 20480
+// x 5120 to bf16 plain 534 us, without activation 566, with bias, GELU and the kept sum 594, as
+// its gradient 631, both of a gated pair's 654.
 // Every wait is bounded as in the Newton-Schulz kernels (HM_ERR_TIMEOUT in the
 // device error word).
 #include "hm.h"
