@@ -142,3 +142,52 @@ def test_mlp_matches_autograd(hm, dev, tokens, d, ff, act, gated, bias, block):
     assert torch.isfinite(y2.float()).all() and not torch.equal(y2, layer.h)
     layer.close()
     assert hm.hm_device_error() == 0
+
+
+def _passes(dev, which, tokens):
+    """A layer, its inputs and one training pass over them -> the results, copied."""
+    from head_muon_mxfp8_gb300.layers import NormMlp, NormQkv
+    g = torch.Generator(device=dev)
+    g.manual_seed(tokens)
+    rand = lambda *s: torch.randn(*s, generator=g, device=dev)  # noqa: E731
+    if which == "qkv":
+        layer = NormQkv(tokens, 160, 3, 1, 64, rot_dim=32)
+        layer.load_weight(rand(layer.d_out, 160) * 160 ** -0.5)
+        inputs = [rand(tokens, 160).bfloat16(), rand(tokens, 160).bfloat16(), torch.randint(0, 5000, (tokens,), generator=g, device=dev)]
+        inputs += [rand(tokens, n, 64).bfloat16() for n in (3, 1, 1)]
+    else:
+        layer = NormMlp(tokens, 160, 352, activation="silu", gated=True)
+        layer.load_weights(*[rand(*s) * 0.07 for s in ((352, 160), (352, 160), (160, 352))])
+        inputs = [rand(tokens, 160).bfloat16() for _ in range(3)]
+
+    def one():
+        layer.zero_grad()
+        if which == "qkv":
+            outs = [*layer.forward(*inputs[:3]), *layer.backward(*inputs[3:])]
+            return outs + [layer.g, layer.dq_gamma, layer.dk_gamma]
+        return [*layer.forward(*inputs[:2]), *layer.backward(inputs[2]), layer.session.g, *layer.dbiases]
+    return layer, inputs, one
+
+
+@pytest.mark.parametrize("which,tokens", [("qkv", 1), ("qkv", 77), ("mlp", 1), ("mlp", 77)])
+def test_captured_passes_repeat_eager_ones(hm, dev, which, tokens):
+    """A graph of a whole pass, the layer's first backward pass in it, replayed on new inputs:
+    bit for bit the eager pass on those inputs, before and after it."""
+    layer, inputs, one = _passes(dev, which, tokens)
+    other, theirs, eager = _passes(dev, which, tokens)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = one()
+    for _ in range(2):
+        for t, o in zip(inputs, theirs):
+            t.copy_(t.flip(0) if t.dtype == torch.int64 else t * -0.75)
+            o.copy_(t)
+        want = [t.clone() for t in eager()]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        assert all(torch.equal(a, b) for a, b in zip(one(), want))
+    layer.close()
+    other.close()
+    assert hm.hm_device_error() == 0
