@@ -464,7 +464,11 @@ hm_status mxfp8_gemm_form(int64_t m, int64_t n, int64_t k, hm_dtype d_dtype, int
  * in or in2 exactly (same address and pitch); any other overlap with an output is
  * HM_ERR_OVERLAP.  Activations: none, max(z, 0), z Phi(z) (GELU), its form with
  * tanh, 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))), and z / (1 + exp(-z))
- * (SiLU); the slope of max(z, 0) at 0 is 0.  f(-infinity) is NaN for the last three.
+ * (SiLU); the slope of max(z, 0) at 0 is 0.  f(-infinity) and the slopes at both
+ * infinities are NaN for the last three.  Relative to themselves, before the rounding:
+ * Phi(-|z|) is within (18 + 1.1 z^2) 2^-24, in HM_BF16 2^-13.5 more; the logistic
+ * factor 1 / (1 + exp(-w)) of the last two within (6 |w| + 8) 2^-24.  What is smaller than
+ * 2^-110 may lose bits or be 0.
  * k = 0: z = 0 before the bias.  Everything else as mxfp8_gemm, without accumulation;
  * the struct is read during the call. */
 #define HM_EPI_FORWARD        0
