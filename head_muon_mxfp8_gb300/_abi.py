@@ -502,9 +502,12 @@ def head_norm_rope_backward(groups, dtype: int, rows: int, head_dim: int, eps: f
 
 
 def rope_turns(rot_dim: int, theta: float = 10000.0, scaling: int = HM_ROPE_UNSCALED, factor: float = 1.0,
-               trained: float = 1.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
-    """(frequencies, scale) of head_norm_rope: the frequencies as the signed 64-bit patterns an int64 tensor takes."""
+               trained: "float | None" = None, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(frequencies, scale) of head_norm_rope: the frequencies as the signed 64-bit patterns an int64 tensor takes.
+    trained: the positions that the model was trained on, needed by HM_ROPE_YARN alone (ValueError)."""
+    if trained is None and scaling == HM_ROPE_YARN:
+        raise ValueError("rope_turns: YaRN needs `trained`, the positions that the model was trained on")
     out, scale = (C.c_uint64 * min(max(1, rot_dim // 2), HM_HEAD_MAX_DIM))(), C.c_float(0)
-    check("rope_turns", lib().rope_turns(rot_dim, theta, scaling, factor, trained, beta_fast, beta_slow, out,
-                                         C.byref(scale)))
+    check("rope_turns", lib().rope_turns(rot_dim, theta, scaling, factor, 1.0 if trained is None else trained, beta_fast,
+                                         beta_slow, out, C.byref(scale)))
     return [v - (1 << 64) if v >> 63 else v for v in out], scale.value

@@ -43,22 +43,35 @@ def _need_heads(name: str, t, shape: Tuple[int, int, int], device) -> None:
                          f"{t.dtype} {list(t.shape)} with strides {list(t.stride())} on {t.device}")
 
 
+def _rotation_table(rot_dim: int, theta: float, scaling: Optional[dict]):
+    """abi.rope_turns of NormQkv's arguments; ([], 1.0) where nothing is rotated."""
+    kw = dict(scaling or {"kind": "unscaled"})
+    kind = kw.pop("kind", None)
+    if kind not in SCALINGS:
+        raise ValueError(f"scaling: a kind of {sorted(SCALINGS)} is expected, not {kind!r}")
+    if kind != "unscaled" and "factor" not in kw:
+        raise ValueError(f"scaling: {kind!r} needs a factor")
+    if kind == "yarn" and kw.get("trained") is None:
+        raise ValueError("scaling: 'yarn' needs `trained`, the positions that the model was trained on")
+    return abi.rope_turns(rot_dim, theta, SCALINGS[kind], **kw) if rot_dim else ([], 1.0)
+
+
 class NormQkv(NormLinear):
     """RMS norm, packed QKV projection (all query heads, then key heads, then value heads; a
     head is an update unit), norm of each query and key head and its rotation by position.
     rot_dim: the rotated part of a head (all of it by default); pairs: adjacent elements
-    instead of halves; scaling: {"kind": "yarn", "factor": 16.0, ...} as abi.rope_turns."""
+    instead of halves; scaling: {"kind": "yarn", "factor": 16.0, "trained": 4096.0} and what else
+    abi.rope_turns takes (ValueError where its kind, factor or YaRN's trained length is missing)."""
 
     def __init__(self, tokens: int, d_in: int, q_heads: int, kv_heads: int, head_dim: int, rot_dim: Optional[int] = None,
                  pairs: bool = False, theta: float = 10000.0, scaling: Optional[dict] = None, head_norm: bool = True,
                  eps: float = 1e-5, block: int = 32, device="cuda"):
         self.q_heads, self.kv_heads, self.head_dim, self.head_norm = q_heads, kv_heads, head_dim, head_norm
-        super().__init__(tokens, d_in, (q_heads + 2 * kv_heads) * head_dim, eps, block, device)
         rot_dim = head_dim if rot_dim is None else rot_dim
-        kw = dict(scaling or {})
-        turns, scale = [], 1.0
-        if rot_dim:
-            turns, scale = abi.rope_turns(rot_dim, theta, SCALINGS[kw.pop("kind", "unscaled")], **kw)
+        if rot_dim > head_dim:
+            raise ValueError(f"rot_dim: at most head_dim ({head_dim}) is expected, not {rot_dim}")
+        turns, scale = _rotation_table(rot_dim, theta, scaling) if rot_dim or scaling else ([], 1.0)
+        super().__init__(tokens, d_in, (q_heads + 2 * kv_heads) * head_dim, eps, block, device)
         self._rot = (scale, rot_dim, abi.HM_ROPE_PAIRS if pairs else abi.HM_ROPE_HALF)
         dev, f32 = self.device, dict(dtype=torch.float32, device=self.device)
         self._turns = torch.tensor(turns, dtype=torch.int64, device=dev)
