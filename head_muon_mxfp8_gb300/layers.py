@@ -173,6 +173,7 @@ class NormMlp:
     and up, and act(gate) * up; else fc1 and act(fc1).  bias: of the first matrices and the
     last one."""
     _summed = False   # whether the small gradients hold a backward pass since they were cleared
+    _passed = False   # whether the buffers hold a whole forward pass
 
     def __init__(self, tokens: int, d: int, d_ff: int, activation: str = "gelu_tanh", gated: bool = False, bias: bool = True,
                  eps: float = 1e-5, block: int = 32, device="cuda"):
@@ -252,6 +253,7 @@ class NormMlp:
         for name, t in (("x", x), ("res", res)):
             if t is not None or name == "x":
                 _need(name, t, (self.tokens, self.d), torch.bfloat16, self.gamma.device)
+        self._passed = False
         st, d, ff = _stream(), self.d, self.d_ff
         abi.rmsnorm_mxfp8(_ptr(x), d, _ptr(res), _ptr(self.h), d, abi.HM_BF16, self.tokens, d, _ptr(self.gamma), self.eps,
                           self.block, _ptr(self.rstd), _ptr(self.x8.q), _ptr(self.x8.s), st)
@@ -267,13 +269,17 @@ class NormMlp:
                            _ptr(self.a8.s), _ptr(self.at8.q), self.at8.k, _ptr(self.at8.s), st)
         self._product(self.a8, last.q, last.s_tiled, d, ff, self.y, abi.HM_EPI_FORWARD, abi.HM_ACT_NONE, self.biases[-1],
                       first=self.h)
+        self._passed = True
         return self.y, self.h
 
     @_on_its_device
     def backward(self, dy: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
         """dy: bf16 [tokens][d], the gradient of y -> (dx, dgamma), dx of x and of res alike.  Adds
-        to the matrices' gradients and, after the first pass of a step, to the others."""
+        to the matrices' gradients and, after the first pass of a step, to the others.  Of the
+        forward pass before it (ValueError without one)."""
         _need("dy", dy, (self.tokens, self.d), torch.bfloat16, self.gamma.device)
+        if not self._passed:
+            raise ValueError("backward: there was no forward pass")
         st, d, ff, m = _stream(), self.d, self.d_ff, self.tokens
         last = self.weights[-1]
         self._quantize_gradient(dy, self.dy8, self.dyt8, self.dbiases[-1])
