@@ -966,6 +966,8 @@ cudaError_t launch_pair(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t
             if (p.epilogue == kEpiBf16) return launch_pair<BN, SUMS, kEpiBf16>(a, lda, b, ldb, p, st);
             if (p.epilogue == kEpiBf16Any) return launch_pair<BN, SUMS, kEpiBf16Any>(a, lda, b, ldb, p, st);
         }
+        // mx_gemm_form names no other tile; D without its epilogue would look like a result
+        if (p.epilogue) return cudaErrorInvalidValue;
     }
     constexpr int smem = C::SMEM + (EPI ? kPairEpiWarps * kPieceBytes : 0);
     static_assert(smem <= 232448, "the ring and the pieces");
