@@ -1223,7 +1223,7 @@ cudaError_t launch_bwd(const RmsGradArgs& a0, cudaStream_t st) {
     return launch_early(dgamma_kernel, a.d / 32, 1024, 0, st, a.partials, parts, a.d, a.accumulate, a.dgamma);
 }
 
-// A group's share of a call's CTAs: by heads and the angles of its rows.
+// A group's share of a launch's CTAs: by heads and the angles of its rows.
 int64_t head_share(int64_t ctas, int heads, int all_heads, int groups) {
     return std::max<int64_t>(1, ctas * (heads + kAngles) / (all_heads + kAngles * groups));
 }

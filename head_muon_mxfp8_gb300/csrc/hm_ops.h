@@ -170,7 +170,7 @@ struct HeadArgs {
     int32_t rot, pairs;  // rotated elements; adjacent pairs instead of halves
     int32_t width;       // elements per vector: 8, 4, 2 or 1
     int32_t lanes;       // of a head (set by the launchers)
-    int32_t all_heads, all_groups;  // of the whole call
+    int32_t all_heads, all_groups;  // of the launch
 };
 // Elements per vector for which every head can be read and written in whole vectors.
 int head_width(const HeadArgs& a, int64_t es);

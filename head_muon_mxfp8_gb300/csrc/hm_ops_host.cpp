@@ -475,19 +475,19 @@ struct HeadCall {
     hm::HeadGroup g[HM_HEAD_GROUPS];
     int n;
 };
-// Launches them by pairs.
+// Launches them by pairs, whose groups share the CTAs.
 template <class Launch>
 hm_status by_pairs(hm::HeadArgs& a, const HeadCall& call, const Launch& launch) {
     static_assert(hm::kHeadGroups == 2, "pairs");
-    a.all_heads = a.all_groups = 0;
-    for (int i = 0; i < call.n; ++i) {
-        a.all_heads += call.g[i].heads;
-        a.all_groups += call.g[i].heads > 0;
-    }
     for (int i = 0; i < call.n; i += 2) {
         a.n = std::min(2, call.n - i);
         std::memset(a.g, 0, sizeof(a.g));
-        for (int k = 0; k < a.n; ++k) a.g[k] = call.g[i + k];
+        a.all_heads = a.all_groups = 0;
+        for (int k = 0; k < a.n; ++k) {
+            a.g[k] = call.g[i + k];
+            a.all_heads += a.g[k].heads;
+            a.all_groups += a.g[k].heads > 0;
+        }
         const hm_status ok = cuda_status(launch(a));
         if (ok != HM_OK) return ok;
     }
@@ -579,12 +579,20 @@ extern "C" hm_status head_norm_rope(const hm_head_group* groups, int n_groups, h
 
 namespace {
 
-// Floats of dgamma's partial sums of group i.
+// Whether a gradient call has anything to do for a group.
+bool takes_part(const hm_head_grad& g, int64_t rows) { return (g.heads && rows) || g.dgamma; }
+
+// Floats of dgamma's partial sums of group i: a row per CTA, which its launch deals out to the
+// pair that it takes (by_pairs, of the groups that take part).
 size_t grad_partials(const hm_head_grad* groups, int n, int i, int64_t rows, int64_t head_dim) {
     const hm_head_grad& g = groups[i];
     if (!g.dgamma || !g.heads || !rows) return 0;
-    int heads = 0, live = 0;
+    int before = 0;
+    for (int k = 0; k < i; ++k) before += takes_part(groups[k], rows);
+    int heads = 0, live = 0, place = 0;
     for (int k = 0; k < n; ++k) {
+        if (!takes_part(groups[k], rows)) continue;
+        if (place++ / 2 != before / 2) continue;
         heads += groups[k].heads;
         live += groups[k].heads > 0;
     }
@@ -634,7 +642,7 @@ extern "C" hm_status head_norm_rope_backward(const hm_head_grad* groups, int n_g
         if (!aligned(g.gamma, 4) || !aligned(g.dgamma, 4)) return HM_ERR_ALIGN;
         if (!head_dim) continue;
         const bool live = g.heads && rows;
-        if (!live && !g.dgamma) continue;
+        if (!takes_part(g, rows)) continue;
         const int k = call.n++;
         from[k] = i;
         hm::HeadGroup& to = call.g[k];
