@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libhm.so")
 SOURCES = ["hm_host.cpp", "hm_elementwise.cu", "hm_ns.cu", "hm_noalloc.cu", "hm_mx32.cu", "hm_ops_host.cpp",
            "hm_mxgemm.cu", "hm_quant.cu", "hm_norm.cu", "hm_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-# (No -split-compile: with it the MXFP8 product ran 20 % slower, 8192 x 20480 x 5120 in 567 us, not 474.)
+# (No -split-compile: with it the MXFP8 product ran 20 % slower, 8192 x 20480 x 5120, the two builds in turn.)
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "-I" + INCLUDE, "-I" + CSRC]
 

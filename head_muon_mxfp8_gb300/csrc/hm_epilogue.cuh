@@ -8,8 +8,8 @@
 // instruction instead, the epilogue without any activation issued 30 instructions per
 // element and took 12 us of a 256 x 256 tile whose products take 3.3 (4096 x
 // 4096 x 1024 bf16: 48.6 us against 17.7 plain; with bias, GELU and the kept sum 81.5, now
-// 31.0).  Otherwise a lane keeps its column, whose neighbours' accesses coalesce at any
-// alignment (34.6 us there; both of a gated pair's gradients 53.7 against 45.3).
+// 32).  Otherwise a lane keeps its column, whose neighbours' accesses coalesce at any
+// alignment (36 us there; both of a gated pair's gradients 56 against 47).
 // What a piece reads is loaded one piece ahead, or, by a lane that keeps its column (twice
 // the registers), before the piece's accumulators are waited for.
 //

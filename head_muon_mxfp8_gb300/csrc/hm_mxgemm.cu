@@ -16,13 +16,14 @@
 //                    A's rows the N side (16 to 128 columns), and K is split
 //                    over the CTAs of a cluster (2 to 8) that add their parts through
 //                    distributed shared memory in rank order.
-// Bound by: large products by the power cap (8192 x 20480 x 5120 to bf16 560 us,
-// 3.07 PFLOP/s at about 1.4 GHz); 6144 x 4096 x 4096 added to fp32, 92 us, by the
+// Bound by: large products by the power cap, so their time goes with the clock that the
+// operands' bits leave (8192 x 20480 x 5120 to bf16, codes of random bits: 580 us, 2.96 PFLOP/s at
+// 1372 MHz median); 6144 x 4096 x 4096 added to fp32, 92 us, by the
 // loads into the SMs and by D; a token's row by latency (1 x 5120 x 5120: 6.4 us,
 // 4.0 at the copy rate).
-// With an epilogue (hm_epilogue.cuh), calls of all kinds in turn under the power cap: 8192 x 20480
-// x 5120 to bf16 plain 534 us, without activation 566, with bias, GELU and the kept sum 594, as
-// its gradient 631, both of a gated pair's 654.
+// With an epilogue (hm_epilogue.cuh), calls of all kinds in turn on those operands and at that
+// clock: plain 580 us, without activation 618, with bias, GELU and the kept sum 657, as its
+// gradient 681, both of a gated pair's 713.
 // Every wait is bounded as in the Newton-Schulz kernels (HM_ERR_TIMEOUT in the
 // device error word).
 #include "hm.h"

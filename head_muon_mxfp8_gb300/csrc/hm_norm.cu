@@ -478,10 +478,12 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* partials, int
 //
 // A pair's angle is positions[row] * freq[i].  In turns, as fixed point with 2^64
 // for a whole one, the product in 64-bit integers drops whole turns by wrapping, so
-// the fraction is exact to the frequency's own last bit times the position:
-// 2^-65 * 10^6 of a turn at the millionth token, where a product in fp32 would be
-// off by 0.06 radians.  The quarter turn is split off as an integer too; sin and cos
-// see at most an eighth of a turn.
+// the fraction is off by the table's own error times the position and by the 2^-32 of a
+// turn below the bits that are kept.  The table's error is 2^-65 of a turn by its fixed point and
+// up to about 2^-55 by rope_turns' doubles for the fastest pair (less as the pairs slow down):
+// 2^-35 of a turn at the millionth token, where a product in fp32 would be off by 0.06
+// radians.  The quarter turn is split off as an integer too; sin and cos see at most an
+// eighth of a turn.
 //
 // The pairs of a head lie in vectors of W elements: vector pair v is the W first and
 // the W second elements of pairs (halves), or two vectors of adjacent pairs; past
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* partials, int
 // Memory-bound.  8192 x 80 heads of 128 bf16: 55.8 us (6.0 TB/s, 0.89 of the measured copy
 // rate; 32768 rows 0.98), gradient with both gammas' 83.5 us (0.89; 0.96); fp32 56.6 and
 // 79.6 us at 4096 rows.  Heads whose vectors are 8 bytes are bound by the instructions of their many
-// small pieces (72 elements: 49.6 and 76.6 us, floors 27.8 and 41.7); one token's 40 heads by
+// small pieces (72 elements: 47.2 and 73.2 us, floors 27.8 and 41.7); one token's 40 heads by
 // latency (2.7 us).
 // ---------------------------------------------------------------------------
 constexpr int kHeadThreads = 256;
@@ -732,8 +734,9 @@ __device__ __forceinline__ void head_planes(const HeadPlace<W, PAIRS>& at, const
     }
 }
 
-// sin and cos of pi y, |y| <= 1/4: their Taylor series, off by less than 2^-30 there;
-// pi in two parts, so that the sine keeps its last bit.
+// sin and cos of pi y, |y| <= 1/4: their Taylor series to y^9 and y^10, off by less than
+// (pi / 4)^11 / 11! = 2^-29 and (pi / 4)^12 / 12! = 2^-33 there; pi in two parts, so that the sine keeps
+// its last bit.
 __device__ __forceinline__ void sincos_eighth(float y, float& s, float& c) {
     const float z = y * y;
     float u = fmaf(z, 0.08214588661f, -0.59926452932f);

@@ -582,8 +582,9 @@ hm_status rmsnorm_backward(const void* dy, int64_t lddy, const void* dres, const
  * 0 .. head_dim (HM_ERR_GEOMETRY).
  * turns: device, rot_dim / 2 frequencies in turns per position as fixed point,
  * freq[i] / (2 pi) * 2^64 (rope_turns makes them): the product with the position
- * wraps at whole turns by itself, so a position of any size or sign keeps a
- * turn's fraction to 32 bits.  positions: device, int64 [rows].  rotation NULL
+ * wraps at whole turns by itself, so a position of any size or sign keeps 32 bits
+ * of a turn's fraction, of the table's frequency: its own error grows with the
+ * position (rope_turns: up to about 2^-55 of a turn each).  positions: device, int64 [rows].  rotation NULL
  * or rot_dim 0: the norm alone.  rows = 0 or n_groups = 0 is a no-op. */
 #define HM_HEAD_MAX_DIM 512
 #define HM_HEAD_GROUPS 4
